@@ -20,6 +20,13 @@
  *   basa_text_attn_fwd        the text queries' output rows (dense over all keys)
  *   basa_window_attn_bwd      gradients w.r.t. q, k, v                 (BASA §3.4)
  *
+ * Around the attention (operators of the models that hold the layer; not on the pages):
+ *
+ *   basa_rope_table, basa_rope_fwd, basa_rope_bwd
+ *                             rotary positions along t, y, x, with the per-head RMS
+ *                             norm of queries and keys before them, from any strided
+ *                             (e.g. token-major packed) layout to the layouts below
+ *
  * Conventions common to every entry point
  * ---------------------------------------
  * Pointers. Every tensor pointer is a DEVICE pointer owned by the caller; the
@@ -326,6 +333,83 @@ basa_status basa_merge_branches(int n, const void *const *outs, const float *con
 basa_status basa_route_windows_noalloc(const void *q, const void *k, int32_t *route_idx,
                                        float *route_score, const basa_params *p,
                                        basa_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Rotary positions with several axes.
+ *
+ * A token's position is (t, y, x): grid token (i, j, l) is at (t0 + t_step i,
+ * y0 + y_step j, x0 + x_step l); text rows have positions of their own. Of the
+ * head_dim / 2 channel pairs of a head, the first dt / 2 turn with the t position,
+ * the next dh / 2 with y, the next dw / 2 with x, and the rest are left as they are.
+ * Pair i of an axis that owns m channels turns by the angle position * theta^(-2 i / m):
+ *   (y_a, y_b) = (x_a cos - x_b sin, x_a sin + x_b cos)
+ * with channels (a, b) = (2 g, 2 g + 1) for pair g of the head (ADJACENT), or
+ * (g, g + head_dim / 2) (HALVES).
+ */
+#define BASA_ROPE_PAIRS_ADJACENT 0
+#define BASA_ROPE_PAIRS_HALVES 1
+#define BASA_ROPE_MAX_TENSORS 8
+
+typedef struct {
+  int dt, dh, dw; /* channels of each axis: even, >= 0, sum <= head_dim */
+  int pairs;      /* BASA_ROPE_PAIRS_* */
+  double theta;   /* > 0 */
+  double t0, y0, x0;             /* position of grid token (0, 0, 0) */
+  double t_step, y_step, x_step; /* position step per token */
+} basa_rope_params;
+
+/* One tensor of a basa_rope_fwd / basa_rope_bwd call: [B, heads, rows, head_dim] with
+ * its own strides in elements (batch, head, row; channels contiguous), so that a slice
+ * of a token-major packed projection [B, rows, 3, heads, head_dim] is read where it is
+ * and written head-major. Row r is row first_row + r of the key sequence: a grid token
+ * in raster order below N = T*H*W, text row (first_row + r - N) from there on.
+ * Strides are >= 0 and multiples of 16 bytes; those of x and dy may be 0 (broadcast), y
+ * must not overlap itself. heads may differ between the tensors of a call. */
+typedef struct {
+  const void *x;       /* forward: input. backward: the forward's input (unused without weight) */
+  int64_t x_stride[3];
+  void *y;             /* forward: output, may be x itself (same strides). backward: dx, may be dy or x itself */
+  int64_t y_stride[3];
+  const void *dy;      /* backward only: gradient of the forward's output */
+  int64_t dy_stride[3];
+  const void *weight;  /* nullable: [head_dim], RMS norm before the rotation */
+  void *dweight;       /* backward only, nullable: [head_dim], overwritten */
+  int heads, rows, first_row;
+  int rotate;          /* 0: no rotation (values, which are only laid out), else 1 */
+} basa_rope_tensor;
+
+/*
+ * basa_rope_table — cos and sin of every position, for the calls below: the plan of a
+ * grid, computed once (float64 angles, rounded to float32). `table` is a device buffer
+ * of basa_rope_table_bytes(rp, p) bytes (0 for invalid parameters), 16-byte aligned.
+ * `text_pos` (device, float [n_text][3], (t, y, x)) may be NULL: text rows then are
+ * not turned. Uses T, H, W, n_text, head_dim of p.
+ */
+size_t basa_rope_table_bytes(const basa_rope_params *rp, const basa_params *p);
+basa_status basa_rope_table(const float *text_pos, float *table, const basa_rope_params *rp,
+                            const basa_params *p, basa_stream_t stream);
+
+/*
+ * basa_rope_fwd — norm and rotation of n (1 <= n <= BASA_ROPE_MAX_TENSORS) tensors in
+ * one launch. With a weight, each row is first
+ *   x * rsqrt(mean(x^2) + eps) * weight          (mean over head_dim, eps > 0)
+ * All arithmetic is float32 and the result is rounded once to the element type. `t` is
+ * a HOST array. `table` may be NULL when nothing is rotated. Uses B, the grid, n_text,
+ * head_dim and dtype of p (weights have the element type too).
+ */
+basa_status basa_rope_fwd(int n, const basa_rope_tensor *t, const float *table, float eps,
+                          const basa_rope_params *rp, const basa_params *p, basa_stream_t stream);
+
+/*
+ * basa_rope_bwd — gradients of basa_rope_fwd: dx (into y) and, where asked for, dweight
+ * (sums over batch, heads and rows in float32 in a fixed order, rounded once; no
+ * atomics: the same bits every run). The parameters are the forward's. `workspace`:
+ * basa_rope_bwd_workspace_bytes(n, t, p) bytes, 16-byte aligned, contents ignored
+ * (NULL when that is 0).
+ */
+size_t basa_rope_bwd_workspace_bytes(int n, const basa_rope_tensor *t, const basa_params *p);
+basa_status basa_rope_bwd(int n, const basa_rope_tensor *t, const float *table, float eps, void *workspace,
+                          const basa_rope_params *rp, const basa_params *p, basa_stream_t stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *basa_status_string(basa_status s);

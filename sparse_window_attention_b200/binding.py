@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbasa.so")
 
@@ -29,6 +30,8 @@ BASA_FLAG_TEST_SKIP_FIRST_KEY_LOAD = 0x1
 BASA_DEVERR_BAD_ROUTE = 0x8
 BASA_KEYS_WINDOWS, BASA_KEYS_POOLED, BASA_KEYS_TEXT, BASA_KEYS_ALL = 1, 2, 4, 7
 BASA_MAX_BRANCHES = 4
+BASA_ROPE_PAIRS_ADJACENT, BASA_ROPE_PAIRS_HALVES = 0, 1
+BASA_ROPE_MAX_TENSORS = 8
 EXPORTED = (
     "basa_pool_kv",
     "basa_route_workspace_bytes",
@@ -43,6 +46,11 @@ EXPORTED = (
     "basa_text_attn_fwd",
     "basa_window_attn_bwd_workspace_bytes",
     "basa_window_attn_bwd",
+    "basa_rope_table_bytes",
+    "basa_rope_table",
+    "basa_rope_fwd",
+    "basa_rope_bwd_workspace_bytes",
+    "basa_rope_bwd",
     "basa_status_string",
     "basa_device_error_status",
 )
@@ -68,6 +76,21 @@ class basa_params(ctypes.Structure):
         ("wait_timeout_us", ctypes.c_uint32),
         ("route_radius", ctypes.c_int),
     ]
+
+
+class basa_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("dt", ctypes.c_int), ("dh", ctypes.c_int), ("dw", ctypes.c_int),
+        ("pairs", ctypes.c_int),
+        ("theta", ctypes.c_double),
+        ("t0", ctypes.c_double), ("y0", ctypes.c_double), ("x0", ctypes.c_double),
+        ("t_step", ctypes.c_double), ("y_step", ctypes.c_double), ("x_step", ctypes.c_double),
+    ]
+
+
+# basa_rope_tensor: x, its strides, y, its strides, dy, its strides, weight, dweight,
+# heads, rows, first_row, rotate
+_ROPE_TENSOR = struct.Struct("=Q3qQ3qQ3qQQ4i")
 
 
 def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
@@ -102,6 +125,17 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.basa_window_attn_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.basa_window_attn_bwd.argtypes = [vp] * 13 + [P, vp]
     lib.basa_window_attn_bwd.restype = ctypes.c_int
+    R = ctypes.POINTER(basa_rope_params)
+    lib.basa_rope_table_bytes.argtypes = [R, P]
+    lib.basa_rope_table_bytes.restype = ctypes.c_size_t
+    lib.basa_rope_table.argtypes = [vp, vp, R, P, vp]
+    lib.basa_rope_table.restype = ctypes.c_int
+    lib.basa_rope_fwd.argtypes = [ctypes.c_int, ctypes.c_char_p, vp, ctypes.c_float, R, P, vp]
+    lib.basa_rope_fwd.restype = ctypes.c_int
+    lib.basa_rope_bwd_workspace_bytes.argtypes = [ctypes.c_int, ctypes.c_char_p, P]
+    lib.basa_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.basa_rope_bwd.argtypes = [ctypes.c_int, ctypes.c_char_p, vp, ctypes.c_float, vp, R, P, vp]
+    lib.basa_rope_bwd.restype = ctypes.c_int
     lib.basa_status_string.argtypes = [ctypes.c_int]
     lib.basa_status_string.restype = ctypes.c_char_p
     lib.basa_device_error_status.argtypes = [ctypes.c_int32]
@@ -249,4 +283,59 @@ def basa_window_attn_bwd(q, k, v, kp, vp, route_idx, out, lse, dout, dq, dk, dv,
                                                         workspace)], ctypes.byref(params), _stream(stream))
     if check:
         _check(st, "basa_window_attn_bwd")
+    return st
+
+
+def make_rope_params(axes, theta=10000.0, pairs=BASA_ROPE_PAIRS_ADJACENT, origin=(0.0, 0.0, 0.0),
+                     step=(1.0, 1.0, 1.0)) -> basa_rope_params:
+    return basa_rope_params(*axes, pairs, theta, *origin, *step)
+
+
+def rope_tensor(x, y, heads, rows, first_row=0, rotate=1, weight=None, dy=None, dweight=None,
+                strides=None) -> bytes:
+    """One basa_rope_tensor. x, y, dy are [B, heads, rows, head_dim] tensors, or device
+    addresses with their (batch, head, row) element strides in ``strides`` (a dict)."""
+
+    def view(name, t):
+        if t is None:
+            return 0, 0, 0, 0
+        s = strides[name] if isinstance(t, int) else t.stride()
+        return _ptr(t), s[0], s[1], s[2]
+
+    return _ROPE_TENSOR.pack(*view("x", x), *view("y", y), *view("dy", dy), _ptr(weight) or 0, _ptr(dweight) or 0,
+                             heads, rows, first_row, rotate)
+
+
+def basa_rope_table_bytes(rope_params: basa_rope_params, params: basa_params) -> int:
+    return _lib.basa_rope_table_bytes(ctypes.byref(rope_params), ctypes.byref(params))
+
+
+def basa_rope_table(text_pos, table, rope_params: basa_rope_params, params: basa_params, stream=None, check=True) -> int:
+    st = _lib.basa_rope_table(_ptr(text_pos), _ptr(table), ctypes.byref(rope_params), ctypes.byref(params),
+                              _stream(stream))
+    if check:
+        _check(st, "basa_rope_table")
+    return st
+
+
+def basa_rope_fwd(tensors, table, eps: float, rope_params: basa_rope_params, params: basa_params, stream=None,
+                  check=True) -> int:
+    """``tensors``: a list of rope_tensor() records."""
+    st = _lib.basa_rope_fwd(len(tensors), b"".join(tensors), _ptr(table), eps, ctypes.byref(rope_params),
+                            ctypes.byref(params), _stream(stream))
+    if check:
+        _check(st, "basa_rope_fwd")
+    return st
+
+
+def basa_rope_bwd_workspace_bytes(tensors, params: basa_params) -> int:
+    return _lib.basa_rope_bwd_workspace_bytes(len(tensors), b"".join(tensors), ctypes.byref(params))
+
+
+def basa_rope_bwd(tensors, table, eps: float, workspace, rope_params: basa_rope_params, params: basa_params, stream=None,
+                  check=True) -> int:
+    st = _lib.basa_rope_bwd(len(tensors), b"".join(tensors), _ptr(table), eps, _ptr(workspace),
+                            ctypes.byref(rope_params), ctypes.byref(params), _stream(stream))
+    if check:
+        _check(st, "basa_rope_bwd")
     return st

@@ -1,6 +1,7 @@
 // C ABI of libbasa: argument checks, then dispatch to the kernel launchers.
 // Every check runs on the host before any CUDA call, so an invalid call
 // returns its status and launches nothing.
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -52,6 +53,82 @@ basa_status check_common(const basa_params *p) {
 }
 
 bool has_pool(const basa_params *p) { return p->pt > 0; }
+
+basa_status check_rope_params(const basa_rope_params *rp, const basa_params *p) {
+  if (!rp) return BASA_ERR_INVALID_ARG;
+  for (int m : {rp->dt, rp->dh, rp->dw})
+    if (m < 0 || m % 2 || m > p->head_dim) return BASA_ERR_INVALID_ARG;
+  if (rp->dt + rp->dh + rp->dw > p->head_dim) return BASA_ERR_INVALID_ARG;
+  if (rp->pairs != BASA_ROPE_PAIRS_ADJACENT && rp->pairs != BASA_ROPE_PAIRS_HALVES) return BASA_ERR_INVALID_ARG;
+  if (!(rp->theta > 0.0)) return BASA_ERR_INVALID_ARG;
+  for (double v : {rp->theta, rp->t0, rp->y0, rp->x0, rp->t_step, rp->y_step, rp->x_step})
+    if (!std::isfinite(v)) return BASA_ERR_INVALID_ARG;
+  return BASA_OK;
+}
+
+bool rope_empty(const basa_rope_tensor &t, const basa_params *p) {
+  return p->B == 0 || t.heads == 0 || t.rows == 0;
+}
+
+// Strides of a [B, heads, rows, head_dim] view: >= 0 and whole 16-byte steps; a view
+// that is written must not meet itself (sorted by stride, each axis steps past the
+// extent of the ones before it).
+bool rope_strides_ok(const int64_t *stride, const basa_rope_tensor &t, const basa_params *p, bool written) {
+  const int64_t vec = p->dtype == BASA_BF16 ? 8 : 4, ext[3] = {p->B, t.heads, t.rows};
+  int64_t order[3][2];
+  int n = 0;
+  for (int a = 0; a < 3; ++a) {
+    if (ext[a] == 1) continue;  // never stepped
+    if (stride[a] < 0 || stride[a] % vec || stride[a] > (int64_t(1) << 56) / ext[a]) return false;
+    int at = n++;
+    for (; at > 0 && order[at - 1][0] > stride[a]; --at) std::memcpy(order[at], order[at - 1], sizeof(order[at]));
+    order[at][0] = stride[a];
+    order[at][1] = ext[a];
+  }
+  int64_t span = p->head_dim;
+  for (int i = 0; i < n && written; ++i) {
+    if (order[i][0] < span) return false;
+    span += order[i][0] * (order[i][1] - 1);
+  }
+  return true;
+}
+
+bool same_strides(const int64_t *a, const int64_t *b) { return a[0] == b[0] && a[1] == b[1] && a[2] == b[2]; }
+
+basa_status check_rope(int n, const basa_rope_tensor *t, const float *table, float eps, bool bwd,
+                       const basa_rope_params *rp, const basa_params *p) {
+  basa_status st = check_common(p);
+  if (st != BASA_OK) return st;
+  if ((st = check_rope_params(rp, p)) != BASA_OK) return st;
+  if (n < 1 || n > BASA_ROPE_MAX_TENSORS || !t) return BASA_ERR_INVALID_ARG;
+  const int64_t rows = int64_t(p->T) * p->H * p->W + p->n_text;
+  const bool turns = rp->dt + rp->dh + rp->dw > 0;
+  for (int i = 0; i < n; ++i) {
+    const basa_rope_tensor &u = t[i];
+    if (u.heads < 0 || u.rows < 0 || u.first_row < 0 || (u.rotate != 0 && u.rotate != 1)) return BASA_ERR_INVALID_ARG;
+    if (int64_t(u.first_row) + u.rows > rows) return BASA_ERR_SHAPE;
+    if (int64_t(p->B) * u.heads >= (int64_t(1) << 31)) return BASA_ERR_UNSUPPORTED;
+    if (u.weight && (!aligned16(u.weight) || !(eps > 0.f) || !std::isfinite(eps))) return BASA_ERR_INVALID_ARG;
+    if (bwd && u.dweight && (!u.weight || !aligned16(u.dweight))) return BASA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (bwd && u.dweight && u.dweight == t[j].dweight) return BASA_ERR_INVALID_ARG;
+    if (rope_empty(u, p)) continue;
+    const bool reads_x = !bwd || u.weight;
+    if (!u.y || !aligned16(u.y) || !rope_strides_ok(u.y_stride, u, p, true)) return BASA_ERR_INVALID_ARG;
+    if (reads_x && (!u.x || !aligned16(u.x) || !rope_strides_ok(u.x_stride, u, p, false))) return BASA_ERR_INVALID_ARG;
+    if (bwd && (!u.dy || !aligned16(u.dy) || !rope_strides_ok(u.dy_stride, u, p, false))) return BASA_ERR_INVALID_ARG;
+    if (u.rotate && turns && (!table || !aligned16(table))) return BASA_ERR_INVALID_ARG;
+    // in place is element by element; a tensor never writes what another one reads or writes
+    if (reads_x && u.x == u.y && !same_strides(u.x_stride, u.y_stride)) return BASA_ERR_INVALID_ARG;
+    if (bwd && u.dy == u.y && !same_strides(u.dy_stride, u.y_stride)) return BASA_ERR_INVALID_ARG;
+    for (int j = 0; j < n; ++j) {
+      if (j == i || rope_empty(t[j], p)) continue;
+      if (t[j].y == u.y || ((!bwd || t[j].weight) && t[j].x == u.y) || (bwd && t[j].dy == u.y))
+        return BASA_ERR_INVALID_ARG;
+    }
+  }
+  return BASA_OK;
+}
 
 }  // namespace
 
@@ -238,6 +315,41 @@ basa_status basa_window_attn_bwd(const void *q, const void *k, const void *v, co
   }
   if (basa::attn_bwd_workspace(*p) > 0 && (!workspace || !aligned16(workspace))) return BASA_ERR_INVALID_ARG;
   return basa::launch_attn_bwd_f32(q, k, v, kp, vp, route_idx, out, lse, dout, dq, dk, dv, workspace, *p, s);
+}
+
+size_t basa_rope_table_bytes(const basa_rope_params *rp, const basa_params *p) {
+  if (check_common(p) != BASA_OK || check_rope_params(rp, p) != BASA_OK) return 0;
+  return basa::rope_table_bytes(*rp, *p);
+}
+
+basa_status basa_rope_table(const float *text_pos, float *table, const basa_rope_params *rp, const basa_params *p,
+                            basa_stream_t stream) {
+  basa_status st = check_common(p);
+  if (st != BASA_OK) return st;
+  if ((st = check_rope_params(rp, p)) != BASA_OK) return st;
+  if (basa::rope_table_bytes(*rp, *p) == 0) return BASA_OK;
+  if (!table || !aligned16(table) || !aligned4(text_pos)) return BASA_ERR_INVALID_ARG;
+  return basa::launch_rope_table(text_pos, table, *rp, *p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+basa_status basa_rope_fwd(int n, const basa_rope_tensor *t, const float *table, float eps, const basa_rope_params *rp,
+                          const basa_params *p, basa_stream_t stream) {
+  basa_status st = check_rope(n, t, table, eps, false, rp, p);
+  if (st != BASA_OK) return st;
+  return basa::launch_rope(n, t, table, eps, nullptr, false, *rp, *p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t basa_rope_bwd_workspace_bytes(int n, const basa_rope_tensor *t, const basa_params *p) {
+  if (check_common(p) != BASA_OK || n < 1 || n > BASA_ROPE_MAX_TENSORS || !t) return 0;
+  return basa::rope_bwd_workspace(n, t, *p);
+}
+
+basa_status basa_rope_bwd(int n, const basa_rope_tensor *t, const float *table, float eps, void *workspace,
+                          const basa_rope_params *rp, const basa_params *p, basa_stream_t stream) {
+  basa_status st = check_rope(n, t, table, eps, true, rp, p);
+  if (st != BASA_OK) return st;
+  if (basa::rope_bwd_workspace(n, t, *p) > 0 && (!workspace || !aligned16(workspace))) return BASA_ERR_INVALID_ARG;
+  return basa::launch_rope(n, t, table, eps, workspace, true, *rp, *p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 basa_status basa_merge_branches(int n, const void *const *outs, const float *const *lses, void *out, float *lse,

@@ -164,5 +164,12 @@ basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, co
                                  void *dq, void *dk, void *dv, void *workspace, const basa_params &p, cudaStream_t s);
 basa_status launch_attn_text_f32(const void *q_text, const void *k, const void *v, void *out_text,
                                  const basa_params &p, cudaStream_t s);
+// Rotary positions (forward, or backward with `bwd`) of n tensors, and their tables.
+size_t rope_table_bytes(const basa_rope_params &rp, const basa_params &p);
+basa_status launch_rope_table(const float *text_pos, float *table, const basa_rope_params &rp, const basa_params &p,
+                              cudaStream_t s);
+size_t rope_bwd_workspace(int n, const basa_rope_tensor *t, const basa_params &p);
+basa_status launch_rope(int n, const basa_rope_tensor *t, const float *table, float eps, void *workspace, bool bwd,
+                        const basa_rope_params &rp, const basa_params &p, cudaStream_t s);
 
 }  // namespace basa

@@ -1,0 +1,474 @@
+// Rotary positions along the t, y and x axes of the token grid (HBM-bound), with the
+// per-head RMS norm of queries and keys before the rotation, and the gradients of both.
+//
+//   xn = x * rsqrt(mean(x^2) + eps) * weight        (a tensor without weight: xn = x)
+//   (y_a, y_b) = (xn_a cos - xn_b sin, xn_a sin + xn_b cos)  for each channel pair (a, b),
+// the angle of pair i of an axis that owns m channels being position * theta^(-2 i / m).
+//
+// What bounds it: one read and one write of the tensors. A row's cos and sin depend on
+// the token only, so a thread keeps those of its channels in registers and walks the
+// (batch, head) units of its row: the angle tables are read once per row and not once
+// per head. A thread owns two 16-byte chunks of a row, half a head apart, so both
+// pairings (adjacent channels, or channel i with i + d/2) find their partners in the
+// thread's own registers, and the norm's sum of squares is a few shuffles.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "basa_internal.h"
+
+namespace basa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+// Units a thread loads before it works on the first: 2 * 16 bytes each.
+constexpr int kUnroll = 4;
+
+struct RopeTensorArgs {
+  const void *x, *dy, *weight;
+  void *y;
+  float *part;  // backward: per-block partial weight gradients [blocks][d]
+  long long xs[3], ys[3], ds[3];  // element strides (batch, head, row)
+  int heads, rows, first_row, rotate;
+  int first_block, row_blocks, groups, group_units;  // blocks = row_blocks x groups of (batch, head) units
+};
+
+struct RopeArgs {
+  RopeTensorArgs t[BASA_ROPE_MAX_TENSORS];
+  int n;
+  const float2 *table;
+  int N, H, W, B;
+  int nt, nh, nw;                     // pairs of each axis
+  long long tab_y, tab_x, tab_text;   // offsets of the tables (the t axis starts at 0)
+  float eps;
+};
+
+template <typename T>
+struct Vec {
+  static constexpr int n = 16 / sizeof(T);
+};
+
+__device__ __forceinline__ void unpack(const uint4 &u, float *v, const __nv_bfloat16 *) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const uint4 &u, float *v, const float *) {
+  v[0] = __uint_as_float(u.x);
+  v[1] = __uint_as_float(u.y);
+  v[2] = __uint_as_float(u.z);
+  v[3] = __uint_as_float(u.w);
+}
+// The only rounding: float32 results to the element type, to nearest even.
+__device__ __forceinline__ uint4 pack(const float *v, const __nv_bfloat16 *) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ uint4 pack(const float *v, const float *) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+// Pair index of a thread's i-th pair (chunk column c): its channels are v[i] and
+// v[VEC + i] when the pairs are halves, v[2i] and v[2i + 1] when they are adjacent.
+template <int D, int VEC, bool HALVES>
+__device__ __forceinline__ int pair_index(int c, int i) {
+  if (HALVES) return VEC * c + i;
+  return i < VEC / 2 ? VEC / 2 * c + i : D / 4 + VEC / 2 * c + (i - VEC / 2);
+}
+
+template <int VEC, bool HALVES>
+__device__ __forceinline__ void rotate_pairs(float *v, const float *cs, const float *sn) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    float &a = v[HALVES ? i : 2 * i], &b = v[HALVES ? VEC + i : 2 * i + 1];
+    const float ra = a * cs[i] - b * sn[i], rb = a * sn[i] + b * cs[i];
+    a = ra;
+    b = rb;
+  }
+}
+
+// Sum over the LPR lanes that share a row (aligned groups of lanes).
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  return x;
+}
+
+// cos and sin of a thread's pairs in row `row` of the key sequence; the backward turns
+// the other way. Pairs behind the axes' channels are left as they are.
+template <int D, int VEC, bool HALVES, bool BWD>
+__device__ __forceinline__ void load_angles(const RopeArgs &a, int row, int c, float *cs, float *sn) {
+  const int P = a.nt + a.nh + a.nw;
+  const int t = row / (a.H * a.W), y = (row / a.W) % a.H, x = row % a.W;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const int p = pair_index<D, VEC, HALVES>(c, i);
+    long long at;
+    if (row >= a.N) at = a.tab_text + (long long)(row - a.N) * P + p;
+    else if (p < a.nt) at = (long long)t * a.nt + p;
+    else if (p < a.nt + a.nh) at = a.tab_y + (long long)y * a.nh + (p - a.nt);
+    else at = a.tab_x + (long long)x * a.nw + (p - a.nt - a.nh);
+    float2 e = make_float2(1.f, 0.f);
+    if (p < P) e = __ldg(a.table + at);
+    cs[i] = e.x;
+    sn[i] = BWD ? -e.y : e.y;
+  }
+}
+
+// One CTA = (tensor, block of 256 / LPR rows, group of (batch, head) units); a thread
+// owns chunk column c of one row and walks the group's units.
+//
+// The backward turns dy back (g = R^T dy) and, behind a norm with xh = x * r,
+// r = rsqrt(mean(x^2) + eps):  dweight = sum g * xh,
+// dx = r * (g w - xh * mean(g w * xh)). Each block sums its rows' weight gradients in a
+// fixed order; rope_dweight_kernel adds the blocks, so nothing depends on timing.
+template <typename T, int D, bool HALVES, bool BWD>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int VEC = Vec<T>::n, LPR = D / 2 / VEC, ROWS = kRopeThreads / LPR;
+  int ti = 0;
+  while (ti + 1 < a.n && int(blockIdx.x) >= a.t[ti + 1].first_block) ++ti;
+  const RopeTensorArgs &t = a.t[ti];
+  const int blk = int(blockIdx.x) - t.first_block;
+  const int group = blk / t.row_blocks;
+  const int c = threadIdx.x % LPR;
+  const int r = (blk % t.row_blocks) * ROWS + threadIdx.x / LPR;
+  const bool valid = r < t.rows;
+  const bool norm = t.weight != nullptr;
+  const int u0 = group * t.group_units, u1 = min(u0 + t.group_units, a.B * t.heads);
+  const T *kind = nullptr;
+
+  float cs[VEC], sn[VEC], w[2 * VEC], dw[2 * VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+  }
+  if (t.rotate && valid) load_angles<D, VEC, HALVES, BWD>(a, t.first_row + r, c, cs, sn);
+  if (norm) {
+    const uint4 *wp = reinterpret_cast<const uint4 *>(t.weight);
+    unpack(__ldg(wp + c), w, kind);
+    unpack(__ldg(wp + LPR + c), w + VEC, kind);
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * VEC; ++i) dw[i] = 0.f;
+
+  const T *x0 = static_cast<const T *>(t.x) + (long long)r * t.xs[2] + c * VEC;
+  T *y0 = static_cast<T *>(t.y) + (long long)r * t.ys[2] + c * VEC;
+  const T *d0 = static_cast<const T *>(t.dy) + (long long)r * t.ds[2] + c * VEC;
+  // Both loops below have the same trip count in every lane (shuffles).
+  for (int u = u0; u < u1; u += kUnroll) {
+    uint4 xa[kUnroll], xb[kUnroll], ga[kUnroll], gb[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      xa[k] = xb[k] = ga[k] = gb[k] = make_uint4(0, 0, 0, 0);
+      if (!valid || u + k >= u1) continue;
+      const int b = (u + k) / t.heads, h = (u + k) % t.heads;
+      if (!BWD || norm) {
+        const T *p = x0 + b * t.xs[0] + h * t.xs[1];
+        xa[k] = __ldcs(reinterpret_cast<const uint4 *>(p));
+        xb[k] = __ldcs(reinterpret_cast<const uint4 *>(p + D / 2));
+      }
+      if (BWD) {
+        const T *p = d0 + b * t.ds[0] + h * t.ds[1];
+        ga[k] = __ldcs(reinterpret_cast<const uint4 *>(p));
+        gb[k] = __ldcs(reinterpret_cast<const uint4 *>(p + D / 2));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      if (u + k >= u1) break;
+      float v[2 * VEC], g[2 * VEC];
+      if (!BWD || norm) {
+        unpack(xa[k], v, kind);
+        unpack(xb[k], v + VEC, kind);
+      }
+      float rms = 0.f;
+      if (norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * VEC; ++i) ss = fmaf(v[i], v[i], ss);
+        rms = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
+      }
+      if (!BWD) {
+        if (norm) {
+#pragma unroll
+          for (int i = 0; i < 2 * VEC; ++i) v[i] = v[i] * rms * w[i];
+        }
+        if (t.rotate) rotate_pairs<VEC, HALVES>(v, cs, sn);
+      } else {
+        unpack(ga[k], g, kind);
+        unpack(gb[k], g + VEC, kind);
+        if (t.rotate) rotate_pairs<VEC, HALVES>(g, cs, sn);
+        if (norm) {
+          float dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < 2 * VEC; ++i) {
+            v[i] *= rms;
+            dw[i] = fmaf(g[i], v[i], dw[i]);
+            g[i] *= w[i];
+            dot = fmaf(g[i], v[i], dot);
+          }
+          dot = row_sum<LPR>(dot) * (1.f / D);
+#pragma unroll
+          for (int i = 0; i < 2 * VEC; ++i) g[i] = rms * (g[i] - v[i] * dot);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * VEC; ++i) v[i] = g[i];
+      }
+      if (valid) {
+        const int b = (u + k) / t.heads, h = (u + k) % t.heads;
+        T *p = y0 + b * t.ys[0] + h * t.ys[1];
+        *reinterpret_cast<uint4 *>(p) = pack(v, kind);
+        *reinterpret_cast<uint4 *>(p + D / 2) = pack(v + VEC, kind);
+      }
+    }
+  }
+  if (BWD) {
+    if (t.part == nullptr) return;  // the same in the whole block
+    __shared__ float red[kRopeThreads / 32][D];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+    for (int i = 0; i < 2 * VEC; ++i) {
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xFFFFFFFFu, dw[i], o);
+      if (lane < LPR) red[warp][(i < VEC ? 0 : D / 2) + c * VEC + i % VEC] = dw[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < kRopeThreads / 32; ++k) s += red[k][threadIdx.x];
+      t.part[(long long)blk * D + threadIdx.x] = s;
+    }
+  }
+}
+
+// dweight[col] = sum over the blocks of their partial sums: one CTA per (tensor, 32
+// columns), 32 slices of the blocks, added in a fixed order.
+struct DweightArgs {
+  const float *part[BASA_ROPE_MAX_TENSORS];
+  void *dst[BASA_ROPE_MAX_TENSORS];
+  int blocks[BASA_ROPE_MAX_TENSORS];
+  int d;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(1024) rope_dweight_kernel(const __grid_constant__ DweightArgs a) {
+  __shared__ float red[32][33];
+  const int ti = blockIdx.y, col = blockIdx.x * 32 + threadIdx.x % 32, slice = threadIdx.x / 32;
+  const float *p = a.part[ti] + col;
+  float s = 0.f;
+#pragma unroll 8
+  for (int b = slice; b < a.blocks[ti]; b += 32) s += p[(long long)b * a.d];
+  red[slice][threadIdx.x % 32] = s;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) sum += red[k][threadIdx.x];
+    static_cast<T *>(a.dst[ti])[col] = T(sum);
+  }
+}
+
+// cos and sin tables: [T][nt], [H][nh], [W][nw], [n_text][nt + nh + nw]. The angle is a
+// float64 product reduced in float64, so far positions keep their fraction of a turn;
+// a few thousand entries, computed once for a grid.
+struct TableArgs {
+  float2 *table;
+  const float *text_pos;  // nullable: text rows are not turned
+  double log_theta, origin[3], step[3];
+  int ext[3], pairs[3], n_text;
+};
+
+__global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableArgs a) {
+  long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, left = i;
+  double pos = 0.0;
+  int axis = 0, p = 0;
+  bool found = false;
+  for (int k = 0; k < 3 && !found; ++k) {
+    const long long n = (long long)a.ext[k] * a.pairs[k];
+    if (left < n) {
+      axis = k;
+      p = int(left % a.pairs[k]);
+      pos = a.origin[k] + a.step[k] * double(left / a.pairs[k]);
+      found = true;
+    } else {
+      left -= n;
+    }
+  }
+  if (!found) {
+    const int P = a.pairs[0] + a.pairs[1] + a.pairs[2];
+    if (left >= (long long)a.n_text * P) return;
+    const long long row = left / P;
+    p = int(left % P);
+    while (p >= a.pairs[axis]) p -= a.pairs[axis++];
+    if (a.text_pos) pos = double(a.text_pos[3 * row + axis]);
+  }
+  double s, c;
+  sincos(pos * exp(-a.log_theta * double(p) / double(a.pairs[axis])), &s, &c);
+  a.table[i] = make_float2(float(c), float(s));
+}
+
+template <typename T, int D, bool HALVES>
+void run_rope(const RopeArgs &a, bool bwd, unsigned blocks, cudaStream_t s) {
+  if (bwd) rope_kernel<T, D, HALVES, true><<<blocks, kRopeThreads, 0, s>>>(a);
+  else rope_kernel<T, D, HALVES, false><<<blocks, kRopeThreads, 0, s>>>(a);
+}
+
+template <typename T, int D>
+void run_rope(const RopeArgs &a, bool bwd, bool halves, unsigned blocks, cudaStream_t s) {
+  if (halves) run_rope<T, D, true>(a, bwd, blocks, s);
+  else run_rope<T, D, false>(a, bwd, blocks, s);
+}
+
+// Blocks of a tensor list: rows in blocks of 256 threads, and the (batch, head) units
+// in as many groups as it takes to give the GPU about kTargetBlocks blocks (8 resident
+// blocks on each of 148 SMs). Depends on the shapes only, so the order of the weight
+// gradients' sums does too. Returns the block count (< 0: too many).
+constexpr long long kTargetBlocks = 8 * 148;
+bool has_rows(const basa_rope_tensor &t, const basa_params &p) { return p.B > 0 && t.heads > 0 && t.rows > 0; }
+long long plan_blocks(int n, const basa_rope_tensor *t, const basa_params &p, RopeArgs *a) {
+  const int rows_per_block = kRopeThreads / (p.head_dim / 2 / (p.dtype == BASA_BF16 ? 8 : 4));
+  long long row_blocks = 0;
+  for (int i = 0; i < n; ++i)
+    if (has_rows(t[i], p)) row_blocks += (t[i].rows + rows_per_block - 1) / rows_per_block;
+  long long blocks = 0;
+  a->n = 0;
+  for (int i = 0; i < n; ++i) {
+    if (!has_rows(t[i], p)) continue;
+    RopeTensorArgs &r = a->t[a->n++];
+    const long long units = (long long)p.B * t[i].heads;
+    const long long want = std::min(units, std::max(1ll, kTargetBlocks / row_blocks));
+    r.row_blocks = (t[i].rows + rows_per_block - 1) / rows_per_block;
+    r.group_units = int((units + want - 1) / want);
+    r.groups = int((units + r.group_units - 1) / r.group_units);
+    r.first_block = int(std::min(blocks, (1ll << 31) - 1));
+    blocks += (long long)r.row_blocks * r.groups;
+  }
+  return blocks < (1ll << 31) ? blocks : -1;
+}
+
+}  // namespace
+
+size_t rope_table_bytes(const basa_rope_params &rp, const basa_params &p) {
+  const size_t entries = size_t(p.T) * (rp.dt / 2) + size_t(p.H) * (rp.dh / 2) + size_t(p.W) * (rp.dw / 2) +
+                         size_t(p.n_text) * ((rp.dt + rp.dh + rp.dw) / 2);
+  return entries * sizeof(float2);
+}
+
+basa_status launch_rope_table(const float *text_pos, float *table, const basa_rope_params &rp, const basa_params &p,
+                              cudaStream_t s) {
+  TableArgs a{};
+  a.table = reinterpret_cast<float2 *>(table);
+  a.text_pos = text_pos;
+  a.log_theta = log(rp.theta);
+  const double origin[3] = {rp.t0, rp.y0, rp.x0}, step[3] = {rp.t_step, rp.y_step, rp.x_step};
+  const int ext[3] = {p.T, p.H, p.W}, pairs[3] = {rp.dt / 2, rp.dh / 2, rp.dw / 2};
+  for (int k = 0; k < 3; ++k) {
+    a.origin[k] = origin[k];
+    a.step[k] = step[k];
+    a.ext[k] = ext[k];
+    a.pairs[k] = pairs[k];
+  }
+  a.n_text = p.n_text;
+  const size_t entries = rope_table_bytes(rp, p) / sizeof(float2);
+  if (entries == 0) return BASA_OK;
+  const size_t blocks = (entries + 255) / 256;
+  if (blocks >= (size_t(1) << 31)) return BASA_ERR_UNSUPPORTED;
+  rope_table_kernel<<<unsigned(blocks), 256, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
+}
+
+size_t rope_bwd_workspace(int n, const basa_rope_tensor *t, const basa_params &p) {
+  RopeArgs a{};
+  if (plan_blocks(n, t, p, &a) < 0) return 0;
+  size_t rows = 0;
+  for (int i = 0, j = 0; i < n; ++i) {
+    if (!has_rows(t[i], p)) continue;
+    if (t[i].dweight) rows += size_t(a.t[j].row_blocks) * a.t[j].groups;
+    ++j;
+  }
+  return rows * p.head_dim * sizeof(float);
+}
+
+basa_status launch_rope(int n, const basa_rope_tensor *t, const float *table, float eps, void *workspace, bool bwd,
+                        const basa_rope_params &rp, const basa_params &p, cudaStream_t s) {
+  RopeArgs a{};
+  const long long blocks = plan_blocks(n, t, p, &a);
+  if (blocks < 0) return BASA_ERR_UNSUPPORTED;
+  a.table = reinterpret_cast<const float2 *>(table);
+  a.N = p.T * p.H * p.W;
+  a.H = p.H;
+  a.W = p.W;
+  a.B = p.B;
+  a.nt = rp.dt / 2;
+  a.nh = rp.dh / 2;
+  a.nw = rp.dw / 2;
+  a.tab_y = (long long)p.T * a.nt;
+  a.tab_x = a.tab_y + (long long)p.H * a.nh;
+  a.tab_text = a.tab_x + (long long)p.W * a.nw;
+  a.eps = eps;
+  DweightArgs d{};
+  d.d = p.head_dim;
+  int n_dw = 0;
+  float *part = static_cast<float *>(workspace);
+  for (int i = 0, j = 0; i < n; ++i) {
+    const basa_rope_tensor &u = t[i];
+    int part_blocks = 0;
+    if (has_rows(u, p)) {
+      RopeTensorArgs &r = a.t[j++];
+      r.x = u.x;
+      r.y = u.y;
+      r.dy = u.dy;
+      r.weight = u.weight;
+      const int ext[3] = {p.B, u.heads, u.rows};
+      for (int k = 0; k < 3; ++k) {  // an axis with one entry is never stepped
+        r.xs[k] = ext[k] > 1 ? u.x_stride[k] : 0;
+        r.ys[k] = ext[k] > 1 ? u.y_stride[k] : 0;
+        r.ds[k] = ext[k] > 1 ? u.dy_stride[k] : 0;
+      }
+      r.heads = u.heads;
+      r.rows = u.rows;
+      r.first_row = u.first_row;
+      r.rotate = u.rotate && a.nt + a.nh + a.nw > 0;
+      if (bwd && u.dweight) {
+        part_blocks = r.row_blocks * r.groups;
+        r.part = part;
+      }
+    }
+    if (bwd && u.dweight) {  // a part without rows gets a gradient of zero
+      d.part[n_dw] = part;
+      d.dst[n_dw] = u.dweight;
+      d.blocks[n_dw++] = part_blocks;
+      part += size_t(part_blocks) * p.head_dim;
+    }
+  }
+  if (blocks > 0) {
+    const bool halves = rp.pairs == BASA_ROPE_PAIRS_HALVES;
+    const unsigned b = unsigned(blocks);
+    if (p.dtype == BASA_BF16) {
+      if (p.head_dim == 128) run_rope<__nv_bfloat16, 128>(a, bwd, halves, b, s);
+      else run_rope<__nv_bfloat16, 64>(a, bwd, halves, b, s);
+    } else {
+      if (p.head_dim == 128) run_rope<float, 128>(a, bwd, halves, b, s);
+      else run_rope<float, 64>(a, bwd, halves, b, s);
+    }
+    if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
+  }
+  if (n_dw > 0) {
+    const dim3 grid(unsigned(p.head_dim / 32), unsigned(n_dw));
+    if (p.dtype == BASA_BF16) rope_dweight_kernel<__nv_bfloat16><<<grid, 1024, 0, s>>>(d);
+    else rope_dweight_kernel<float><<<grid, 1024, 0, s>>>(d);
+    if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
+  }
+  return BASA_OK;
+}
+
+}  // namespace basa

@@ -231,3 +231,92 @@ def test_backward_chunking_fills_whole_waves():
         chunks, units = _bwd_chunks(wl, synth.SHIFT_CYCLES[name][-1])
         assert chunks == want, (name, chunks)
         assert units * chunks <= 148, (name, units * chunks)  # one wave
+
+
+def _rope(dt=16, dh=56, dw=56, pairs=0, theta=10000.0, **kw):
+    return B.make_rope_params((dt, dh, dw), theta, pairs, **kw)
+
+
+def _rope_tensor(x=FAKE, y=FAKE + (1 << 20), heads=2, rows=4, first_row=0, rotate=1, weight=None, dy=None, dweight=None):
+    strides = {name: (2 * 4 * 128, 4 * 128, 128) for name in ("x", "y", "dy")}
+    return B.rope_tensor(x, y, heads, rows, first_row, rotate, weight, dy, dweight, strides=strides)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dt=15), 1), (dict(dw=58), 1), (dict(dt=-2), 1), (dict(pairs=2), 1), (dict(theta=0.0), 1),
+    (dict(theta=float("inf")), 1), (dict(origin=(0.0, float("nan"), 0.0)), 1),
+])
+def test_rope_params_rejected(kw, status):
+    p = _p()
+    assert B.basa_rope_fwd([_rope_tensor()], FAKE, 1e-6, _rope(**kw), p, stream=0, check=False) == status
+    assert B.basa_rope_table(None, FAKE, _rope(**kw), p, stream=0, check=False) == status
+    assert B.basa_rope_table_bytes(_rope(**kw), p) == 0
+
+
+def test_rope_table_bytes():
+    # pairs 8, 28, 28 of 1, 64, 64 positions and 64 pairs of 16 text rows, 8 bytes each
+    assert B.basa_rope_table_bytes(_rope(), _p()) == 8 * (8 + 28 * 64 + 28 * 64 + 64 * 16)
+    assert B.basa_rope_table(None, FAKE + 8, _rope(), _p(), stream=0, check=False) == 1
+    assert B.basa_rope_table(FAKE + 2, FAKE, _rope(), _p(), stream=0, check=False) == 1
+
+
+def test_rope_checks():
+    p = _p()  # 64 x 64 grid, 16 text rows
+
+    def fwd(*t, table=FAKE, eps=1e-6, pp=p):
+        return B.basa_rope_fwd(list(t), table, eps, _rope(), pp, stream=0, check=False)
+
+    T = _rope_tensor
+    assert fwd() == 1 and fwd(*[T(rows=0)] * 9) == 1  # 1..8 tensors
+    assert fwd(T(first_row=-1)) == 1 and fwd(T(heads=-1)) == 1 and fwd(T(rows=-1)) == 1 and fwd(T(rotate=2)) == 1
+    assert fwd(T(first_row=4096 + 13)) == 2  # rows past the sequence
+    assert fwd(T(), pp=_p(head_dim=96)) == 3
+    assert fwd(T(x=0)) == 1 and fwd(T(y=0)) == 1 and fwd(T(x=FAKE + 8)) == 1 and fwd(T(y=FAKE + 8)) == 1
+    assert fwd(T(weight=FAKE + 8)) == 1
+    assert fwd(T(weight=FAKE), eps=0.0) == 1 and fwd(T(weight=FAKE), eps=float("nan")) == 1
+    assert fwd(T(), table=None) == 1 and fwd(T(), table=FAKE + 8) == 1
+    # in place needs the same strides; no tensor writes what another one uses
+    assert fwd(T(y=FAKE, x=FAKE), T(x=FAKE, y=FAKE + (2 << 20))) == 1
+    assert fwd(T(), T(x=FAKE + (3 << 20))) == 1  # the same output twice
+
+
+def test_rope_strides_checked():
+    p = _p()
+
+    def fwd(xs, ys, x=FAKE, y=FAKE + (1 << 20), pp=p):
+        t = B.rope_tensor(x, y, 2, 4, strides={"x": xs, "y": ys})
+        return B.basa_rope_fwd([t], FAKE, 1e-6, _rope(), pp, stream=0, check=False)
+
+    good = (1024, 512, 128)
+    assert fwd((1024, 512, 132), good) == 1  # not a multiple of 16 bytes
+    assert fwd((1024, -512, 128), good) == 1
+    assert fwd((1024, 512, 1 << 60), good) == 1
+    assert fwd(good, (1024, 512, 120)) == 1 and fwd(good, (1024, 384, 128)) == 1 and fwd(good, (1024, 0, 128)) == 1
+    assert fwd(good, (1024, 128, 256), x=FAKE, y=FAKE) == 1  # in place with other strides
+
+
+def test_rope_backward_checks():
+    p = _p()
+
+    def bwd(*t, ws=FAKE):
+        return B.basa_rope_bwd(list(t), FAKE, 1e-6, ws, _rope(), p, stream=0, check=False)
+
+    def T(**kw):
+        return _rope_tensor(dy=kw.pop("dy", FAKE + (4 << 20)), **kw)
+
+    dw = FAKE + (8 << 20)
+    assert bwd(T(dy=None)) == 1
+    assert bwd(T(dweight=dw)) == 1  # a gradient without its weight
+    assert bwd(T(weight=FAKE, dweight=dw), ws=None) == 1 and bwd(T(weight=FAKE, dweight=dw), ws=FAKE + 8) == 1
+    assert bwd(T(weight=FAKE, dweight=dw + 8)) == 1
+    assert bwd(T(weight=FAKE, dweight=dw), T(y=FAKE + (2 << 20), weight=FAKE, dweight=dw)) == 1  # the same gradient twice
+    assert bwd(T(x=0, weight=FAKE)) == 1
+    # one block of 32 rows in groups of one unit each: 2 partial rows of 128 floats
+    assert B.basa_rope_bwd_workspace_bytes([T(weight=FAKE, dweight=dw)], p) == 2 * 128 * 4
+    assert B.basa_rope_bwd_workspace_bytes([T(weight=FAKE)], p) == 0
+    assert B.basa_rope_bwd_workspace_bytes([T(weight=FAKE, dweight=dw, rows=0)], p) == 0
+
+
+def test_rope_empty_is_a_no_op():
+    for t, kw in ((_rope_tensor(x=0, y=0, rows=0), {}), (_rope_tensor(x=0, y=0, heads=0), {}), (_rope_tensor(x=0, y=0), dict(B=0))):
+        assert B.basa_rope_fwd([t], None, 1e-6, _rope(), _p(**kw), stream=0, check=False) == 0
