@@ -26,6 +26,10 @@
  *                             rotary positions along t, y, x, with the per-head RMS
  *                             norm of queries and keys before them, from any strided
  *                             (e.g. token-major packed) layout to the layouts below
+ *   basa_diff_attn_fwd, basa_diff_attn_bwd, basa_diff_text_attn_fwd, basa_diff_pool_kv
+ *                             differential attention over the layer's key lists: the
+ *                             difference of two softmax maps with a learned weight per
+ *                             head, and an RMS norm of each head's rows
  *
  * Conventions common to every entry point
  * ---------------------------------------
@@ -410,6 +414,81 @@ basa_status basa_rope_fwd(int n, const basa_rope_tensor *t, const float *table, 
 size_t basa_rope_bwd_workspace_bytes(int n, const basa_rope_tensor *t, const basa_params *p);
 basa_status basa_rope_bwd(int n, const basa_rope_tensor *t, const float *table, float eps, void *workspace,
                           const basa_rope_params *rp, const basa_params *p, basa_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Differential attention over the key lists of basa_window_attn_fwd.
+ *
+ * Head h has two softmax maps, 2h and 2h + 1, that share its values (and its routes):
+ *   O1 = softmax(q[2h] K[2h]^T / sqrt(d)) V[h],   O2 = softmax(q[2h+1] K[2h+1]^T / sqrt(d)) V[h]
+ *   a = O1 - lambda[h] O2
+ *   out = gain * weight * a * rsqrt(mean(a^2) + eps)      (mean over head_dim)
+ *   out = a                                               without a weight
+ * In these calls p->heads counts the differential heads:
+ *   q, dq        [B, 2 heads, N, head_dim]
+ *   k, dk        [B, 2 heads, N + n_text, head_dim],  kp [B, 2 heads, Np, head_dim]
+ *   v, dv        [B, heads, N + n_text, head_dim],    vp [B, heads, Np, head_dim]
+ *   route_idx    [B, heads, nWin, routed_k]
+ *   out, dout    [B, heads, N, head_dim]
+ * Scores, softmax statistics, the difference and the norm are float32, the result is
+ * rounded once. bfloat16 requires head_dim == 128; float32 supports 64 and 128. Pointer
+ * rules, route ids and dev_err are those of basa_window_attn_fwd.
+ */
+typedef struct {
+  const void *lambda; /* device, [heads], element type p->dtype (16-bit: 2-byte aligned) */
+  const void *weight; /* device, nullable: [head_dim], element type, 16-byte aligned */
+  float gain, eps;    /* with a weight: finite gain, eps > 0 */
+} basa_diff_params;
+
+/*
+ * basa_diff_pool_kv — pooled keys and values, as basa_pool_kv: kp of the 2 heads maps,
+ * vp of the heads.
+ */
+basa_status basa_diff_pool_kv(const void *k, const void *v, void *kp, void *vp, const basa_params *p,
+                              basa_stream_t stream);
+
+/*
+ * basa_diff_attn_fwd — forward. For a backward, `second` and `lse` receive O2
+ * [B, heads, N, head_dim] and the maps' log-sum-exp (float32 [B, 2 heads, N]); `pre`
+ * receives a (nullable: without a weight `out` is a). All three may be NULL otherwise.
+ * `workspace`: basa_diff_attn_workspace_bytes(p) bytes (0 with bfloat16: pass NULL;
+ * float32: the two maps' outputs), 16-byte aligned, contents ignored.
+ */
+size_t basa_diff_attn_workspace_bytes(const basa_params *p);
+basa_status basa_diff_attn_fwd(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                               const int32_t *route_idx, const basa_diff_params *dp, void *out, void *pre,
+                               void *second, float *lse, void *workspace, const basa_params *p,
+                               basa_stream_t stream);
+
+/*
+ * basa_diff_attn_bwd — gradients with respect to q, k, v, lambda and weight. `pre` is a
+ * (the forward's `pre`, or `out` without a weight), `second` and `lse` the forward's.
+ * As in basa_window_attn_bwd pooled keys and values pass their gradients on to their
+ * patch's tokens and routing passes none. dlambda [heads] and dweight [head_dim] (NULL
+ * iff there is no weight) have the element type; they are summed in float32 in a fixed
+ * order. All outputs are overwritten. With bfloat16 nothing is accumulated atomically:
+ * the same bits every run; P, dS and the gradient behind the norm are rounded to bfloat16
+ * before the tensor-core products. With float32 dk and dv are accumulated with atomic
+ * adds. `workspace`: basa_diff_attn_bwd_workspace_bytes(dp, p) bytes, 256-byte aligned,
+ * contents ignored. Limits as basa_window_attn_bwd; B >= 1 (of an empty batch only a
+ * call without heads and weight, which has nothing to write, is accepted).
+ */
+size_t basa_diff_attn_bwd_workspace_bytes(const basa_diff_params *dp, const basa_params *p);
+basa_status basa_diff_attn_bwd(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                               const int32_t *route_idx, const basa_diff_params *dp, const void *pre,
+                               const void *second, const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                               void *dlambda, void *dweight, void *workspace, const basa_params *p,
+                               basa_stream_t stream);
+
+/*
+ * basa_diff_text_attn_fwd — the text queries' rows: each map attends densely to every
+ * row of k, v (as basa_text_attn_fwd), then difference and norm as above. q_text
+ * [B, 2 heads, n_text, head_dim], out_text [B, heads, n_text, head_dim], n_text >= 1.
+ * `workspace`: basa_diff_text_attn_workspace_bytes(p) bytes of float32 map outputs,
+ * 16-byte aligned, contents ignored.
+ */
+size_t basa_diff_text_attn_workspace_bytes(const basa_params *p);
+basa_status basa_diff_text_attn_fwd(const void *q_text, const void *k, const void *v, const basa_diff_params *dp,
+                                    void *out_text, void *workspace, const basa_params *p, basa_stream_t stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *basa_status_string(basa_status s);

@@ -51,6 +51,13 @@ EXPORTED = (
     "basa_rope_fwd",
     "basa_rope_bwd_workspace_bytes",
     "basa_rope_bwd",
+    "basa_diff_pool_kv",
+    "basa_diff_attn_workspace_bytes",
+    "basa_diff_attn_fwd",
+    "basa_diff_attn_bwd_workspace_bytes",
+    "basa_diff_attn_bwd",
+    "basa_diff_text_attn_workspace_bytes",
+    "basa_diff_text_attn_fwd",
     "basa_status_string",
     "basa_device_error_status",
 )
@@ -85,6 +92,14 @@ class basa_rope_params(ctypes.Structure):
         ("theta", ctypes.c_double),
         ("t0", ctypes.c_double), ("y0", ctypes.c_double), ("x0", ctypes.c_double),
         ("t_step", ctypes.c_double), ("y_step", ctypes.c_double), ("x_step", ctypes.c_double),
+    ]
+
+
+class basa_diff_params(ctypes.Structure):
+    _fields_ = [
+        ("lam", ctypes.c_void_p),  # `lambda` in the header
+        ("weight", ctypes.c_void_p),
+        ("gain", ctypes.c_float), ("eps", ctypes.c_float),
     ]
 
 
@@ -136,6 +151,21 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.basa_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.basa_rope_bwd.argtypes = [ctypes.c_int, ctypes.c_char_p, vp, ctypes.c_float, vp, R, P, vp]
     lib.basa_rope_bwd.restype = ctypes.c_int
+    D = ctypes.POINTER(basa_diff_params)
+    lib.basa_diff_pool_kv.argtypes = [vp, vp, vp, vp, P, vp]
+    lib.basa_diff_pool_kv.restype = ctypes.c_int
+    lib.basa_diff_attn_workspace_bytes.argtypes = [P]
+    lib.basa_diff_attn_workspace_bytes.restype = ctypes.c_size_t
+    lib.basa_diff_attn_fwd.argtypes = [vp] * 6 + [D] + [vp] * 5 + [P, vp]
+    lib.basa_diff_attn_fwd.restype = ctypes.c_int
+    lib.basa_diff_attn_bwd_workspace_bytes.argtypes = [D, P]
+    lib.basa_diff_attn_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.basa_diff_attn_bwd.argtypes = [vp] * 6 + [D] + [vp] * 10 + [P, vp]
+    lib.basa_diff_attn_bwd.restype = ctypes.c_int
+    lib.basa_diff_text_attn_workspace_bytes.argtypes = [P]
+    lib.basa_diff_text_attn_workspace_bytes.restype = ctypes.c_size_t
+    lib.basa_diff_text_attn_fwd.argtypes = [vp, vp, vp, D, vp, vp, P, vp]
+    lib.basa_diff_text_attn_fwd.restype = ctypes.c_int
     lib.basa_status_string.argtypes = [ctypes.c_int]
     lib.basa_status_string.restype = ctypes.c_char_p
     lib.basa_device_error_status.argtypes = [ctypes.c_int32]
@@ -338,4 +368,56 @@ def basa_rope_bwd(tensors, table, eps: float, workspace, rope_params: basa_rope_
                             ctypes.byref(rope_params), ctypes.byref(params), _stream(stream))
     if check:
         _check(st, "basa_rope_bwd")
+    return st
+
+
+def make_diff_params(lam, weight=None, gain=1.0, eps=1e-6) -> basa_diff_params:
+    return basa_diff_params(_ptr(lam), _ptr(weight), gain, eps)
+
+
+def basa_diff_pool_kv(k, v, kp, vp, params: basa_params, stream=None, check=True) -> int:
+    st = _lib.basa_diff_pool_kv(_ptr(k), _ptr(v), _ptr(kp), _ptr(vp), ctypes.byref(params), _stream(stream))
+    if check:
+        _check(st, "basa_diff_pool_kv")
+    return st
+
+
+def basa_diff_attn_workspace_bytes(params: basa_params) -> int:
+    return _lib.basa_diff_attn_workspace_bytes(ctypes.byref(params))
+
+
+def basa_diff_attn_fwd(q, k, v, kp, vp, route_idx, diff_params: basa_diff_params, out, pre, second, lse, workspace,
+                       params: basa_params, stream=None, check=True) -> int:
+    st = _lib.basa_diff_attn_fwd(*[_ptr(x) for x in (q, k, v, kp, vp, route_idx)], ctypes.byref(diff_params),
+                                 *[_ptr(x) for x in (out, pre, second, lse, workspace)], ctypes.byref(params),
+                                 _stream(stream))
+    if check:
+        _check(st, "basa_diff_attn_fwd")
+    return st
+
+
+def basa_diff_attn_bwd_workspace_bytes(diff_params: basa_diff_params, params: basa_params) -> int:
+    return _lib.basa_diff_attn_bwd_workspace_bytes(ctypes.byref(diff_params), ctypes.byref(params))
+
+
+def basa_diff_attn_bwd(q, k, v, kp, vp, route_idx, diff_params: basa_diff_params, pre, second, lse, dout, dq, dk, dv,
+                       dlam, dweight, workspace, params: basa_params, stream=None, check=True) -> int:
+    st = _lib.basa_diff_attn_bwd(*[_ptr(x) for x in (q, k, v, kp, vp, route_idx)], ctypes.byref(diff_params),
+                                 *[_ptr(x) for x in (pre, second, lse, dout, dq, dk, dv, dlam, dweight, workspace)],
+                                 ctypes.byref(params), _stream(stream))
+    if check:
+        _check(st, "basa_diff_attn_bwd")
+    return st
+
+
+def basa_diff_text_attn_workspace_bytes(params: basa_params) -> int:
+    return _lib.basa_diff_text_attn_workspace_bytes(ctypes.byref(params))
+
+
+def basa_diff_text_attn_fwd(q_text, k, v, diff_params: basa_diff_params, out_text, workspace, params: basa_params,
+                            stream=None, check=True) -> int:
+    st = _lib.basa_diff_text_attn_fwd(_ptr(q_text), _ptr(k), _ptr(v), ctypes.byref(diff_params), _ptr(out_text),
+                                      _ptr(workspace), ctypes.byref(params), _stream(stream))
+    if check:
+        _check(st, "basa_diff_text_attn_fwd")
     return st

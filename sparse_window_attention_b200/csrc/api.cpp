@@ -54,6 +54,38 @@ basa_status check_common(const basa_params *p) {
 
 bool has_pool(const basa_params *p) { return p->pt > 0; }
 
+bool aligned_element(const void *x, const basa_params *p) {
+  return (reinterpret_cast<uintptr_t>(x) & (p->dtype == BASA_BF16 ? 1u : 3u)) == 0;
+}
+
+// Differential attention: shape (2 heads maps), then the parameters, then the inputs.
+basa_status check_diff_shape(const basa_params *p) {
+  basa_status st = check_common(p);
+  if (st != BASA_OK) return st;
+  if (p->dtype == BASA_BF16 && p->head_dim != 128) return BASA_ERR_UNSUPPORTED;
+  if (2 * int64_t(p->B) * p->heads >= (int64_t(1) << 31)) return BASA_ERR_UNSUPPORTED;
+  return BASA_OK;
+}
+
+basa_status check_diff(const basa_diff_params *dp, const basa_params *p) {
+  basa_status st = check_diff_shape(p);
+  if (st != BASA_OK) return st;
+  if (!dp || !aligned_element(dp->lambda, p) || !aligned16(dp->weight)) return BASA_ERR_INVALID_ARG;
+  if (dp->weight && (!std::isfinite(dp->gain) || !(dp->eps > 0.f) || !std::isfinite(dp->eps))) return BASA_ERR_INVALID_ARG;
+  return BASA_OK;
+}
+
+basa_status check_diff_inputs(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                              const int32_t *route_idx, const basa_diff_params *dp, const basa_params *p) {
+  for (const void *x : {q, k, v, dp->lambda})
+    if (!x) return BASA_ERR_INVALID_ARG;
+  for (const void *x : {q, k, v, kp, vp})
+    if (!aligned16(x)) return BASA_ERR_INVALID_ARG;
+  if (has_pool(p) != (kp != nullptr) || has_pool(p) != (vp != nullptr)) return BASA_ERR_INVALID_ARG;
+  if ((p->routed_k > 0) != (route_idx != nullptr) || !aligned4(route_idx)) return BASA_ERR_INVALID_ARG;
+  return BASA_OK;
+}
+
 basa_status check_rope_params(const basa_rope_params *rp, const basa_params *p) {
   if (!rp) return BASA_ERR_INVALID_ARG;
   for (int m : {rp->dt, rp->dh, rp->dw})
@@ -350,6 +382,94 @@ basa_status basa_rope_bwd(int n, const basa_rope_tensor *t, const float *table, 
   if (st != BASA_OK) return st;
   if (basa::rope_bwd_workspace(n, t, *p) > 0 && (!workspace || !aligned16(workspace))) return BASA_ERR_INVALID_ARG;
   return basa::launch_rope(n, t, table, eps, workspace, true, *rp, *p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+basa_status basa_diff_pool_kv(const void *k, const void *v, void *kp, void *vp, const basa_params *p,
+                              basa_stream_t stream) {
+  basa_status st = check_diff_shape(p);
+  if (st != BASA_OK) return st;
+  if (!has_pool(p)) return BASA_ERR_INVALID_ARG;
+  if (empty_batch(p)) return BASA_OK;
+  for (const void *x : {k, v, static_cast<const void *>(kp), static_cast<const void *>(vp)})
+    if (!x || !aligned16(x)) return BASA_ERR_INVALID_ARG;
+  const int units = p->B * p->heads;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = basa::launch_pool_rows(k, kp, 2 * units, *p, s)) != BASA_OK) return st;
+  return basa::launch_pool_rows(v, vp, units, *p, s);
+}
+
+size_t basa_diff_attn_workspace_bytes(const basa_params *p) {
+  if (check_diff_shape(p) != BASA_OK || p->dtype == BASA_BF16) return 0;
+  return basa::diff_f32_workspace(*p, int64_t(p->T) * p->H * p->W);
+}
+
+basa_status basa_diff_attn_fwd(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                               const int32_t *route_idx, const basa_diff_params *dp, void *out, void *pre, void *second,
+                               float *lse, void *workspace, const basa_params *p, basa_stream_t stream) {
+  basa_status st = check_diff(dp, p);
+  if (st != BASA_OK) return st;
+  if (empty_batch(p)) return BASA_OK;
+  if ((st = check_diff_inputs(q, k, v, kp, vp, route_idx, dp, p)) != BASA_OK) return st;
+  if (!out || !aligned16(out) || !aligned16(pre) || !aligned16(second) || !aligned4(lse)) return BASA_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p->dtype == BASA_BF16)
+    return basa::launch_diff_attn_bf16(q, k, v, kp, vp, route_idx, *dp, out, pre, second, lse, *p, s);
+  if (!workspace || !aligned16(workspace)) return BASA_ERR_INVALID_ARG;
+  return basa::launch_diff_attn_f32(q, k, v, kp, vp, route_idx, *dp, out, pre, second, lse, workspace, *p, s);
+}
+
+size_t basa_diff_attn_bwd_workspace_bytes(const basa_diff_params *dp, const basa_params *p) {
+  if (check_diff(dp, p) != BASA_OK || empty_batch(p)) return 0;
+  return p->dtype == BASA_BF16 ? basa::diff_attn_bwd_bf16_workspace(dp->weight != nullptr, *p)
+                               : basa::diff_attn_bwd_f32_workspace(dp->weight != nullptr, *p);
+}
+
+basa_status basa_diff_attn_bwd(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                               const int32_t *route_idx, const basa_diff_params *dp, const void *pre, const void *second,
+                               const float *lse, const void *dout, void *dq, void *dk, void *dv, void *dlambda,
+                               void *dweight, void *workspace, const basa_params *p, basa_stream_t stream) {
+  basa_status st = check_diff(dp, p);
+  if (st != BASA_OK) return st;
+  if (p->dtype == BASA_BF16 && p->routed_k > 0 && int64_t(p->T / p->wt) * (p->H / p->wh) * (p->W / p->ww) > 4096)
+    return BASA_ERR_UNSUPPORTED;
+  if (empty_batch(p)) return p->heads > 0 || dp->weight ? BASA_ERR_INVALID_ARG : BASA_OK;
+  if ((st = check_diff_inputs(q, k, v, kp, vp, route_idx, dp, p)) != BASA_OK) return st;
+  for (const void *x : {pre, second, static_cast<const void *>(lse), dout, static_cast<const void *>(dq),
+                        static_cast<const void *>(dk), static_cast<const void *>(dv)})
+    if (!x) return BASA_ERR_INVALID_ARG;
+  for (const void *x : {pre, second, dout, static_cast<const void *>(dq), static_cast<const void *>(dk),
+                        static_cast<const void *>(dv), static_cast<const void *>(dweight)})
+    if (!aligned16(x)) return BASA_ERR_INVALID_ARG;
+  if (!dlambda || !aligned_element(dlambda, p) || !aligned4(lse)) return BASA_ERR_INVALID_ARG;
+  if ((dweight != nullptr) != (dp->weight != nullptr)) return BASA_ERR_INVALID_ARG;
+  const size_t need = basa_diff_attn_bwd_workspace_bytes(dp, p);
+  if (need == 0) return BASA_ERR_UNSUPPORTED;  // the tiling plan does not fit the kernel's limits
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return BASA_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const auto launch = p->dtype == BASA_BF16 ? basa::launch_diff_attn_bwd_bf16 : basa::launch_diff_attn_bwd_f32;
+  return launch(q, k, v, kp, vp, route_idx, *dp, pre, second, lse, dout, dq, dk, dv, dlambda, dweight, workspace, *p, s);
+}
+
+size_t basa_diff_text_attn_workspace_bytes(const basa_params *p) {
+  if (check_diff_shape(p) != BASA_OK || p->n_text < 1 || empty_batch(p)) return 0;
+  return p->dtype == BASA_BF16 ? basa::diff_text_workspace(*p, basa::device_sm_count())
+                               : basa::diff_f32_workspace(*p, p->n_text);
+}
+
+basa_status basa_diff_text_attn_fwd(const void *q_text, const void *k, const void *v, const basa_diff_params *dp,
+                                    void *out_text, void *workspace, const basa_params *p, basa_stream_t stream) {
+  basa_status st = check_diff(dp, p);
+  if (st != BASA_OK) return st;
+  if (p->n_text < 1) return BASA_ERR_INVALID_ARG;
+  if (empty_batch(p)) return BASA_OK;
+  for (const void *x : {q_text, k, v, static_cast<const void *>(out_text), static_cast<const void *>(workspace)})
+    if (!x || !aligned16(x)) return BASA_ERR_INVALID_ARG;
+  if (!dp->lambda) return BASA_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p->dtype == BASA_F32) return basa::launch_diff_text_f32(q_text, k, v, *dp, out_text, workspace, *p, s);
+  const int sms = basa::device_sm_count();
+  if (sms <= 0) return BASA_ERR_CUDA;
+  return basa::launch_diff_text_bf16(q_text, k, v, *dp, out_text, workspace, *p, sms, s);
 }
 
 basa_status basa_merge_branches(int n, const void *const *outs, const float *const *lses, void *out, float *lse,

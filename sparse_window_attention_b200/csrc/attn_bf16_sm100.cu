@@ -26,6 +26,17 @@
 // epilogue writes each query row's log-sum-exp; and the text-query rows, where the
 // queries are 128-row boxes of the text rows and the key stream is every k/v row,
 // split over CTA groups whose partial results are merged by log-sum-exp.
+//
+// Differential form (FORM kDiff): out = softmax(q1 K1^T) V - lambda
+// softmax(q2 K2^T) V over the same key list, optionally RMS-normalised per row. The two
+// softmax groups take the two maps of ONE query tile instead of two query tiles: key
+// tiles come in pairs K1, K2 and one V tile serves both maps, so a key step loads three
+// tiles for the same four MMAs. Each map is normalised by its own sum only at the end,
+// so both products with V are needed (P1/l1 - lambda P2/l2 is not known while the sums
+// run); the difference and the norm are taken from TMEM in float32 and rounded once.
+// For a backward the difference before the norm and the second map's output are stored
+// too: with those two, rounded relative to their own size, the first map's follows as
+// their sum, where a difference of two rounded maps would lose what cancels in it.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -71,6 +82,7 @@ struct alignas(64) AttnParams {
   CUtensorMap map_kp, map_vp, map_kt, map_vt;
   CUtensorMap map_kp8, map_vp8;  // pooled rows in 8-row boxes (the pooled tail, see below)
   CUtensorMap map_qd, map_od;  // text-query mode: query rows and output rows (d, row, b*head)
+  CUtensorMap map_pre[kMaxShapes], map_o2[kMaxShapes];  // differential form: what a backward needs
   WindowPlan plan;
   const int32_t *route;
   int32_t *dev_err;
@@ -93,6 +105,12 @@ struct alignas(64) AttnParams {
   int text_row0;  // first k/v row of the text segment: N (window mode) or 0
   float *lse;       // nullable: log-sum-exp of each query row's scaled scores [B*heads][N]
   int all_full;  // every key tile of the launch is full: no column masks
+  int v_shift;   // v and vp belong to unit bh >> v_shift (two maps that share their values)
+  // differential form: a CTA's unit is a (batch, differential head); map g's q, k, kp are unit 2 * unit + g
+  const __nv_bfloat16 *lambda, *norm_weight;  // [heads]; nullable [128]
+  int heads, store_pre, store_o2;
+  float gain, eps;
+  float *part;  // FORM kPart: float32 outputs [split][b*head][n_text][128]
   uint32_t flags;
   unsigned long long timeout_ns;
 };
@@ -253,11 +271,27 @@ __device__ __forceinline__ void apply_mask(uint32_t (&s)[N], const uint32_t *mas
   }
 }
 
+// Writes 32 bf16 values (columns [32 cc, 32 cc + 32) of row `row`) into a swizzled tile.
+__device__ __forceinline__ void stage_cols32(uint8_t *tile, int row, int cc, const float *x) {
+  const uint32_t base = ptx::smem_u32(tile) + uint32_t(cc >> 1) * kHalfBytes + uint32_t(row) * 128u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    ptx::st_shared_v4(base + ((uint32_t((cc & 1) * 4 + i) ^ uint32_t(row & 7)) << 4),
+                      ptx::pack_bf16x2(x[8 * i], x[8 * i + 1]), ptx::pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                      ptx::pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), ptx::pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+}
+
+// kPlain: one softmax map; kDiff: differential attention; kPart: text-query rows whose
+// (partial) outputs leave in float32, for a difference of maps taken afterwards.
+enum Form { kPlain = 0, kDiff = 1, kPart = 2 };
+
+template <int FORM>
 __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_constant__ AttnParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + kSmemCtrl);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr bool DIFF = FORM == kDiff;
 
   int pair, w = 0, bh, split = 0, ot = 0, oy = 0, ox = 0, wtype = 0, n_q_tiles;
   PlanType ty{0, 0};
@@ -267,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
     bh = blockIdx.x / (P.dense_pairs * P.n_splits);
     n_q_tiles = P.dense_q_tiles;
   } else {
-    const int pairs = P.plan.max_pairs;
+    const int pairs = DIFF ? P.dense_q_tiles : P.plan.max_pairs;  // DIFF: query tiles of a window
     pair = blockIdx.x % pairs;
     w = (blockIdx.x / pairs) % P.g.nWin;
     bh = blockIdx.x / (pairs * P.g.nWin);
@@ -275,9 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
     ty = P.plan.type[wtype];
     n_q_tiles = ty.n_tiles;
   }
-  const int q_tile0 = 2 * pair;
+  const int q_tile0 = DIFF ? pair : 2 * pair;
   if (q_tile0 >= n_q_tiles) return;  // whole CTA: this window type has fewer query tiles
-  const bool has_q1 = q_tile0 + 1 < n_q_tiles;
+  const bool has_q1 = DIFF || q_tile0 + 1 < n_q_tiles;
+  constexpr int kPer = DIFF ? 3 : 2;  // ring items of a key step: K, V, or K1, K2, V
+  // unit of map g's queries and keys, and of the values
+  const int unit0 = DIFF ? 2 * bh : bh, unit_step = DIFF ? 1 : 0, unit_v = DIFF ? bh : bh >> P.v_shift;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -346,19 +383,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
       } else {
         // a tile's TMA boxes deliver 256 bytes per valid row (two 128-byte halves)
         uint32_t qbytes = uint32_t(P.plan.tile[ty.first_tile + q_tile0].valid_rows) * 256u;
-        if (has_q1) qbytes += uint32_t(P.plan.tile[ty.first_tile + q_tile0 + 1].valid_rows) * 256u;
+        if (has_q1) qbytes += DIFF ? qbytes : uint32_t(P.plan.tile[ty.first_tile + q_tile0 + 1].valid_rows) * 256u;
         ptx::mbar_arrive_expect_tx(&c.q_full, qbytes);
         for (int g = 0; g < (has_q1 ? 2 : 1); ++g)
-          sm100::load_window_tile(P.plan, P.g, P.map_q, P.plan.tile[ty.first_tile + q_tile0 + g], c.org[0], bh,
-                                  smem + kSmemQ + g * kTileBytes, &c.q_full);
+          sm100::load_window_tile(P.plan, P.g, P.map_q, P.plan.tile[ty.first_tile + q_tile0 + (DIFF ? 0 : g)], c.org[0],
+                                  unit0 + g * unit_step, smem + kSmemQ + g * kTileBytes, &c.q_full);
       }
       KeyIter it = first_key(P, c);
       int last = -1;
       bool skipped0 = false;
       for (int j = 0; j < n_kt; ++j) {
         bool ok = true;
-        for (int kv = 0; kv < 2; ++kv) {
-          const int item = 2 * j + kv;
+        for (int kv = 0; kv < kPer; ++kv) {
+          const int item = kPer * j + kv;
           const int slot = item % kStages;
           if (!wt.wait(&c.empty[slot], ((item / kStages) & 1) ^ 1)) { ok = false; break; }
           if (item == 0 && (P.flags & BASA_FLAG_TEST_SKIP_FIRST_KEY_LOAD)) { skipped0 = true; last = item; continue; }
@@ -366,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
           // Arm the barrier with the byte count before issuing the copies.
           const uint32_t bytes = key_tile_bytes(P, c, it);
           ptx::mbar_arrive_expect_tx(&c.full[slot], bytes);
-          load_key_tile(P, c, it, kv == 1, bh, dst, &c.full[slot]);
+          const bool is_v = kv == kPer - 1;
+          load_key_tile(P, c, it, is_v, is_v ? unit_v : unit0 + kv * unit_step, dst, &c.full[slot]);
           last = item;
         }
         if (!ok) break;
@@ -394,12 +432,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
         ptx::tc_fence_after();
         sm100::issue_ss(tS0, sQ, sRk);
         ptx::mma_commit(&c.s_full[0]);
-        if (has_q1) {
+        if (has_q1 && !DIFF) {
           sm100::issue_ss(tS1, sQ + kTileDesc, sRk);
           ptx::mma_commit(&c.s_full[1]);
         }
         ptx::mma_commit(&c.empty[0]);
-        for (int j = 0; j < n_kt; ++j) {
+        bool started = true;
+        if (DIFF) {
+          started = wt.wait(&c.full[1], 0);
+          if (started) {
+            ptx::tc_fence_after();
+            sm100::issue_ss(tS1, sQ + kTileDesc, sRk + kTileDesc);
+            ptx::mma_commit(&c.s_full[1]);
+            ptx::mma_commit(&c.empty[1]);
+          }
+        }
+        for (int j = 0; DIFF && started && j < n_kt; ++j) {
+          // items of this step's V and of the next step's K1, K2
+          const int vi = 3 * j + 2, k0 = vi + 1, k1 = vi + 2;
+          const uint32_t vaddr = sRv + (vi % kStages) * kTileDesc;
+          const bool more = j + 1 < n_kt;
+          if (!wt.wait(&c.full[vi % kStages], (vi / kStages) & 1)) break;
+          if (!wt.wait(&c.p_full[0], j & 1)) break;
+          ptx::tc_fence_after();
+          sm100::issue_ts(tO0, tS0, vaddr, j > 0);
+          if (more) {
+            if (!wt.wait(&c.full[k0 % kStages], (k0 / kStages) & 1)) break;
+            ptx::tc_fence_after();
+            sm100::issue_ss(tS0, sQ, sRk + (k0 % kStages) * kTileDesc);
+            ptx::mma_commit(&c.s_full[0]);
+            ptx::mma_commit(&c.empty[k0 % kStages]);
+          } else {
+            ptx::mma_commit(&c.o_full[0]);
+          }
+          if (!wt.wait(&c.p_full[1], j & 1)) break;
+          ptx::tc_fence_after();
+          sm100::issue_ts(tO1, tS1, vaddr, j > 0);
+          ptx::mma_commit(&c.empty[vi % kStages]);
+          if (more) {
+            if (!wt.wait(&c.full[k1 % kStages], (k1 / kStages) & 1)) break;
+            ptx::tc_fence_after();
+            sm100::issue_ss(tS1, sQ + kTileDesc, sRk + (k1 % kStages) * kTileDesc);
+            ptx::mma_commit(&c.s_full[1]);
+            ptx::mma_commit(&c.empty[k1 % kStages]);
+          } else {
+            ptx::mma_commit(&c.o_full[1]);
+          }
+        }
+        for (int j = 0; !DIFF && j < n_kt; ++j) {
           const int vi = 2 * j + 1, ki = 2 * j + 2;
           const uint32_t vaddr = sRv + (vi % kStages) * kTileDesc, kaddr = sRk + (ki % kStages) * kTileDesc;
           const bool more = j + 1 < n_kt;
@@ -524,36 +604,115 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
           advance(P, c, it);
       }
     }
-    if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.o_full[g], 0));
-    if (ok) {
-      ptx::tc_fence_after();
-      const float inv = 1.0f / l;
-      const uint64_t inv2 = ptx::f2_pack(inv, inv);
-      const uint32_t o_row = ptx::smem_u32(q_tile) + row * 128;
+    if (DIFF) {
+      // Both maps' outputs are read by both groups: group g takes columns [64 g, 64 g + 64)
+      // of O1 / l1 - lambda O2 / l2 (a TMEM lane holds the same query row of both).
+      // The ring is free by now: out is staged in its slot 0, row sums in its slot 1;
+      // the difference before the norm and O2 / l2, when asked for, over the query tiles.
+      float *inv_l = reinterpret_cast<float *>(smem + kSmemRing + kTileBytes);  // [2][128]
+      float *sq = inv_l + 2 * kTileRows;                                         // [2][128]
+      if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.o_full[0], 0) && wt.wait(&c.o_full[1], 0));
+      if (ok) inv_l[g * kTileRows + row] = 1.0f / l;
+      ptx::named_barrier(3, 256);
+      float a[64];
+      float ss = 0.f;
+      if (ok) {
+        ptx::tc_fence_after();
+        const float i0 = inv_l[row], i1 = inv_l[kTileRows + row];
+        const float lam = __bfloat162float(P.lambda[bh % P.heads]);
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        uint32_t r[32];
-        ptx::tmem_ld32(tO + cc * 32, r);
-        ptx::tmem_ld_wait(r);
+        for (int h = 0; h < 2; ++h) {
+          const int cc = 2 * g + h;
+          uint32_t r0[32], r1[32];
+          ptx::tmem_ld32(tmem + lane_off + 256 + cc * 32, r0);
+          ptx::tmem_ld32(tmem + lane_off + 384 + cc * 32, r1);
+          ptx::tmem_ld_wait(r0);
+          ptx::tmem_ld_wait(r1);
+          float o1[32];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          float lo, hi;
-          ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), inv2), lo, hi);
-          r[i] = __float_as_uint(lo);
-          r[i + 1] = __float_as_uint(hi);
+          for (int i = 0; i < 32; ++i) {
+            o1[i] = __uint_as_float(r1[i]) * i1;
+            a[32 * h + i] = fmaf(-lam, o1[i], __uint_as_float(r0[i]) * i0);
+            ss = fmaf(a[32 * h + i], a[32 * h + i], ss);
+          }
+          if (P.store_pre) stage_cols32(smem + kSmemQ, row, cc, a + 32 * h);
+          if (P.store_o2) stage_cols32(smem + kSmemQ + kTileBytes, row, cc, o1);
         }
+        sq[g * kTileRows + row] = ss;
+      }
+      if (P.norm_weight != nullptr) ptx::named_barrier(3, 256);
+      if (ok) {
+        if (P.norm_weight != nullptr) {
+          const float f = rsqrtf((sq[row] + sq[kTileRows + row]) * (1.0f / 128.0f) + P.eps) * P.gain;
+          const uint4 *w4 = reinterpret_cast<const uint4 *>(P.norm_weight + 64 * g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c16 = cc * 4 + i;
-          const uint32_t addr = o_row + (c16 >> 3) * kHalfBytes + (((c16 & 7) ^ swz) << 4);
-          const int b = 8 * i;
-          ptx::st_shared_v4(addr, ptx::pack_bf16x2(__uint_as_float(r[b]), __uint_as_float(r[b + 1])),
-                            ptx::pack_bf16x2(__uint_as_float(r[b + 2]), __uint_as_float(r[b + 3])),
-                            ptx::pack_bf16x2(__uint_as_float(r[b + 4]), __uint_as_float(r[b + 5])),
-                            ptx::pack_bf16x2(__uint_as_float(r[b + 6]), __uint_as_float(r[b + 7])));
+          for (int i = 0; i < 8; ++i) {
+            const uint4 u = __ldg(w4 + i);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[8 * i + 2 * e] *= f * __uint_as_float(w[e] << 16);
+              a[8 * i + 2 * e + 1] *= f * __uint_as_float(w[e] & 0xFFFF0000u);
+            }
+          }
+        }
+        stage_cols32(smem + kSmemRing, row, 2 * g, a);
+        stage_cols32(smem + kSmemRing, row, 2 * g + 1, a + 32);
+        ptx::fence_proxy_async_smem();
+      }
+    } else if (FORM == kPart) {
+      // this thread's row of O / l as it is, 512 bytes (rows past n_text are not written)
+      if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.o_full[g], 0));
+      const int qrow = (q_tile0 + g) * kTileRows + row;
+      if (ok) {
+        ptx::tc_fence_after();
+        const float inv = 1.0f / l;
+        float4 *dst = reinterpret_cast<float4 *>(P.part + (((long long)split * P.bh_count + bh) * P.n_text + qrow) * 128);
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t r[32];
+          ptx::tmem_ld32(tO + cc * 32, r);
+          ptx::tmem_ld_wait(r);
+          if (qrow < P.n_text && !*reinterpret_cast<volatile int *>(&c.abort)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[8 * cc + i] = make_float4(__uint_as_float(r[4 * i]) * inv, __uint_as_float(r[4 * i + 1]) * inv,
+                                            __uint_as_float(r[4 * i + 2]) * inv, __uint_as_float(r[4 * i + 3]) * inv);
+          }
         }
       }
-      ptx::fence_proxy_async_smem();
+    } else {
+      if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.o_full[g], 0));
+      if (ok) {
+        ptx::tc_fence_after();
+        const float inv = 1.0f / l;
+        const uint64_t inv2 = ptx::f2_pack(inv, inv);
+        const uint32_t o_row = ptx::smem_u32(q_tile) + row * 128;
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t r[32];
+          ptx::tmem_ld32(tO + cc * 32, r);
+          ptx::tmem_ld_wait(r);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float lo, hi;
+            ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), inv2), lo, hi);
+            r[i] = __float_as_uint(lo);
+            r[i + 1] = __float_as_uint(hi);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c16 = cc * 4 + i;
+            const uint32_t addr = o_row + (c16 >> 3) * kHalfBytes + (((c16 & 7) ^ swz) << 4);
+            const int b = 8 * i;
+            ptx::st_shared_v4(addr, ptx::pack_bf16x2(__uint_as_float(r[b]), __uint_as_float(r[b + 1])),
+                              ptx::pack_bf16x2(__uint_as_float(r[b + 2]), __uint_as_float(r[b + 3])),
+                              ptx::pack_bf16x2(__uint_as_float(r[b + 4]), __uint_as_float(r[b + 5])),
+                              ptx::pack_bf16x2(__uint_as_float(r[b + 6]), __uint_as_float(r[b + 7])));
+          }
+        }
+        ptx::fence_proxy_async_smem();
+      }
     }
     if (ok && P.lse != nullptr && P.dense) {
       const int qrow = (q_tile0 + g) * kTileRows + row;
@@ -563,11 +722,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
       // log-sum-exp of this row: m and l are in base 2 of the scaled scores
       int t, y, x;
       const int org[3] = {ot, oy, ox};
-      if (sm100::tile_row_token(P.plan, P.g, P.plan.tile[ty.first_tile + q_tile0 + g], org, row, &t, &y, &x))
-        P.lse[(long long)bh * P.g.N + ((long long)t * P.g.H + y) * P.g.W + x] = (m + log2f(l)) * 0.6931471805599453f;
+      if (sm100::tile_row_token(P.plan, P.g, P.plan.tile[ty.first_tile + q_tile0 + (DIFF ? 0 : g)], org, row, &t, &y, &x))
+        P.lse[(long long)(unit0 + g * unit_step) * P.g.N + ((long long)t * P.g.H + y) * P.g.W + x] = (m + log2f(l)) * 0.6931471805599453f;
     }
-    ptx::named_barrier(1 + g, 128);
-    if (P.dense && active && row == 0 && !*reinterpret_cast<volatile int *>(&c.abort)) {
+    if (DIFF) {
+      ptx::named_barrier(3, 256);  // both groups have staged their columns
+      if (row == 0 && !*reinterpret_cast<volatile int *>(&c.abort)) {
+        const int org[3] = {ot, oy, ox};
+        const PlanTile &tile = P.plan.tile[ty.first_tile + q_tile0];
+        if (g == 0) sm100::store_window_tile(P.plan, P.g, P.map_o, tile, org, bh, smem + kSmemRing);
+        if (g == 0 && P.store_pre) sm100::store_window_tile(P.plan, P.g, P.map_pre, tile, org, bh, q_tile);
+        if (g == 1 && P.store_o2) sm100::store_window_tile(P.plan, P.g, P.map_o2, tile, org, bh, q_tile);
+        ptx::tma_store_commit();
+        ptx::tma_store_wait_read_all();
+      }
+    } else if (FORM == kPlain) {
+      ptx::named_barrier(1 + g, 128);
+    }
+    if (FORM != kPlain) {
+    } else if (P.dense && active && row == 0 && !*reinterpret_cast<volatile int *>(&c.abort)) {
       // rows past n_text fall outside the output map and are not written
       const int orow = (q_tile0 + g) * kTileRows, ob = split * P.bh_count + bh;
       ptx::tma_store_3d(&P.map_od, q_tile, 0, orow, ob);
@@ -634,10 +807,12 @@ bool plan_pool_tail(AttnParams &P) {
   return true;
 }
 
+template <int FORM>
 basa_status run_attn(const AttnParams &P, long long blocks, cudaStream_t s) {
-  if (cudaFuncSetAttribute(attn_bf16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+  if (cudaFuncSetAttribute(attn_bf16_kernel<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+      cudaSuccess)
     return BASA_ERR_CUDA;
-  attn_bf16_kernel<<<unsigned(blocks), kThreads, kSmemBytes, s>>>(P);
+  attn_bf16_kernel<FORM><<<unsigned(blocks), kThreads, kSmemBytes, s>>>(P);
   return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
 }
 
@@ -718,20 +893,24 @@ int device_sm_count() {
   return n[dev];
 }
 
-basa_status launch_attn_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
-                             const int32_t *route_idx, void *out, float *lse, uint32_t keys, const basa_params &p,
-                             cudaStream_t s) {
+namespace {
+// Parameters of a window-mode launch. `maps` softmax maps share a head's values: q, k, kp
+// have maps * heads heads, v, vp and out have heads.
+basa_status window_params(AttnParams &P, const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                          const int32_t *route_idx, void *out, float *lse, uint32_t keys, const basa_params &p,
+                          int maps) {
   if (!tensor_map_encoder()) return BASA_ERR_CUDA;
-  AttnParams P;
   std::memset(&P, 0, sizeof(P));
   basa_status st = build_window_plan(p, &P.plan);
   if (st != BASA_OK) return st;
   P.g = make_geo(p);
   const long long N = P.g.N;
   const long long kv_rows = N + p.n_text;
+  basa_params pm = p;
+  pm.heads = p.heads * maps;
   for (int i = 0; i < P.plan.n_shapes; ++i) {
-    if (!encode_grid_map(&P.map_q[i], q, p, N, P.plan.shape[i]) ||
-        !encode_grid_map(&P.map_k[i], k, p, kv_rows, P.plan.shape[i]) ||
+    if (!encode_grid_map(&P.map_q[i], q, pm, N, P.plan.shape[i]) ||
+        !encode_grid_map(&P.map_k[i], k, pm, kv_rows, P.plan.shape[i]) ||
         !encode_grid_map(&P.map_v[i], v, p, kv_rows, P.plan.shape[i]) ||
         !encode_grid_map(&P.map_o[i], out, p, N, P.plan.shape[i]))
       return BASA_ERR_CUDA;
@@ -739,15 +918,15 @@ basa_status launch_attn_bf16(const void *q, const void *k, const void *v, const 
   P.n_pool = p.pt > 0 ? (p.T / p.pt) * (p.H / p.ph) * (p.W / p.pw) : 0;
   P.n_text = p.n_text;
   if (P.n_pool > 0) {
-    if (!encode_rows_map(&P.map_kp, kp, p, P.n_pool) || !encode_rows_map(&P.map_vp, vp, p, P.n_pool))
+    if (!encode_rows_map(&P.map_kp, kp, pm, P.n_pool) || !encode_rows_map(&P.map_vp, vp, p, P.n_pool))
       return BASA_ERR_CUDA;
   }
   if (p.n_text > 0) {
-    if (!encode_rows_map(&P.map_kt, k, p, kv_rows) || !encode_rows_map(&P.map_vt, v, p, kv_rows)) return BASA_ERR_CUDA;
+    if (!encode_rows_map(&P.map_kt, k, pm, kv_rows) || !encode_rows_map(&P.map_vt, v, p, kv_rows)) return BASA_ERR_CUDA;
   }
   P.n_pool_tiles = (keys & BASA_KEYS_POOLED) ? (P.n_pool + kTileRows - 1) / kTileRows : 0;
   if ((keys & BASA_KEYS_POOLED) && (keys & BASA_KEYS_WINDOWS) && plan_pool_tail(P)) {
-    if (!encode_rows_map(&P.map_kp8, kp, p, P.n_pool, 8) || !encode_rows_map(&P.map_vp8, vp, p, P.n_pool, 8))
+    if (!encode_rows_map(&P.map_kp8, kp, pm, P.n_pool, 8) || !encode_rows_map(&P.map_vp8, vp, p, P.n_pool, 8))
       return BASA_ERR_CUDA;
   }
   P.n_text_tiles = (keys & BASA_KEYS_TEXT) ? (p.n_text + kTileRows - 1) / kTileRows : 0;
@@ -762,9 +941,42 @@ basa_status launch_attn_bf16(const void *q, const void *k, const void *v, const 
   P.all_full = (P.n_pool % kTileRows == 0) && (p.n_text % kTileRows == 0);
   for (int i = 0; i < P.plan.n_tiles; ++i) P.all_full &= P.plan.tile[i].valid_rows == kTileRows;
   P.timeout_ns = (p.wait_timeout_us ? (unsigned long long)p.wait_timeout_us : 2000000ull) * 1000ull;
+  return BASA_OK;
+}
+}  // namespace
+
+basa_status launch_attn_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                             const int32_t *route_idx, void *out, float *lse, uint32_t keys, const basa_params &p,
+                             cudaStream_t s) {
+  AttnParams P;
+  basa_status st = window_params(P, q, k, v, kp, vp, route_idx, out, lse, keys, p, 1);
+  if (st != BASA_OK) return st;
   const long long blocks = (long long)p.B * p.heads * P.g.nWin * P.plan.max_pairs;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  return run_attn(P, blocks, s);
+  return run_attn<kPlain>(P, blocks, s);
+}
+
+basa_status launch_diff_attn_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                                  const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
+                                  void *second, float *lse, const basa_params &p, cudaStream_t s) {
+  AttnParams P;
+  basa_status st = window_params(P, q, k, v, kp, vp, route_idx, out, lse, BASA_KEYS_ALL, p, 2);
+  if (st != BASA_OK) return st;
+  P.lambda = static_cast<const __nv_bfloat16 *>(dp.lambda);
+  P.norm_weight = static_cast<const __nv_bfloat16 *>(dp.weight);
+  P.gain = dp.gain;
+  P.eps = dp.eps;
+  P.heads = p.heads;
+  P.store_pre = pre != nullptr;
+  P.store_o2 = second != nullptr;
+  for (int i = 0; i < P.plan.n_shapes; ++i)
+    if ((pre && !encode_grid_map(&P.map_pre[i], pre, p, P.g.N, P.plan.shape[i])) ||
+        (second && !encode_grid_map(&P.map_o2[i], second, p, P.g.N, P.plan.shape[i])))
+      return BASA_ERR_CUDA;
+  for (int t = 0; t < 8; ++t) P.dense_q_tiles = std::max<int>(P.dense_q_tiles, P.plan.type[t].n_tiles);
+  const long long blocks = (long long)p.B * p.heads * P.g.nWin * P.dense_q_tiles;
+  if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
+  return run_attn<kDiff>(P, blocks, s);
 }
 
 size_t text_attn_workspace(const basa_params &p, int sms) {
@@ -774,27 +986,22 @@ size_t text_attn_workspace(const basa_params &p, int sms) {
   return rows * p.head_dim * 2 + rows * sizeof(float);  // partial outputs (bf16), then their log-sum-exp
 }
 
-basa_status launch_attn_text_bf16(const void *q_text, const void *k, const void *v, void *out_text, void *workspace,
-                                  const basa_params &p, int sms, cudaStream_t s) {
+namespace {
+// Parameters of a text-query launch over p.heads maps, whose values v_shift maps share
+// in groups of 2^v_shift. The caller sets where the outputs go.
+basa_status text_params(AttnParams &P, const void *q_text, const void *k, const void *v, const basa_params &p, int splits,
+                        int v_shift) {
   if (!tensor_map_encoder()) return BASA_ERR_CUDA;
-  AttnParams P;
   std::memset(&P, 0, sizeof(P));
   P.g = make_geo(p);
   const long long N = P.g.N;
   const long long kv_rows = N + p.n_text;
   const int bh = p.B * p.heads;
-  const int splits = text_splits(p, sms);
-  uint8_t *part = static_cast<uint8_t *>(workspace);
-  float *part_lse = reinterpret_cast<float *>(part + size_t(splits) * bh * p.n_text * p.head_dim * 2);
-  if (!encode_rows_map(&P.map_kt, k, p, kv_rows) || !encode_rows_map(&P.map_vt, v, p, kv_rows) ||
+  basa_params pv = p;
+  pv.heads = p.heads >> v_shift;
+  P.v_shift = v_shift;
+  if (!encode_rows_map(&P.map_kt, k, p, kv_rows) || !encode_rows_map(&P.map_vt, v, pv, kv_rows) ||
       !encode_rows_map(&P.map_qd, q_text, p, p.n_text))
-    return BASA_ERR_CUDA;
-  // outputs: straight to out_text, or per-split partials [split][b*head][n_text][d]
-  basa_params po = p;
-  po.B = 1;
-  po.heads = splits * bh;
-  if (!encode_rows_map(&P.map_od, splits > 1 ? static_cast<const void *>(part) : out_text, splits > 1 ? po : p,
-                       p.n_text))
     return BASA_ERR_CUDA;
   P.dense = 1;
   P.dense_rows = int(kv_rows);
@@ -809,15 +1016,35 @@ basa_status launch_attn_text_bf16(const void *q_text, const void *k, const void 
   P.routed_k = 0;
   P.use_windows = 0;
   P.text_row0 = 0;
-  P.lse = P.n_splits > 1 ? part_lse : nullptr;
   P.dev_err = p.dev_err;
   P.scale_log2 = float(1.4426950408889634 / std::sqrt(double(p.head_dim)));
   P.flags = p.flags;
   P.all_full = kv_rows % kTileRows == 0;
   P.timeout_ns = (p.wait_timeout_us ? (unsigned long long)p.wait_timeout_us : 2000000ull) * 1000ull;
+  return BASA_OK;
+}
+}  // namespace
+
+basa_status launch_attn_text_bf16(const void *q_text, const void *k, const void *v, void *out_text, void *workspace,
+                                  const basa_params &p, int sms, cudaStream_t s) {
+  AttnParams P;
+  const int bh = p.B * p.heads;
+  const int splits = text_splits(p, sms);
+  basa_status st = text_params(P, q_text, k, v, p, splits, 0);
+  if (st != BASA_OK) return st;
+  uint8_t *part = static_cast<uint8_t *>(workspace);
+  float *part_lse = reinterpret_cast<float *>(part + size_t(splits) * bh * p.n_text * p.head_dim * 2);
+  // outputs: straight to out_text, or per-split partials [split][b*head][n_text][d]
+  basa_params po = p;
+  po.B = 1;
+  po.heads = splits * bh;
+  if (!encode_rows_map(&P.map_od, splits > 1 ? static_cast<const void *>(part) : out_text, splits > 1 ? po : p,
+                       p.n_text))
+    return BASA_ERR_CUDA;
+  P.lse = P.n_splits > 1 ? part_lse : nullptr;
   const long long blocks = (long long)bh * P.dense_pairs * P.n_splits;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  basa_status st = run_attn(P, blocks, s);
+  st = run_attn<kPlain>(P, blocks, s);
   if (st != BASA_OK || P.n_splits == 1) return st;
   const void *outs[kMaxTextSplits];
   const float *lses[kMaxTextSplits];
@@ -826,6 +1053,32 @@ basa_status launch_attn_text_bf16(const void *q_text, const void *k, const void 
     lses[i] = part_lse + size_t(i) * bh * p.n_text;
   }
   return launch_merge_rows(P.n_splits, outs, lses, out_text, nullptr, (long long)bh * p.n_text, p.head_dim, p.dtype, s);
+}
+
+// The two maps' text rows, each by itself, split over the key range; every split's
+// outputs stay in float32 until the maps' difference is taken.
+size_t diff_text_workspace(const basa_params &p, int sms) {
+  basa_params pm = p;
+  pm.heads = 2 * p.heads;
+  const size_t rows = size_t(text_splits(pm, sms)) * pm.B * pm.heads * p.n_text;
+  return rows * (p.head_dim + 1) * sizeof(float);  // partial outputs, then their log-sum-exp
+}
+
+basa_status launch_diff_text_bf16(const void *q_text, const void *k, const void *v, const basa_diff_params &dp,
+                                  void *out_text, void *workspace, const basa_params &p, int sms, cudaStream_t s) {
+  AttnParams P;
+  basa_params pm = p;
+  pm.heads = 2 * p.heads;
+  const int splits = text_splits(pm, sms);
+  basa_status st = text_params(P, q_text, k, v, pm, splits, 1);
+  if (st != BASA_OK) return st;
+  const size_t rows = size_t(splits) * pm.B * pm.heads * p.n_text;
+  P.part = static_cast<float *>(workspace);
+  P.lse = P.part + rows * p.head_dim;
+  const long long blocks = (long long)P.bh_count * P.dense_pairs * P.n_splits;
+  if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
+  if ((st = run_attn<kPart>(P, blocks, s)) != BASA_OK) return st;
+  return launch_diff_combine(P.n_splits, P.part, P.lse, p.n_text, dp, out_text, nullptr, nullptr, p, s);
 }
 
 }  // namespace basa

@@ -28,6 +28,14 @@
 //                MMAs; the epilogue adds the pooled-key gradient of each token's
 //                patch / |patch| and stores dk, dv at the tokens' positions.
 //
+// Differential form (template argument DIFF; out = O1 - lambda O2 of two maps that share
+// their values, the norm's gradient g taken beforehand and D per map in the records): the
+// dq pass runs over the maps, with map 2's sums scaled by -lambda in its epilogue. The
+// dK/dV passes run both maps of a (batch, head) in ONE CTA, map 2 first: its dK leaves,
+// the dV accumulator is multiplied by -lambda in TMEM, and map 1 adds to it, so the two
+// maps' dV meet without a buffer or an atomic. (Both maps at once, sharing dout V^T, would
+// take six 128-column accumulators and TMEM holds four.)
+//
 // Warp roles (320 threads): warp 0 TMA loads, warp 1 issues tcgen05 MMAs (one
 // thread), warps 2-9 compute P and dS: two warpgroups, each owning 64 of the 128
 // columns of a row (the backward has no row reductions, so the columns split
@@ -88,9 +96,13 @@ struct alignas(64) BwdParams {
   int32_t *dev_err;
   const float4 *rec;  // the records, [bh][N] (dq pass: each thread reads its row's)
   const float *dkvp;  // final pooled-key gradients: dkp [bh][Np][128], then dvp
-  float *part;        // long key tiles: [bh][tile][chunk][dK | dV][128][128] partial sums
+  float *part;        // long key tiles: [bh][tile][chunk][dK (of each map) | dV][128][128] partial sums
+  const __nv_bfloat16 *lambda;  // differential form: [heads]
+  __nv_bfloat16 *dk;            // differential form: dk itself, for map 2's rows
+  int heads;
   Geo g;
-  int bh_count, routed_k, n_pool, n_text, n_pool_tiles, n_text_tiles, n_long_tiles;
+  int bh_count;  // units of v, dout and the routes (differential form: q, k have two for each)
+  int routed_k, n_pool, n_text, n_pool_tiles, n_text_tiles, n_long_tiles;
   int pt, ph, pw;
   float inv_patch;
   float scale_log2;  // log2(e) / sqrt(d)
@@ -107,7 +119,7 @@ struct Ctrl {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   // dq pass: a_ready, s_full[0], s_free, dp_full[0], ds_full[0]; dK/dV passes: s_full[0],
   // dp_full[0], and per compute group p_full[g], ds_full[g]
-  uint64_t row_full, s_full[2], dp_full[2], s_free, a_ready, p_full[2], ds_full[2], acc_full, drain;
+  uint64_t row_full, row_free, s_full[2], dp_full[2], s_free, a_ready, p_full[2], ds_full[2], acc_full, drain;
   uint32_t tmem_base;
   int abort;
   int n_cols;   // column tiles streamed by this CTA
@@ -139,7 +151,7 @@ __device__ __forceinline__ void key_next(const BwdParams &P, const Ctrl &c, KeyI
   }
 }
 __device__ __forceinline__ uint32_t load_key(const BwdParams &P, const Ctrl &c, const KeyIter &it, bool is_v, int bh,
-                                             uint8_t *dst, uint64_t *bar) {
+                                             uint8_t *dst, uint64_t *bar) {  // bh: unit of the tensor read
   if (it.seg <= P.routed_k) {
     const PlanTile &tile = P.plan.tile[P.plan.type[c.wtype[it.seg]].first_tile + it.t];
     load_window_tile(P.plan, P.g, is_v ? P.map_v : P.map_k, tile, c.org[it.seg], bh, dst, bar);
@@ -251,7 +263,7 @@ __device__ __forceinline__ void load_row_half(const uint8_t *tile, int row, int 
   }
 }
 
-template <int MODE>
+template <int MODE, bool DIFF>
 __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid_constant__ BwdParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -274,6 +286,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     window_origin(P.g, w, &ot, &oy, &ox, &wtype);
     if (tile_idx >= P.plan.type[wtype].n_tiles) return;  // whole CTA: this window type has fewer tiles
   }
+  // Units: bh counts maps in the dq pass and values (two maps each) in the dK/dV passes.
+  const int bh_v = DIFF && MODE == kDq ? bh >> 1 : bh;       // unit of v, dout and the routes
+  constexpr int kMaps = DIFF && MODE != kDq ? 2 : 1;         // maps this CTA goes through
+  auto map_unit = [&](int m) { return kMaps == 2 ? 2 * bh + 1 - m : bh; };  // unit of q, k of its m-th map
+  const float neg_lambda = DIFF ? -__bfloat162float(P.lambda[bh_v % P.heads]) : 1.f;
   const int row_org[3] = {ot, oy, ox};
   const PlanTile &row_tile = P.plan.tile[P.plan.type[wtype].first_tile + tile_idx];  // window modes
 
@@ -283,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
       ptx::mbar_init(&c.empty[i], 1);
     }
     ptx::mbar_init(&c.row_full, 1);
+    ptx::mbar_init(&c.row_free, 1);
     const uint32_t per_group = MODE == kDq ? 256 : 128;  // compute threads that arrive
     for (int g = 0; g < 2; ++g) {
       ptx::mbar_init(&c.s_full[g], 1);
@@ -299,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
       c.wtype[0] = wtype;
       c.org[0][0] = ot; c.org[0][1] = oy; c.org[0][2] = ox;
       for (int r = 0; r < P.routed_k; ++r) {
-        int u = P.route[((long long)bh * P.g.nWin + w) * P.routed_k + r];
+        int u = P.route[((long long)bh_v * P.g.nWin + w) * P.routed_k + r];
         if (u < 0 || u >= P.g.nWin) {  // reported, and replaced by the own window: accesses stay in bounds
           if (P.dev_err) atomicOr(P.dev_err, BASA_DEVERR_BAD_ROUTE);
           u = w;
@@ -378,22 +396,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
       if (MODE == kDq) {
         ptx::mbar_arrive_expect_tx(&c.row_full, uint32_t(row_tile.valid_rows) * 512u);
         load_window_tile(P.plan, P.g, P.map_q, row_tile, row_org, bh, row0, &c.row_full);
-        load_window_tile(P.plan, P.g, P.map_do, row_tile, row_org, bh, row1, &c.row_full);
+        load_window_tile(P.plan, P.g, P.map_do, row_tile, row_org, bh_v, row1, &c.row_full);
       } else if (MODE == kDkvWindow) {
         ptx::mbar_arrive_expect_tx(&c.row_full, uint32_t(row_tile.valid_rows) * 512u);
-        load_window_tile(P.plan, P.g, P.map_k, row_tile, row_org, bh, row0, &c.row_full);
+        load_window_tile(P.plan, P.g, P.map_k, row_tile, row_org, map_unit(0), row0, &c.row_full);
         load_window_tile(P.plan, P.g, P.map_v, row_tile, row_org, bh, row1, &c.row_full);
       } else {
         const bool pooled = kt < P.n_pool_tiles;
         const CUtensorMap *mk = pooled ? &P.map_kp : &P.map_kt, *mv = pooled ? &P.map_vp : &P.map_vt;
         const int row = pooled ? kt * kTileRows : P.g.N + (kt - P.n_pool_tiles) * kTileRows;
         ptx::mbar_arrive_expect_tx(&c.row_full, 2 * kTileBytes);
-        ptx::tma_load_3d(row0, mk, &c.row_full, 0, row, bh);
-        ptx::tma_load_3d(row0 + kHalfBytes, mk, &c.row_full, 64, row, bh);
+        ptx::tma_load_3d(row0, mk, &c.row_full, 0, row, map_unit(0));
+        ptx::tma_load_3d(row0 + kHalfBytes, mk, &c.row_full, 64, row, map_unit(0));
         ptx::tma_load_3d(row1, mv, &c.row_full, 0, row, bh);
         ptx::tma_load_3d(row1 + kHalfBytes, mv, &c.row_full, 64, row, bh);
       }
-      int last = -1, last_k = -1, last_v = -1;
+      int last = -1, last_k = -1, last_v = -1, row_loads = 1;
       bool skipped0 = false;  // test hook: the first ring item was never loaded
       if (MODE == kDq) {
         KeyIter it;
@@ -412,45 +430,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
                                        ? uint32_t(P.plan.tile[P.plan.type[c.wtype[it.seg]].first_tile + it.t].valid_rows) * 256u
                                        : kTileBytes;
             ptx::mbar_arrive_expect_tx(&c.full[slot], bytes);
-            load_key(P, c, it, kv == 1, bh, smem + kSmemRing + slot * kTileBytes, &c.full[slot]);
+            load_key(P, c, it, kv == 1, kv == 1 ? bh_v : bh, smem + kSmemRing + slot * kTileBytes, &c.full[slot]);
             (kv ? last_v : last_k) = j;
           }
           if (!ok) break;
           key_next(P, c, it);
         }
       } else if (n_cols > 0) {
-        QIter it;
-        q_first(P, list, MODE, MODE == kDkvLong ? chunk * P.chunk_tiles : 0, it);
-        for (int j = 0; j < n_cols; ++j) {
-          bool ok = true;
-          const PlanTile &tile = q_tile(P, it);
-          for (int kv = 0; kv < 2; ++kv) {
-            const int item = 2 * j + kv, slot = item % kSlots;
-            if (!wt.wait(&c.empty[slot], ((item / kSlots) & 1) ^ 1)) { ok = false; break; }
-            if (item == 0 && (P.flags & BASA_FLAG_TEST_SKIP_FIRST_KEY_LOAD)) {
-              skipped0 = true;
-              last = 0;
-              continue;
-            }
-            uint8_t *dst = smem + kSmemRing + slot * kTileBytes;
-            if (kv == 0) {  // q tile and its records (record buffer j & 1, freed with the q slot)
-              ptx::mbar_arrive_expect_tx(&c.full[slot], uint32_t(tile.valid_rows) * (256u + 16u));
-              load_window_tile(P.plan, P.g, P.map_q, tile, it.org, bh, dst, &c.full[slot]);
-              load_window_records(P.plan, P.g, P.map_rec, tile, it.org, bh, smem + L::rec + (j & 1) * kRecBytes,
-                                  &c.full[slot]);
+        bool ok = true;
+        for (int m = 0; ok && m < kMaps; ++m) {
+          const int unit = map_unit(m);
+          if (m == 1) {  // the key tile of map 1, once the last product with map 2's has read it
+            if (!wt.wait(&c.row_free, 0)) break;
+            const bool pooled = MODE == kDkvLong && kt < P.n_pool_tiles;
+            if (MODE == kDkvWindow) {
+              ptx::mbar_arrive_expect_tx(&c.row_full, uint32_t(row_tile.valid_rows) * 256u);
+              load_window_tile(P.plan, P.g, P.map_k, row_tile, row_org, unit, row0, &c.row_full);
             } else {
-              ptx::mbar_arrive_expect_tx(&c.full[slot], uint32_t(tile.valid_rows) * 256u);
-              load_window_tile(P.plan, P.g, P.map_do, tile, it.org, bh, dst, &c.full[slot]);
+              const CUtensorMap *mk = pooled ? &P.map_kp : &P.map_kt;
+              const int row = pooled ? kt * kTileRows : P.g.N + (kt - P.n_pool_tiles) * kTileRows;
+              ptx::mbar_arrive_expect_tx(&c.row_full, kTileBytes);
+              ptx::tma_load_3d(row0, mk, &c.row_full, 0, row, unit);
+              ptx::tma_load_3d(row0 + kHalfBytes, mk, &c.row_full, 64, row, unit);
             }
-            last = item;
+            row_loads = 2;
           }
-          if (!ok) break;
-          q_next(P, list, MODE, n_windows, it);
+          QIter it;
+          q_first(P, list, MODE, MODE == kDkvLong ? chunk * P.chunk_tiles : 0, it);
+          for (int j = m * n_cols; j < (m + 1) * n_cols; ++j) {
+            const PlanTile &tile = q_tile(P, it);
+            for (int kv = 0; kv < 2; ++kv) {
+              const int item = 2 * j + kv, slot = item % kSlots;
+              if (!wt.wait(&c.empty[slot], ((item / kSlots) & 1) ^ 1)) { ok = false; break; }
+              if (item == 0 && (P.flags & BASA_FLAG_TEST_SKIP_FIRST_KEY_LOAD)) {
+                skipped0 = true;
+                last = 0;
+                continue;
+              }
+              uint8_t *dst = smem + kSmemRing + slot * kTileBytes;
+              if (kv == 0) {  // q tile and its records (record buffer j & 1, freed with the q slot)
+                ptx::mbar_arrive_expect_tx(&c.full[slot], uint32_t(tile.valid_rows) * (256u + 16u));
+                load_window_tile(P.plan, P.g, P.map_q, tile, it.org, unit, dst, &c.full[slot]);
+                load_window_records(P.plan, P.g, P.map_rec, tile, it.org, unit, smem + L::rec + (j & 1) * kRecBytes,
+                                    &c.full[slot]);
+              } else {
+                ptx::mbar_arrive_expect_tx(&c.full[slot], uint32_t(tile.valid_rows) * 256u);
+                load_window_tile(P.plan, P.g, P.map_do, tile, it.org, bh, dst, &c.full[slot]);
+              }
+              last = item;
+            }
+            if (!ok) break;
+            q_next(P, list, MODE, n_windows, it);
+          }
         }
       }
       // Drain: wait for the copies still in flight (immediate when all were consumed).
       // A slot's earlier copies completed before the slot was granted again.
-      drain.wait(&c.row_full, 0);
+      drain.wait(&c.row_full, (row_loads - 1) & 1);
       if (MODE == kDq) {
         for (int j = max(0, last_k - 2); j <= last_k; ++j)
           if (j > 0 || !skipped0) drain.wait(&c.full[dq_slot(j, false)], dq_phase(j, false));
@@ -522,11 +558,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
         // is in TMEM. S^T and dP^T stay whole N = 128 products (an N = 64 half reads
         // the same A operand from shared memory for half the work).
         const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
+        // Differential form: tiles [0, n_cols) are map 2's, [n_cols, 2 n_cols) map 1's.
+        const int total = kMaps * n_cols;
         ok = wt.wait(&c.full[0], 0);
         if (ok) {
           ptx::tc_fence_after();
           issue_ss(tS, r0, ringK + slot_of(0));  // S^T(0) = K q0^T
           ptx::mma_commit(&c.s_full[0]);
+          if (kMaps == 2 && n_cols == 1) ptx::mma_commit(&c.row_free);
           ok = wt.wait(&c.full[1], 0);
         }
         if (ok) {
@@ -534,9 +573,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           issue_ss(tDP, r1, ringK + slot_of(1));  // dP^T(0) = V dout0^T
           ptx::mma_commit(&c.dp_full[0]);
         }
-        for (int j = 0; ok && j < n_cols; ++j) {
+        for (int j = 0; ok && j < total; ++j) {
           const int qi = 2 * j, di = 2 * j + 1, qn = qi + 2, dn = di + 2;
-          const bool more = j + 1 < n_cols;
+          const bool more = j + 1 < total;
+          const bool map_start = j == 0 || (kMaps == 2 && j == n_cols);
+          if (kMaps == 2 && j == n_cols) {
+            // both groups have read map 2's dK and rescaled dV before their first P^T
+            ok = wt.wait(&c.p_full[0], j & 1) && wt.wait(&c.p_full[1], j & 1);
+            if (!ok) break;
+          }
           for (int g = 0; ok && g < 2; ++g) {
             ok = wt.wait(&c.p_full[g], j & 1);
             if (!ok) break;
@@ -547,18 +592,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           ptx::mma_commit(&c.empty[di % kSlots]);
           if (more) {
             if (!wt.wait(&c.full[qn % kSlots], (qn / kSlots) & 1)) break;
+            if (kMaps == 2 && j + 1 == n_cols && !wt.wait(&c.row_full, 1)) break;
             ptx::tc_fence_after();
             issue_ss(tS, r0, ringK + slot_of(qn));  // S^T(j+1): P^T(j) has been read by dV
             ptx::mma_commit(&c.s_full[0]);
+            if (kMaps == 2 && j + 2 == n_cols) ptx::mma_commit(&c.row_free);
           }
           for (int g = 0; ok && g < 2; ++g) {
             ok = wt.wait(&c.ds_full[g], j & 1);
             if (!ok) break;
             ptx::tc_fence_after();
-            issue_ts_group(tDK, tDP, ringMn + slot_of(qi), g, j > 0 || g > 0);  // dK += dS^T(j) q_j
+            issue_ts_group(tDK, tDP, ringMn + slot_of(qi), g, !map_start || g > 0);  // dK += dS^T(j) q_j
           }
           if (!ok) break;
           ptx::mma_commit(&c.empty[qi % kSlots]);
+          if (kMaps == 2 && j + 1 == n_cols) ptx::mma_commit(&c.acc_full);  // map 2 is complete
           if (more) {
             if (!wt.wait(&c.full[dn % kSlots], (dn / kSlots) & 1)) break;
             ptx::tc_fence_after();
@@ -655,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
         float x[64];
         tmem_ld64f(tmem + lane_off + 256 + col, x);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) x[i] *= P.scale;
+        for (int i = 0; i < 64; ++i) x[i] *= DIFF && (bh & 1) ? P.scale * neg_lambda : P.scale;
         stage_row_half(row0, row, g, x);  // the q tile is no longer read
         ptx::fence_proxy_async_smem();
       }
@@ -669,129 +717,166 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
       const uint32_t tS = tmem + lane_off + col, tDP = tmem + lane_off + 128 + col;
       float *wrec = reinterpret_cast<float *>(smem + L::col_rec) + (warp - 2) * 128;  // [-L log2 e x 64 | -D x 64]
       const float4 *nl4 = reinterpret_cast<const float4 *>(wrec), *nd4 = reinterpret_cast<const float4 *>(wrec + 64);
-      QIter it;
-      if (n_cols > 0) q_first(P, list, MODE, MODE == kDkvLong ? chunk * P.chunk_tiles : 0, it);
-      for (int j = 0; ok && j < n_cols; ++j) {
-        ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.s_full[0], j & 1));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        float p[64];
-        tmem_ld64f(tS, p);
-        {
-          // This warp's 64 query records {-L log2 e, -D, 0, 0}, one load per lane
-          // for two columns, rewritten as two arrays that the loops below read four
-          // values at a time.
-          const float4 *r = reinterpret_cast<const float4 *>(smem + L::rec + (j & 1) * kRecBytes) + col;
-          const float4 a = r[lane], b = r[32 + lane];
-          __syncwarp();  // every lane has read the previous tile's arrays
-          wrec[lane] = a.x;
-          wrec[32 + lane] = b.x;
-          wrec[64 + lane] = a.y;
-          wrec[96 + lane] = b.y;
-          __syncwarp();
-        }
-        uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
-        if (!P.all_full) {
-          const PlanTile &qt = q_tile(P, it);
-          m0 = qt.mask[2 * g];
-          m1 = qt.mask[2 * g + 1];
-        }
-        const uint64_t sl2x2 = ptx::f2_pack(sl2, sl2);
+      // unrolled: the two maps' epilogues differ (a rolled loop spills over 800 bytes a thread)
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 nl = nl4[i / 4];
-          float x0, x1, x2, x3;
-          ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(p[i], p[i + 1]), sl2x2, ptx::f2_pack(nl.x, nl.y)), x0, x1);
-          ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(p[i + 2], p[i + 3]), sl2x2, ptx::f2_pack(nl.z, nl.w)), x2, x3);
-          p[i] = ptx::ex2(x0);
-          p[i + 1] = ptx::ex2(x1);
-          p[i + 2] = ptx::ex2(x2);
-          p[i + 3] = ptx::ex2(x3);
-        }
-        const bool partial = (m0 & m1) != 0xFFFFFFFFu;  // warp-uniform: a partial query tile
-        if (partial) zero_masked(p, m0, m1);
-        uint32_t pk[32];
-        pack64(p, pk);
-        ptx::tmem_st32(tS, pk);  // P^T (bf16) over the first half of this thread's S^T columns
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&c.p_full[g]);
-        ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.dp_full[0], j & 1));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        float dp[64];
-        tmem_ld64f(tDP, dp);
+      for (int m = 0; m < kMaps; ++m) {
+        QIter it;
+        if (n_cols > 0) q_first(P, list, MODE, MODE == kDkvLong ? chunk * P.chunk_tiles : 0, it);
+        for (int j = m * n_cols; ok && j < (m + 1) * n_cols; ++j) {
+          ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.s_full[0], j & 1));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          float p[64];
+          tmem_ld64f(tS, p);
+          {
+            // This warp's 64 query records {-L log2 e, -D, 0, 0}, one load per lane
+            // for two columns, rewritten as two arrays that the loops below read four
+            // values at a time.
+            const float4 *r = reinterpret_cast<const float4 *>(smem + L::rec + (j & 1) * kRecBytes) + col;
+            const float4 a = r[lane], b = r[32 + lane];
+            __syncwarp();  // every lane has read the previous tile's arrays
+            wrec[lane] = a.x;
+            wrec[32 + lane] = b.x;
+            wrec[64 + lane] = a.y;
+            wrec[96 + lane] = b.y;
+            __syncwarp();
+          }
+          uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
+          if (!P.all_full) {
+            const PlanTile &qt = q_tile(P, it);
+            m0 = qt.mask[2 * g];
+            m1 = qt.mask[2 * g + 1];
+          }
+          const uint64_t sl2x2 = ptx::f2_pack(sl2, sl2);
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 nd = nd4[i / 4];
-          float d0, d1, d2, d3;
-          ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(p[i], p[i + 1]),
-                                    ptx::fadd2(ptx::f2_pack(dp[i], dp[i + 1]), ptx::f2_pack(nd.x, nd.y))),
-                         d0, d1);
-          ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(p[i + 2], p[i + 3]),
-                                    ptx::fadd2(ptx::f2_pack(dp[i + 2], dp[i + 3]), ptx::f2_pack(nd.z, nd.w))),
-                         d2, d3);
-          dp[i] = d0;
-          dp[i + 1] = d1;
-          dp[i + 2] = d2;
-          dp[i + 3] = d3;
+          for (int i = 0; i < 64; i += 4) {
+            const float4 nl = nl4[i / 4];
+            float x0, x1, x2, x3;
+            ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(p[i], p[i + 1]), sl2x2, ptx::f2_pack(nl.x, nl.y)), x0, x1);
+            ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(p[i + 2], p[i + 3]), sl2x2, ptx::f2_pack(nl.z, nl.w)), x2, x3);
+            p[i] = ptx::ex2(x0);
+            p[i + 1] = ptx::ex2(x1);
+            p[i + 2] = ptx::ex2(x2);
+            p[i + 3] = ptx::ex2(x3);
+          }
+          const bool partial = (m0 & m1) != 0xFFFFFFFFu;  // warp-uniform: a partial query tile
+          if (partial) zero_masked(p, m0, m1);
+          uint32_t pk[32];
+          pack64(p, pk);
+          ptx::tmem_st32(tS, pk);  // P^T (bf16) over the first half of this thread's S^T columns
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&c.p_full[g]);
+          ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.dp_full[0], j & 1));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          float dp[64];
+          tmem_ld64f(tDP, dp);
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const float4 nd = nd4[i / 4];
+            float d0, d1, d2, d3;
+            ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(p[i], p[i + 1]),
+                                      ptx::fadd2(ptx::f2_pack(dp[i], dp[i + 1]), ptx::f2_pack(nd.x, nd.y))),
+                           d0, d1);
+            ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(p[i + 2], p[i + 3]),
+                                      ptx::fadd2(ptx::f2_pack(dp[i + 2], dp[i + 3]), ptx::f2_pack(nd.z, nd.w))),
+                           d2, d3);
+            dp[i] = d0;
+            dp[i + 1] = d1;
+            dp[i + 2] = d2;
+            dp[i + 3] = d3;
+          }
+          if (partial) zero_masked(dp, m0, m1);  // dS = 0 there whatever dP holds
+          pack64(dp, pk);
+          ptx::tmem_st32(tDP, pk);  // dS^T (bf16) over the first half of this thread's dP^T columns
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&c.ds_full[g]);
+          q_next(P, list, MODE, n_windows, it);
         }
-        if (partial) zero_masked(dp, m0, m1);  // dS = 0 there whatever dP holds
-        pack64(dp, pk);
-        ptx::tmem_st32(tDP, pk);  // dS^T (bf16) over the first half of this thread's dP^T columns
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&c.ds_full[g]);
-        q_next(P, list, MODE, n_windows, it);
-      }
-      if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.acc_full, 0));
-      if (ok) {
+        if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.acc_full, n_cols > 0 ? m : 0));
+        if (!ok) continue;
         ptx::tc_fence_after();
+        const bool last_map = m + 1 == kMaps;
+        const int unit = map_unit(m);  // of k and dk
+        if (!last_map) {  // map 2's part of dV, before map 1 adds to it
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            ptx::tmem_ld32(tmem + lane_off + 256 + col + 32 * h, r);
+            ptx::tmem_ld_wait(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * neg_lambda);
+            ptx::tmem_st32(tmem + lane_off + 256 + col + 32 * h, r);
+          }
+        }
         float dv[64], dk[64];
         if (n_cols > 0) {
-          tmem_ld64f(tmem + lane_off + 256 + col, dv);
           tmem_ld64f(tmem + lane_off + 384 + col, dk);
+          if (last_map) tmem_ld64f(tmem + lane_off + 256 + col, dv);
         } else {
 #pragma unroll
           for (int i = 0; i < 64; ++i) dv[i] = dk[i] = 0.f;
         }
+        const float dk_scale = last_map ? P.scale : P.scale * neg_lambda;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) dk[i] *= P.scale;
+        for (int i = 0; i < 64; ++i) dk[i] *= dk_scale;
+        if (!last_map) {
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+        }
         if (MODE == kDkvLong) {
-          // partial sums of this chunk, float32 [dK | dV][row][128]
-          float *dst = P.part + ((((long long)bh * P.n_long_tiles + kt) * P.n_chunks + chunk) * 2) * (kTileRows * 128);
-          float4 *pk4 = reinterpret_cast<float4 *>(dst + row * 128 + col);
-          float4 *pv4 = reinterpret_cast<float4 *>(dst + kTileRows * 128 + row * 128 + col);
+          // partial sums of this chunk, float32 [dK of each map | dV][row][128]
+          float *dst = P.part + ((((long long)bh * P.n_long_tiles + kt) * P.n_chunks + chunk) * (kMaps + 1)) * (kTileRows * 128) +
+                       row * 128 + col;
+          float4 *pk4 = reinterpret_cast<float4 *>(dst + (kMaps - 1 - m) * (kTileRows * 128));
+          float4 *pv4 = reinterpret_cast<float4 *>(dst + kMaps * (kTileRows * 128));
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             pk4[i] = make_float4(dk[4 * i], dk[4 * i + 1], dk[4 * i + 2], dk[4 * i + 3]);
-            pv4[i] = make_float4(dv[4 * i], dv[4 * i + 1], dv[4 * i + 2], dv[4 * i + 3]);
+            if (last_map) pv4[i] = make_float4(dv[4 * i], dv[4 * i + 1], dv[4 * i + 2], dv[4 * i + 3]);
           }
         } else {
           int t, y, x;
-          if (P.n_pool > 0 && tile_row_token(P.plan, P.g, row_tile, row_org, row, &t, &y, &x)) {
+          const bool token = (P.n_pool > 0 || !last_map) && tile_row_token(P.plan, P.g, row_tile, row_org, row, &t, &y, &x);
+          if (P.n_pool > 0 && token) {
             // the pooled keys' gradient of this token's patch, spread evenly
             const int pidx = ((t / P.pt) * (P.g.H / P.ph) + y / P.ph) * (P.g.W / P.pw) + x / P.pw;
-            const float4 *gk = reinterpret_cast<const float4 *>(P.dkvp + ((long long)bh * P.n_pool + pidx) * 128 + col);
+            const float4 *gk = reinterpret_cast<const float4 *>(P.dkvp + ((long long)unit * P.n_pool + pidx) * 128 + col);
             const float4 *gv = reinterpret_cast<const float4 *>(
-                P.dkvp + ((long long)(P.bh_count + bh) * P.n_pool + pidx) * 128 + col);
+                P.dkvp + (((long long)kMaps * P.bh_count + bh) * P.n_pool + pidx) * 128 + col);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float4 a = gk[i], b = gv[i];
+              const float4 a = gk[i];
               dk[4 * i] += a.x * P.inv_patch; dk[4 * i + 1] += a.y * P.inv_patch;
               dk[4 * i + 2] += a.z * P.inv_patch; dk[4 * i + 3] += a.w * P.inv_patch;
-              dv[4 * i] += b.x * P.inv_patch; dv[4 * i + 1] += b.y * P.inv_patch;
-              dv[4 * i + 2] += b.z * P.inv_patch; dv[4 * i + 3] += b.w * P.inv_patch;
+              if (last_map) {
+                const float4 b = gv[i];
+                dv[4 * i] += b.x * P.inv_patch; dv[4 * i + 1] += b.y * P.inv_patch;
+                dv[4 * i + 2] += b.z * P.inv_patch; dv[4 * i + 3] += b.w * P.inv_patch;
+              }
             }
           }
-          stage_row_half(row0, row, g, dk);  // the k and v tiles are no longer read
-          stage_row_half(row1, row, g, dv);
-          ptx::fence_proxy_async_smem();
+          if (last_map) {
+            stage_row_half(row0, row, g, dk);  // the k and v tiles are no longer read
+            stage_row_half(row1, row, g, dv);
+            ptx::fence_proxy_async_smem();
+          } else if (token && !*reinterpret_cast<volatile int *>(&c.abort)) {
+            // the key tile's place in shared memory is map 1's already: 128 bytes a thread
+            const long long tok = ((long long)t * P.g.H + y) * P.g.W + x;
+            uint4 *dst = reinterpret_cast<uint4 *>(P.dk + ((long long)unit * (P.g.N + P.n_text) + tok) * 128 + col);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_uint4(ptx::pack_bf16x2(dk[8 * i], dk[8 * i + 1]), ptx::pack_bf16x2(dk[8 * i + 2], dk[8 * i + 3]),
+                                  ptx::pack_bf16x2(dk[8 * i + 4], dk[8 * i + 5]),
+                                  ptx::pack_bf16x2(dk[8 * i + 6], dk[8 * i + 7]));
+          }
         }
       }
       ptx::named_barrier(1, 256);
       if (MODE == kDkvWindow && threadIdx.x == 64 && ok && !*reinterpret_cast<volatile int *>(&c.abort)) {
-        store_window_tile(P.plan, P.g, P.map_dk, row_tile, row_org, bh, row0);
+        store_window_tile(P.plan, P.g, P.map_dk, row_tile, row_org, map_unit(kMaps - 1), row0);
         store_window_tile(P.plan, P.g, P.map_dv, row_tile, row_org, bh, row1);
         ptx::tma_store_commit();
         ptx::tma_store_wait_read_all();
@@ -830,13 +915,16 @@ __global__ void __launch_bounds__(256) bwd_records_kernel(const __nv_bfloat16 *o
 }
 
 // Sums the chunks of the long key tiles in order: pooled rows -> dkvp (float32),
-// text rows -> dk, dv (bf16, rows N.. of each b*head).
+// text rows -> dk, dv (bf16, rows N.. of each b*head). `maps` dK arrays and one dV for
+// each unit of v; a thread sums one of them.
 __global__ void __launch_bounds__(256) bwd_reduce_kernel(const float *part, float *dkvp, __nv_bfloat16 *dk,
-                                                         __nv_bfloat16 *dv, int bh_count, int n_long, int n_chunks,
-                                                         int n_pool, int n_pool_tiles, int n_text, long long N) {
+                                                         __nv_bfloat16 *dv, int bh_count, int maps, int n_long,
+                                                         int n_chunks, int n_pool, int n_pool_tiles, int n_text,
+                                                         long long N) {
   const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;  // (bh, tile, row, 4-column group)
   const long long total = (long long)bh_count * n_long * kTileRows * 32;
   if (idx >= total) return;
+  const int which = blockIdx.y;  // dK of map `which`, or dV
   const int c4 = int(idx % 32);
   const int row = int((idx / 32) % kTileRows);
   const int tile = int((idx / (32 * kTileRows)) % n_long);
@@ -844,28 +932,27 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(const float *part, floa
   const bool pooled = tile < n_pool_tiles;
   const int r = (pooled ? tile : tile - n_pool_tiles) * kTileRows + row;
   if (r >= (pooled ? n_pool : n_text)) return;
-  float4 sk = make_float4(0.f, 0.f, 0.f, 0.f), sv = sk;
-  const float *base = part + (((long long)bh * n_long + tile) * n_chunks) * 2 * (kTileRows * 128);
-  for (int ch = 0; ch < n_chunks; ++ch) {
-    const float *p = base + (long long)ch * 2 * (kTileRows * 128) + row * 128 + c4 * 4;
+  const long long step = (long long)(maps + 1) * (kTileRows * 128);
+  const float *p = part + (((long long)bh * n_long + tile) * n_chunks) * step + which * (kTileRows * 128) + row * 128 + c4 * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int ch = 0; ch < n_chunks; ++ch, p += step) {
     const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + kTileRows * 128);
-    sk.x += a.x; sk.y += a.y; sk.z += a.z; sk.w += a.w;
-    sv.x += b.x; sv.y += b.y; sv.z += b.z; sv.w += b.w;
+    s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
   }
+  const bool is_v = which == maps;
+  const long long unit = is_v ? bh : (long long)maps * bh + which;
   if (pooled) {
-    *reinterpret_cast<float4 *>(dkvp + ((long long)bh * n_pool + r) * 128 + c4 * 4) = sk;
-    *reinterpret_cast<float4 *>(dkvp + ((long long)bh_count * n_pool + (long long)bh * n_pool + r) * 128 + c4 * 4) = sv;
+    const long long at = (is_v ? (long long)maps * bh_count : 0) + unit;
+    *reinterpret_cast<float4 *>(dkvp + (at * n_pool + r) * 128 + c4 * 4) = s;
   } else {
-    const long long o = ((long long)bh * (N + n_text) + N + r) * 128 + c4 * 4;
-    reinterpret_cast<uint2 *>(dk + o)[0] = make_uint2(ptx::pack_bf16x2(sk.x, sk.y), ptx::pack_bf16x2(sk.z, sk.w));
-    reinterpret_cast<uint2 *>(dv + o)[0] = make_uint2(ptx::pack_bf16x2(sv.x, sv.y), ptx::pack_bf16x2(sv.z, sv.w));
+    const long long o = (unit * (N + n_text) + N + r) * 128 + c4 * 4;
+    reinterpret_cast<uint2 *>((is_v ? dv : dk) + o)[0] = make_uint2(ptx::pack_bf16x2(s.x, s.y), ptx::pack_bf16x2(s.z, s.w));
   }
 }
 
 // ----------------------------------------------------------------- host side
 struct BwdLayout {
-  size_t rec, part, dkvp, total;
+  size_t rec, part, dkvp, total;  // of `maps` maps for each unit of v
   int n_long, n_chunks, chunk_tiles, q_tiles;
 };
 
@@ -890,7 +977,7 @@ int head_query_tiles(const basa_params &p, const WindowPlan &plan) {
 // the chunk sums (hence the bits of the results) are the same on every device.
 constexpr long long kLongSms = 148;
 constexpr double kLongCtaCostTiles = 3.5;
-BwdLayout bwd_layout(const basa_params &p, const WindowPlan &plan) {
+BwdLayout bwd_layout(const basa_params &p, const WindowPlan &plan, int maps) {
   BwdLayout L{};
   const long long bh = (long long)p.B * p.heads;
   const long long N = (long long)p.T * p.H * p.W;
@@ -913,63 +1000,56 @@ BwdLayout bwd_layout(const basa_params &p, const WindowPlan &plan) {
       }
     }
   }
-  L.rec = align256(size_t(bh) * N * 16);
-  L.part = align256(size_t(bh) * L.n_long * L.n_chunks * 2 * kTileRows * 128 * sizeof(float));
-  L.dkvp = align256(size_t(bh) * n_pool * 128 * sizeof(float) * 2);
+  L.rec = align256(size_t(maps) * bh * N * 16);
+  L.part = align256(size_t(bh) * L.n_long * L.n_chunks * (maps + 1) * kTileRows * 128 * sizeof(float));
+  L.dkvp = align256(size_t(bh) * n_pool * 128 * sizeof(float) * (maps + 1));
   L.total = L.rec + L.part + L.dkvp;
   return L;
 }
 
-template <int MODE>
+template <int MODE, bool DIFF>
 basa_status run_bwd(const BwdParams &P, long long blocks, cudaStream_t s) {
   if (blocks <= 0) return BASA_OK;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(attn_bwd_bf16_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<MODE>::bytes) !=
-      cudaSuccess)
+  if (cudaFuncSetAttribute(attn_bwd_bf16_kernel<MODE, DIFF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Smem<MODE>::bytes) != cudaSuccess)
     return BASA_ERR_CUDA;
-  attn_bwd_bf16_kernel<MODE><<<unsigned(blocks), kThreads, Smem<MODE>::bytes, s>>>(P);
+  attn_bwd_bf16_kernel<MODE, DIFF><<<unsigned(blocks), kThreads, Smem<MODE>::bytes, s>>>(P);
   return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
 }
 
-}  // namespace
-
-size_t attn_bwd_bf16_workspace(const basa_params &p) {
-  static thread_local WindowPlan plan;  // large: kept off the stack
-  if (build_window_plan(p, &plan) != BASA_OK) return 0;
-  return bwd_layout(p, plan).total;
-}
-
-basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
-                                 const int32_t *route_idx, const void *out, const float *lse, const void *dout,
-                                 void *dq, void *dk, void *dv, void *workspace, const basa_params &p, cudaStream_t s) {
+// Parameters of a backward over p.heads units of v with `maps` maps each; the
+// workspace starts with a BwdLayout (records, partial sums, pooled gradients).
+basa_status bwd_params(BwdParams &P, BwdLayout &L, const void *q, const void *k, const void *v, const void *kp,
+                       const void *vp, const int32_t *route_idx, const void *dout, void *dq, void *dk, void *dv,
+                       void *workspace, const basa_params &p, int maps) {
   if (!tensor_map_encoder()) return BASA_ERR_CUDA;
-  static thread_local BwdParams P;  // large: kept off the stack
   std::memset(&P, 0, sizeof(P));
   basa_status st = build_window_plan(p, &P.plan);
   if (st != BASA_OK) return st;
-  const BwdLayout L = bwd_layout(p, P.plan);
+  L = bwd_layout(p, P.plan, maps);
   P.g = make_geo(p);
   if (p.routed_k > 0 && P.g.nWin > kMaxList) return BASA_ERR_UNSUPPORTED;
   const long long N = P.g.N, kv_rows = N + p.n_text, bh = (long long)p.B * p.heads;
+  basa_params pm = p;
+  pm.heads = p.heads * maps;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  float4 *rec = reinterpret_cast<float4 *>(ws);
+  P.rec = reinterpret_cast<const float4 *>(ws);
   P.part = reinterpret_cast<float *>(ws + L.rec);
-  float *dkvp = reinterpret_cast<float *>(ws + L.rec + L.part);
-  P.dkvp = dkvp;
-  P.rec = rec;
+  P.dkvp = reinterpret_cast<const float *>(ws + L.rec + L.part);
   for (int i = 0; i < P.plan.n_shapes; ++i) {
     const PlanShape &sh = P.plan.shape[i];
-    if (!encode_grid_map(&P.map_q[i], q, p, N, sh) || !encode_grid_map(&P.map_k[i], k, p, kv_rows, sh) ||
+    if (!encode_grid_map(&P.map_q[i], q, pm, N, sh) || !encode_grid_map(&P.map_k[i], k, pm, kv_rows, sh) ||
         !encode_grid_map(&P.map_v[i], v, p, kv_rows, sh) || !encode_grid_map(&P.map_do[i], dout, p, N, sh) ||
-        !encode_record_map(&P.map_rec[i], rec, p, sh) || !encode_grid_map(&P.map_dq[i], dq, p, N, sh) ||
-        !encode_grid_map(&P.map_dk[i], dk, p, kv_rows, sh) || !encode_grid_map(&P.map_dv[i], dv, p, kv_rows, sh))
+        !encode_record_map(&P.map_rec[i], ws, pm, sh) || !encode_grid_map(&P.map_dq[i], dq, pm, N, sh) ||
+        !encode_grid_map(&P.map_dk[i], dk, pm, kv_rows, sh) || !encode_grid_map(&P.map_dv[i], dv, p, kv_rows, sh))
       return BASA_ERR_CUDA;
   }
   P.n_pool = p.pt > 0 ? (p.T / p.pt) * (p.H / p.ph) * (p.W / p.pw) : 0;
   P.n_text = p.n_text;
-  if (P.n_pool > 0 && (!encode_rows_map(&P.map_kp, kp, p, P.n_pool) || !encode_rows_map(&P.map_vp, vp, p, P.n_pool)))
+  if (P.n_pool > 0 && (!encode_rows_map(&P.map_kp, kp, pm, P.n_pool) || !encode_rows_map(&P.map_vp, vp, p, P.n_pool)))
     return BASA_ERR_CUDA;
-  if (p.n_text > 0 && (!encode_rows_map(&P.map_kt, k, p, kv_rows) || !encode_rows_map(&P.map_vt, v, p, kv_rows)))
+  if (p.n_text > 0 && (!encode_rows_map(&P.map_kt, k, pm, kv_rows) || !encode_rows_map(&P.map_vt, v, p, kv_rows)))
     return BASA_ERR_CUDA;
   P.n_pool_tiles = (P.n_pool + kTileRows - 1) / kTileRows;
   P.n_text_tiles = (p.n_text + kTileRows - 1) / kTileRows;
@@ -993,22 +1073,80 @@ basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, co
   P.q_tiles = L.q_tiles;
   P.timeout_ns = (p.wait_timeout_us ? (unsigned long long)p.wait_timeout_us : 2000000ull) * 1000ull;
   P.flags = p.flags;
+  return BASA_OK;
+}
 
-  const long long rows = bh * N;
-  bwd_records_kernel<<<unsigned((rows + 15) / 16), 256, 0, s>>>(
-      static_cast<const __nv_bfloat16 *>(out), static_cast<const __nv_bfloat16 *>(dout), lse, rec, rows);
-  if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
-  const long long window_blocks = bh * P.g.nWin * P.max_tiles;
-  if ((st = run_bwd<kDq>(P, window_blocks, s)) != BASA_OK) return st;
+// The passes after the records: dq, pooled and text dK/dV, their chunks' sums, window dK/dV.
+template <bool DIFF>
+basa_status run_passes(const BwdParams &P, const BwdLayout &L, void *dk, void *dv, const basa_params &p, cudaStream_t s) {
+  constexpr int maps = DIFF ? 2 : 1;
+  const long long bh = P.bh_count, window_blocks = bh * P.g.nWin * P.max_tiles;
+  basa_status st = run_bwd<kDq, DIFF>(P, maps * window_blocks, s);
+  if (st != BASA_OK) return st;
   if (L.n_long > 0) {
-    if ((st = run_bwd<kDkvLong>(P, bh * L.n_long * L.n_chunks, s)) != BASA_OK) return st;
+    if ((st = run_bwd<kDkvLong, DIFF>(P, bh * L.n_long * L.n_chunks, s)) != BASA_OK) return st;
     const long long threads = bh * L.n_long * kTileRows * 32;
-    bwd_reduce_kernel<<<unsigned((threads + 255) / 256), 256, 0, s>>>(
-        P.part, dkvp, static_cast<__nv_bfloat16 *>(dk), static_cast<__nv_bfloat16 *>(dv), int(bh), L.n_long,
-        L.n_chunks, P.n_pool, P.n_pool_tiles, p.n_text, N);
+    bwd_reduce_kernel<<<dim3(unsigned((threads + 255) / 256), maps + 1), 256, 0, s>>>(
+        P.part, const_cast<float *>(P.dkvp), static_cast<__nv_bfloat16 *>(dk), static_cast<__nv_bfloat16 *>(dv), int(bh),
+        maps, L.n_long, L.n_chunks, P.n_pool, P.n_pool_tiles, p.n_text, P.g.N);
     if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
   }
-  return run_bwd<kDkvWindow>(P, window_blocks, s);
+  return run_bwd<kDkvWindow, DIFF>(P, window_blocks, s);
+}
+
+}  // namespace
+
+size_t attn_bwd_bf16_workspace(const basa_params &p) {
+  static thread_local WindowPlan plan;  // large: kept off the stack
+  if (build_window_plan(p, &plan) != BASA_OK) return 0;
+  return bwd_layout(p, plan, 1).total;
+}
+
+basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                                 const int32_t *route_idx, const void *out, const float *lse, const void *dout,
+                                 void *dq, void *dk, void *dv, void *workspace, const basa_params &p, cudaStream_t s) {
+  static thread_local BwdParams P;  // large: kept off the stack
+  BwdLayout L;
+  basa_status st = bwd_params(P, L, q, k, v, kp, vp, route_idx, dout, dq, dk, dv, workspace, p, 1);
+  if (st != BASA_OK) return st;
+  const long long rows = (long long)P.bh_count * P.g.N;
+  bwd_records_kernel<<<unsigned((rows + 15) / 16), 256, 0, s>>>(
+      static_cast<const __nv_bfloat16 *>(out), static_cast<const __nv_bfloat16 *>(dout), lse,
+      static_cast<float4 *>(workspace), rows);
+  if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
+  return run_passes<false>(P, L, dk, dv, p, s);
+}
+
+// Differential form: the layout of two maps, then g (with a norm), then the partial sums
+// of dlambda and dweight.
+size_t diff_attn_bwd_bf16_workspace(bool norm, const basa_params &p) {
+  static thread_local WindowPlan plan;
+  if (build_window_plan(p, &plan) != BASA_OK) return 0;
+  const size_t g = norm ? align256(size_t(p.B) * p.heads * p.T * p.H * p.W * p.head_dim * 2) : 0;
+  return bwd_layout(p, plan, 2).total + g + align256(diff_prep_workspace(p));
+}
+
+basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                                      const int32_t *route_idx, const basa_diff_params &dp, const void *pre,
+                                      const void *second, const float *lse, const void *dout, void *dq, void *dk,
+                                      void *dv, void *dlambda, void *dweight, void *workspace, const basa_params &p,
+                                      cudaStream_t s) {
+  static thread_local BwdParams P;
+  static thread_local WindowPlan plan;
+  basa_status st = build_window_plan(p, &plan);
+  if (st != BASA_OK) return st;
+  uint8_t *ws = static_cast<uint8_t *>(workspace), *g = ws + bwd_layout(p, plan, 2).total, *part = g;
+  if (dp.weight) part += align256(size_t(p.B) * p.heads * p.T * p.H * p.W * p.head_dim * 2);
+  const void *grad = dp.weight ? g : dout;
+  BwdLayout L;
+  if ((st = bwd_params(P, L, q, k, v, kp, vp, route_idx, grad, dq, dk, dv, ws, p, 2)) != BASA_OK) return st;
+  P.lambda = static_cast<const __nv_bfloat16 *>(dp.lambda);
+  P.heads = p.heads;
+  P.dk = static_cast<__nv_bfloat16 *>(dk);
+  st = launch_diff_prep(pre, second, lse, dout, dp, g, reinterpret_cast<float4 *>(ws), nullptr, dlambda, dweight,
+                        reinterpret_cast<float *>(part), p, s);
+  if (st != BASA_OK) return st;
+  return run_passes<true>(P, L, dk, dv, p, s);
 }
 
 }  // namespace basa

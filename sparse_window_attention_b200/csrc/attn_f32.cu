@@ -22,6 +22,7 @@ struct F32Args {
   Geo g;
   int heads, d, n_text, n_pool, routed_k, win_tok, q_chunks;
   int n_vis_keys, n_pool_keys, n_text_keys;  // keys taken from each group (0 = group not selected)
+  int v_shift;  // v, vp and the routes belong to unit bh >> v_shift (maps that share their values)
   int dense;  // text-query rows: queries are q_text rows, keys are all N + n_text rows of k, v
   float scale;
 };
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(F32Args a) {
   const long long bh = blockIdx.x / (a.q_chunks * n_win);
   if (threadIdx.x == 0) wins[0] = w;
   if (!a.dense && threadIdx.x > 0 && threadIdx.x <= a.routed_k)
-    wins[threadIdx.x] = checked_route(a, a.route[(bh * a.g.nWin + w) * a.routed_k + threadIdx.x - 1], w);
+    wins[threadIdx.x] = checked_route(a, a.route[((bh >> a.v_shift) * a.g.nWin + w) * a.routed_k + threadIdx.x - 1], w);
   __syncthreads();
 
   const int half = threadIdx.x % TPQ;
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(F32Args a) {
       float4 kv4 = make_float4(0.f, 0.f, 0.f, 0.f), vv4 = kv4;
       if (k0 + r < nk) {
         kv4 = reinterpret_cast<const float4 *>(key_row(a, a.k, a.kp, bh, wins, k0 + r))[c4];
-        vv4 = reinterpret_cast<const float4 *>(key_row(a, a.v, a.vp, bh, wins, k0 + r))[c4];
+        vv4 = reinterpret_cast<const float4 *>(key_row(a, a.v, a.vp, bh >> a.v_shift, wins, k0 + r))[c4];
       }
       reinterpret_cast<float4 *>(&ks[r][0])[c4] = kv4;
       reinterpret_cast<float4 *>(&vs[r][0])[c4] = vv4;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(F32Args a) {
 
 basa_status launch_attn_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                             const int32_t *route_idx, void *out, float *lse, uint32_t keys, const basa_params &p,
-                            cudaStream_t s) {
+                            cudaStream_t s, int v_shift) {
   F32Args a{};
   a.q = static_cast<const float *>(q);
   a.k = static_cast<const float *>(k);
@@ -165,6 +166,7 @@ basa_status launch_attn_f32(const void *q, const void *k, const void *v, const v
   a.routed_k = p.routed_k;
   a.win_tok = p.wt * p.wh * p.ww;
   a.lse = lse;
+  a.v_shift = v_shift;
   a.n_vis_keys = (keys & BASA_KEYS_WINDOWS) ? a.win_tok * (1 + a.routed_k) : 0;
   a.n_pool_keys = (keys & BASA_KEYS_POOLED) ? a.n_pool : 0;
   a.n_text_keys = (keys & BASA_KEYS_TEXT) ? a.n_text : 0;
@@ -179,8 +181,9 @@ basa_status launch_attn_f32(const void *q, const void *k, const void *v, const v
 }
 
 basa_status launch_attn_text_f32(const void *q_text, const void *k, const void *v, void *out_text,
-                                 const basa_params &p, cudaStream_t s) {
+                                 const basa_params &p, cudaStream_t s, int v_shift) {
   F32Args a{};
+  a.v_shift = v_shift;
   a.q = static_cast<const float *>(q_text);
   a.k = static_cast<const float *>(k);
   a.v = static_cast<const float *>(v);
@@ -216,6 +219,8 @@ constexpr int kBwdKeyTile = 16;
 struct BwdArgs {
   F32Args f;  // q, k, v, kp, vp, route and geometry as in the forward
   const float *out, *lse, *dout;
+  const float *drow;    // differential form: D of each row instead of dout . out
+  const float *lambda;  // differential form: odd maps count -lambda[head]; heads = f.heads / 2
   float *dq, *dk, *dv, *dkp, *dvp;
 };
 
@@ -243,9 +248,10 @@ __device__ __forceinline__ long long key_dest(const F32Args &a, long long bh, co
   return bh * rows + a.g.N + j;
 }
 
+template <int D>
 __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
   const F32Args &a = b.f;
-  constexpr int D = 128, C = D / kBwdTPQ, QPB = kBwdThreads / kBwdTPQ;
+  constexpr int C = D / kBwdTPQ, QPB = kBwdThreads / kBwdTPQ;
   __shared__ float ks[kBwdKeyTile][D], vs[kBwdKeyTile][D];
   __shared__ float dks[kBwdKeyTile][D], dvs[kBwdKeyTile][D];
   __shared__ int wins[1 + kMaxRouted];
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
   const long long bh = blockIdx.x / (a.q_chunks * a.g.nWin);
   if (threadIdx.x == 0) wins[0] = w;
   if (threadIdx.x > 0 && threadIdx.x <= a.routed_k)
-    wins[threadIdx.x] = checked_route(a, a.route[(bh * a.g.nWin + w) * a.routed_k + threadIdx.x - 1], w);
+    wins[threadIdx.x] = checked_route(a, a.route[((bh >> a.v_shift) * a.g.nWin + w) * a.routed_k + threadIdx.x - 1], w);
   __syncthreads();
   const int part = threadIdx.x % kBwdTPQ;  // columns part, part + TPQ, ...
   const int lq = chunk * QPB + threadIdx.x / kBwdTPQ;
@@ -266,20 +272,23 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
     const int lt = lq / (a.g.wh * a.g.ww), ly = (lq / a.g.ww) % a.g.wh, lx = lq % a.g.ww;
     qtok = ((long long)((ot + lt) % a.g.T) * a.g.H + (oy + ly) % a.g.H) * a.g.W + (ox + lx) % a.g.W;
   }
-  const long long qrow = bh * a.g.N + qtok;
+  const long long qrow = bh * a.g.N + qtok, grow = (bh >> a.v_shift) * a.g.N + qtok;
+  // what this map's dq, dK and dV are multiplied by
+  const float factor = b.lambda && (bh & 1) ? -b.lambda[(bh >> 1) % (a.heads >> 1)] : 1.f;
   float q[C], dout[C], dq[C];
   float Dpart = 0.f;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int col = i * kBwdTPQ + part;
     q[i] = active ? a.q[qrow * D + col] : 0.f;
-    dout[i] = active ? b.dout[qrow * D + col] : 0.f;
-    Dpart = fmaf(dout[i], active ? b.out[qrow * D + col] : 0.f, Dpart);
+    dout[i] = active ? b.dout[grow * D + col] : 0.f;
+    if (!b.drow) Dpart = fmaf(dout[i], active ? b.out[qrow * D + col] : 0.f, Dpart);
     dq[i] = 0.f;
   }
   // the TPQ threads of a query are adjacent lanes
   float Drow = Dpart + __shfl_xor_sync(0xffffffffu, Dpart, 1);
   Drow += __shfl_xor_sync(0xffffffffu, Drow, 2);
+  if (b.drow) Drow = active ? b.drow[qrow] : 0.f;
   const float L = active ? b.lse[qrow] : 0.f;
   const int nk = a.n_vis_keys + a.n_pool_keys + a.n_text_keys;
   for (int k0 = 0; k0 < nk; k0 += kBwdKeyTile) {
@@ -289,7 +298,7 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
       float4 kv4 = make_float4(0.f, 0.f, 0.f, 0.f), vv4 = kv4;
       if (k0 + r < nk) {
         kv4 = reinterpret_cast<const float4 *>(key_row(a, a.k, a.kp, bh, wins, k0 + r))[c4];
-        vv4 = reinterpret_cast<const float4 *>(key_row(a, a.v, a.vp, bh, wins, k0 + r))[c4];
+        vv4 = reinterpret_cast<const float4 *>(key_row(a, a.v, a.vp, bh >> a.v_shift, wins, k0 + r))[c4];
       }
       reinterpret_cast<float4 *>(&ks[r][0])[c4] = kv4;
       reinterpret_cast<float4 *>(&vs[r][0])[c4] = vv4;
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
       const float ds = p * (dpp - Drow);
       // the 8 queries of a warp add to the same key row: sum them with shuffles
       // (lanes l, l ^ 4, l ^ 8, l ^ 16 share a column) and let 4 lanes add to shared memory
-      const float dsq = active ? ds * a.scale : 0.f, pa = active ? p : 0.f;
+      const float dsq = active ? ds * a.scale * factor : 0.f, pa = active ? p * factor : 0.f;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const int col = i * kBwdTPQ + part;
@@ -337,20 +346,20 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
       if (k0 + r >= nk) continue;
       bool pooled;
       const long long dst = key_dest(a, bh, wins, k0 + r, &pooled);
+      const long long dst_v = a.v_shift ? key_dest(a, bh >> a.v_shift, wins, k0 + r, &pooled) : dst;
       atomicAdd((pooled ? b.dkp : b.dk) + dst * D + col, dks[r][col]);
-      atomicAdd((pooled ? b.dvp : b.dv) + dst * D + col, dvs[r][col]);
+      atomicAdd((pooled ? b.dvp : b.dv) + dst_v * D + col, dvs[r][col]);
     }
   }
   if (active) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) b.dq[qrow * D + i * kBwdTPQ + part] = dq[i] * a.scale;
+    for (int i = 0; i < C; ++i) b.dq[qrow * D + i * kBwdTPQ + part] = dq[i] * (a.scale * factor);
   }
 }
 
-// dk, dv of every visual token += dkp, dvp of its pool patch / |patch|.
-__global__ void __launch_bounds__(256) pool_bwd_kernel(const float *dkp, const float *dvp, float *dk, float *dv,
-                                                       Geo g, int pt, int ph, int pw, int n_pool, int n_text, int d,
-                                                       long long total, float inv) {
+// dx (dk or dv) of every visual token += dxp of its pool patch / |patch|.
+__global__ void __launch_bounds__(256) pool_bwd_kernel(const float *dxp, float *dx, Geo g, int pt, int ph, int pw,
+                                                       int n_pool, int n_text, int d, long long total, float inv) {
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;  // (bh, token, float4 column)
   if (i >= total) return;
   const int d4 = d / 4;
@@ -360,24 +369,20 @@ __global__ void __launch_bounds__(256) pool_bwd_kernel(const float *dkp, const f
   const long long P = ((long long)(t / pt) * (g.H / ph) + y / ph) * (g.W / pw) + x / pw;
   const long long src = (bh * n_pool + P) * d4 + c4;
   const long long dst = (bh * ((long long)g.N + n_text) + tok) * d4 + c4;
-  const float4 a = reinterpret_cast<const float4 *>(dkp)[src], b2 = reinterpret_cast<const float4 *>(dvp)[src];
-  float4 &k4 = reinterpret_cast<float4 *>(dk)[dst];
-  float4 &v4 = reinterpret_cast<float4 *>(dv)[dst];
-  k4.x += a.x * inv; k4.y += a.y * inv; k4.z += a.z * inv; k4.w += a.w * inv;
-  v4.x += b2.x * inv; v4.y += b2.y * inv; v4.z += b2.z * inv; v4.w += b2.w * inv;
+  const float4 a = reinterpret_cast<const float4 *>(dxp)[src];
+  float4 &x4 = reinterpret_cast<float4 *>(dx)[dst];
+  x4.x += a.x * inv; x4.y += a.y * inv; x4.z += a.z * inv; x4.w += a.w * inv;
 }
 
 }  // namespace
 
-size_t attn_bwd_workspace(const basa_params &p) {
-  const size_t n_pool = p.pt > 0 ? size_t(p.T / p.pt) * (p.H / p.ph) * (p.W / p.pw) : 0;
-  return 2 * size_t(p.B) * p.heads * n_pool * p.head_dim * sizeof(float);
-}
+namespace {
 
-basa_status launch_attn_bwd_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
-                                const int32_t *route_idx, const void *out, const float *lse, const void *dout,
-                                void *dq, void *dk, void *dv, void *workspace, const basa_params &p, cudaStream_t s) {
-  BwdArgs b{};
+// The backward over `maps` = p.heads x B units whose values are shared in groups of
+// 2^v_shift; `pooled` holds the pooled keys' gradients, then the pooled values'.
+basa_status run_attn_bwd_f32(BwdArgs b, const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                             const int32_t *route_idx, void *dq, void *dk, void *dv, float *pooled,
+                             const basa_params &p, int v_shift, cudaStream_t s) {
   F32Args &a = b.f;
   a.q = static_cast<const float *>(q);
   a.k = static_cast<const float *>(k);
@@ -396,32 +401,119 @@ basa_status launch_attn_bwd_f32(const void *q, const void *k, const void *v, con
   a.n_vis_keys = a.win_tok * (1 + a.routed_k);
   a.n_pool_keys = a.n_pool;
   a.n_text_keys = p.n_text;
+  a.v_shift = v_shift;
   a.q_chunks = (a.win_tok + kBwdThreads / kBwdTPQ - 1) / (kBwdThreads / kBwdTPQ);
   a.scale = 1.0f / sqrtf(float(p.head_dim));
-  b.out = static_cast<const float *>(out);
-  b.lse = lse;
-  b.dout = static_cast<const float *>(dout);
   b.dq = static_cast<float *>(dq);
   b.dk = static_cast<float *>(dk);
   b.dv = static_cast<float *>(dv);
-  b.dkp = static_cast<float *>(workspace);
-  b.dvp = b.dkp + size_t(p.B) * p.heads * a.n_pool * p.head_dim;
-  const size_t kv_bytes = size_t(p.B) * p.heads * (size_t(a.g.N) + p.n_text) * p.head_dim * sizeof(float);
-  if (cudaMemsetAsync(dk, 0, kv_bytes, s) != cudaSuccess || cudaMemsetAsync(dv, 0, kv_bytes, s) != cudaSuccess)
+  const size_t bh = size_t(p.B) * p.heads, bh_v = bh >> v_shift;
+  b.dkp = pooled;
+  b.dvp = b.dkp + bh * a.n_pool * p.head_dim;
+  const size_t unit_bytes = (size_t(a.g.N) + p.n_text) * p.head_dim * sizeof(float);
+  if (cudaMemsetAsync(dk, 0, bh * unit_bytes, s) != cudaSuccess ||
+      cudaMemsetAsync(dv, 0, bh_v * unit_bytes, s) != cudaSuccess)
     return BASA_ERR_CUDA;
-  if (a.n_pool > 0 && cudaMemsetAsync(workspace, 0, attn_bwd_workspace(p), s) != cudaSuccess) return BASA_ERR_CUDA;
-  const long long blocks = (long long)p.B * p.heads * a.g.nWin * a.q_chunks;
+  if (a.n_pool > 0 &&
+      cudaMemsetAsync(pooled, 0, (bh + bh_v) * a.n_pool * p.head_dim * sizeof(float), s) != cudaSuccess)
+    return BASA_ERR_CUDA;
+  const long long blocks = (long long)bh * a.g.nWin * a.q_chunks;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  attn_bwd_f32_kernel<<<unsigned(blocks), kBwdThreads, 0, s>>>(b);
+  if (p.head_dim == 64) attn_bwd_f32_kernel<64><<<unsigned(blocks), kBwdThreads, 0, s>>>(b);
+  else attn_bwd_f32_kernel<128><<<unsigned(blocks), kBwdThreads, 0, s>>>(b);
   if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
-  if (a.n_pool > 0) {
-    const long long total = (long long)p.B * p.heads * a.g.N * (p.head_dim / 4);
-    pool_bwd_kernel<<<unsigned((total + 255) / 256), 256, 0, s>>>(b.dkp, b.dvp, b.dk, b.dv, a.g, p.pt, p.ph, p.pw,
-                                                                 a.n_pool, p.n_text, p.head_dim, total,
+  for (int i = 0; a.n_pool > 0 && i < 2; ++i) {
+    const long long total = (long long)(i ? bh_v : bh) * a.g.N * (p.head_dim / 4);
+    pool_bwd_kernel<<<unsigned((total + 255) / 256), 256, 0, s>>>(i ? b.dvp : b.dkp, i ? b.dv : b.dk, a.g, p.pt, p.ph,
+                                                                 p.pw, a.n_pool, p.n_text, p.head_dim, total,
                                                                  1.0f / float(p.pt * p.ph * p.pw));
     if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
   }
   return BASA_OK;
+}
+
+size_t pooled_grad_bytes(const basa_params &p, int units) {
+  const size_t n_pool = p.pt > 0 ? size_t(p.T / p.pt) * (p.H / p.ph) * (p.W / p.pw) : 0;
+  return size_t(units) * n_pool * p.head_dim * sizeof(float);
+}
+
+}  // namespace
+
+size_t attn_bwd_workspace(const basa_params &p) { return pooled_grad_bytes(p, 2 * p.B * p.heads); }
+
+basa_status launch_attn_bwd_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                                const int32_t *route_idx, const void *out, const float *lse, const void *dout,
+                                void *dq, void *dk, void *dv, void *workspace, const basa_params &p, cudaStream_t s) {
+  BwdArgs b{};
+  b.out = static_cast<const float *>(out);
+  b.lse = lse;
+  b.dout = static_cast<const float *>(dout);
+  return run_attn_bwd_f32(b, q, k, v, kp, vp, route_idx, dq, dk, dv, static_cast<float *>(workspace), p, 0, s);
+}
+
+// ----------------------------------------------------------------- differential form
+// The maps by themselves (q, k of 2 heads maps, the values of each pair shared), then
+// their difference and norm in one pass over the float32 map outputs.
+size_t diff_f32_workspace(const basa_params &p, long long rows) {
+  return 2 * size_t(p.B) * p.heads * rows * p.head_dim * sizeof(float);
+}
+
+basa_status launch_diff_attn_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                                 const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
+                                 void *second, float *lse, void *workspace, const basa_params &p, cudaStream_t s) {
+  basa_params pm = p;
+  pm.heads = 2 * p.heads;
+  basa_status st = launch_attn_f32(q, k, v, kp, vp, route_idx, workspace, lse, BASA_KEYS_ALL, pm, s, 1);
+  if (st != BASA_OK) return st;
+  return launch_diff_combine(1, static_cast<const float *>(workspace), nullptr, (long long)p.T * p.H * p.W, dp, out, pre,
+                             second, p, s);
+}
+
+basa_status launch_diff_text_f32(const void *q_text, const void *k, const void *v, const basa_diff_params &dp,
+                                 void *out_text, void *workspace, const basa_params &p, cudaStream_t s) {
+  basa_params pm = p;
+  pm.heads = 2 * p.heads;
+  basa_status st = launch_attn_text_f32(q_text, k, v, workspace, pm, s, 1);
+  if (st != BASA_OK) return st;
+  return launch_diff_combine(1, static_cast<const float *>(workspace), nullptr, p.n_text, dp, out_text, nullptr, nullptr,
+                             p, s);
+}
+
+namespace {
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+}  // namespace
+
+// Workspace: pooled gradients, D of each map's rows, g (with a norm), partial sums.
+size_t diff_attn_bwd_f32_workspace(bool norm, const basa_params &p) {
+  const size_t rows = size_t(p.B) * p.heads * p.T * p.H * p.W;
+  return align256(pooled_grad_bytes(p, 3 * p.B * p.heads)) + align256(2 * rows * sizeof(float)) +
+         (norm ? align256(rows * p.head_dim * sizeof(float)) : 0) + align256(diff_prep_workspace(p));
+}
+
+basa_status launch_diff_attn_bwd_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                                     const int32_t *route_idx, const basa_diff_params &dp, const void *pre,
+                                     const void *second, const float *lse, const void *dout, void *dq, void *dk,
+                                     void *dv, void *dlambda, void *dweight, void *workspace, const basa_params &p,
+                                     cudaStream_t s) {
+  const size_t rows = size_t(p.B) * p.heads * p.T * p.H * p.W;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  float *pooled = reinterpret_cast<float *>(ws);
+  ws += align256(pooled_grad_bytes(p, 3 * p.B * p.heads));
+  float *drow = reinterpret_cast<float *>(ws);
+  ws += align256(2 * rows * sizeof(float));
+  float *g = reinterpret_cast<float *>(ws);
+  if (dp.weight) ws += align256(rows * p.head_dim * sizeof(float));
+  basa_status st = launch_diff_prep(pre, second, lse, dout, dp, g, nullptr, drow, dlambda, dweight,
+                                    reinterpret_cast<float *>(ws), p, s);
+  if (st != BASA_OK) return st;
+  BwdArgs b{};
+  b.lse = lse;
+  b.dout = dp.weight ? g : static_cast<const float *>(dout);
+  b.drow = drow;
+  b.lambda = static_cast<const float *>(dp.lambda);
+  basa_params pm = p;
+  pm.heads = 2 * p.heads;
+  return run_attn_bwd_f32(b, q, k, v, kp, vp, route_idx, dq, dk, dv, pooled, pm, 1, s);
 }
 
 }  // namespace basa

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kMeanThreads, 2) box_mean_kernel(BoxMeanArgs a
 }
 
 template <typename T, typename OutT>
-basa_status run_box_mean(BoxMeanArgs a, int bh, cudaStream_t s) {
+basa_status run_box_mean(BoxMeanArgs a, int bh, cudaStream_t s, int tensors = 2) {
   const int lpr = a.d / (16 / int(sizeof(T)));
   a.nb_cta = std::max(1, std::min(a.nbx, kMeanThreads / lpr));
   a.splits = std::max(1, kMeanThreads / (lpr * a.nb_cta));
@@ -170,7 +170,7 @@ basa_status run_box_mean(BoxMeanArgs a, int bh, cudaStream_t s) {
   const size_t smem = a.splits > 1 ? size_t(threads) * (16 / sizeof(T)) * sizeof(float) : 0;
   const long long blocks = (long long)bh * a.nbt * a.nby * a.xgroups;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  dim3 grid(unsigned(blocks), 1, 2);
+  dim3 grid(unsigned(blocks), 1, unsigned(tensors));
   box_mean_kernel<T, OutT><<<grid, threads, smem, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
 }
@@ -280,10 +280,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs 
 
 }  // namespace
 
-basa_status launch_pool_kv(const void *k, const void *v, void *kp, void *vp, const basa_params &p, cudaStream_t s) {
-  BoxMeanArgs a{};
-  a.src[0] = k; a.src[1] = v;
-  a.dst[0] = kp; a.dst[1] = vp;
+namespace {
+// Pool-patch means of `tensors` tensors of bh units each.
+basa_status run_pool(BoxMeanArgs a, int bh, int tensors, const basa_params &p, cudaStream_t s) {
   const long long N = (long long)p.T * p.H * p.W;
   a.src_bh_stride[0] = a.src_bh_stride[1] = (N + p.n_text) * p.head_dim;
   a.d = p.head_dim;
@@ -292,9 +291,23 @@ basa_status launch_pool_kv(const void *k, const void *v, void *kp, void *vp, con
   a.nbt = p.T / p.pt; a.nby = p.H / p.ph; a.nbx = p.W / p.pw;
   a.ot = a.oy = a.ox = 0;
   a.inv_count = 1.0f / float(p.pt * p.ph * p.pw);
-  const int bh = p.B * p.heads;
-  if (p.dtype == BASA_BF16) return run_box_mean<__nv_bfloat16, __nv_bfloat16>(a, bh, s);
-  return run_box_mean<float, float>(a, bh, s);
+  if (p.dtype == BASA_BF16) return run_box_mean<__nv_bfloat16, __nv_bfloat16>(a, bh, s, tensors);
+  return run_box_mean<float, float>(a, bh, s, tensors);
+}
+}  // namespace
+
+basa_status launch_pool_kv(const void *k, const void *v, void *kp, void *vp, const basa_params &p, cudaStream_t s) {
+  BoxMeanArgs a{};
+  a.src[0] = k; a.src[1] = v;
+  a.dst[0] = kp; a.dst[1] = vp;
+  return run_pool(a, p.B * p.heads, 2, p, s);
+}
+
+basa_status launch_pool_rows(const void *x, void *xp, int units, const basa_params &p, cudaStream_t s) {
+  BoxMeanArgs a{};
+  a.src[0] = a.src[1] = x;
+  a.dst[0] = a.dst[1] = xp;
+  return run_pool(a, units, 1, p, s);
 }
 
 basa_status launch_route(const void *q, const void *k, int32_t *route_idx, float *route_score, void *workspace,

@@ -320,3 +320,87 @@ def test_rope_backward_checks():
 def test_rope_empty_is_a_no_op():
     for t, kw in ((_rope_tensor(x=0, y=0, rows=0), {}), (_rope_tensor(x=0, y=0, heads=0), {}), (_rope_tensor(x=0, y=0), dict(B=0))):
         assert B.basa_rope_fwd([t], None, 1e-6, _rope(), _p(**kw), stream=0, check=False) == 0
+
+
+def _diff(lam=FAKE, weight=FAKE, gain=1.0, eps=1e-6):
+    return B.make_diff_params(lam, weight, gain, eps)
+
+
+def _diff_fwd(dp=None, p=None, q=FAKE, k=FAKE, v=FAKE, kp=FAKE, vp=FAKE, route=None, out=FAKE, pre=None, second=None,
+              lse=None, ws=None):
+    return B.basa_diff_attn_fwd(q, k, v, kp, vp, route, dp or _diff(), out, pre, second, lse, ws, p or _p(), stream=0,
+                                check=False)
+
+
+def test_diff_forward_checks():
+    assert ctypes.sizeof(B.basa_diff_params) == 24 and B.basa_diff_params.gain.offset == 16
+    for kw in (dict(head_dim=96), dict(head_dim=64), dict(B=1 << 15, heads=1 << 15)):
+        assert _diff_fwd(p=_p(**kw)) == 3
+    assert _diff_fwd(p=_p(window=(1, 16, 20))) == 2 and _diff_fwd(p=_p(shift=(0, 64, 0))) == 2
+    for kw in (dict(lam=None), dict(lam=FAKE + 1), dict(weight=FAKE + 8), dict(gain=float("inf")), dict(eps=0.0),
+               dict(eps=float("nan"))):
+        assert _diff_fwd(_diff(**kw)) == 1, kw
+    for kw in (dict(q=None), dict(k=None), dict(v=None), dict(kp=None), dict(vp=None), dict(out=None), dict(route=FAKE),
+               dict(q=FAKE + 8), dict(kp=FAKE + 8), dict(out=FAKE + 8), dict(pre=FAKE + 8), dict(second=FAKE + 8),
+               dict(lse=FAKE + 2)):
+        assert _diff_fwd(**kw) == 1, kw
+    assert _diff_fwd(p=_p(routed_k=2)) == 1 and _diff_fwd(p=_p(routed_k=2), route=FAKE + 2) == 1
+    assert _diff_fwd(p=_p(pool=(0, 0, 0))) == 1  # pooled keys without a pool patch
+    f32 = _p(dtype="f32")
+    assert _diff_fwd(p=f32) == 1 and _diff_fwd(p=f32, ws=FAKE + 8) == 1  # float32 needs its workspace
+    assert _diff_fwd(_diff(lam=FAKE + 2), f32, ws=FAKE) == 1
+    assert B.basa_diff_attn_workspace_bytes(_p()) == 0
+    assert B.basa_diff_attn_workspace_bytes(f32) == 4 * 4096 * 128 * 4
+    for heads in (dict(B=0), dict(heads=0)):
+        assert _diff_fwd(_diff(None, None), _p(**heads), *[None] * 5) == 0
+
+
+def test_diff_pool_checks():
+    call = lambda p=None, **kw: B.basa_diff_pool_kv(*[kw.get(n, FAKE) for n in ("k", "v", "kp", "vp")], p or _p(), stream=0, check=False)  # noqa: E731
+    assert call(_p(pool=(0, 0, 0))) == 1
+    for name in ("k", "v", "kp", "vp"):
+        assert call(**{name: None}) == 1 and call(**{name: FAKE + 8}) == 1
+    assert call(_p(B=0), k=None) == 0
+
+
+def test_diff_backward_checks():
+    names = ("pre", "second", "lse", "dout", "dq", "dk", "dv", "dlam", "dweight", "ws")
+
+    def call(dp=None, p=None, route=None, **kw):
+        return B.basa_diff_attn_bwd(*[kw.get(n, FAKE) for n in ("q", "k", "v", "kp", "vp")], route, dp or _diff(),
+                                    *[kw.get(n, FAKE) for n in names], p or _p(), stream=0, check=False)
+
+    for name in ("q", "k", "v", "kp", "vp") + names:
+        assert call(**{name: None}) == 1, name
+    for name in ("q", "k", "v", "kp", "vp", "pre", "second", "dout", "dq", "dk", "dv", "dweight", "ws"):
+        assert call(**{name: FAKE + 8}) == 1, name
+    assert call(lse=FAKE + 2) == 1 and call(dlam=FAKE + 1) == 1 and call(ws=FAKE + 16) == 1
+    assert call(_diff(weight=None)) == 1  # a gradient without its weight
+    assert call(p=_p(head_dim=64)) == 3 and call(p=_p(routed_k=1)) == 1
+    assert call(p=_p(window=(1, 1, 1), pool=(0, 0, 0), grid=(1, 128, 64), routed_k=1), kp=None, vp=None, route=FAKE) == 3
+    # the gradients of nothing: there is no call that leaves weights' gradients unwritten
+    assert call(p=_p(B=0)) == 1 and call(_diff(weight=None), _p(heads=0), dweight=None) == 0
+
+
+def test_diff_backward_workspace():
+    norm, plain = _diff(), _diff(weight=None)
+    for dtype, size in (("bf16", 2), ("f32", 4)):
+        p = _p(dtype=dtype)
+        got = B.basa_diff_attn_bwd_workspace_bytes(norm, p), B.basa_diff_attn_bwd_workspace_bytes(plain, p)
+        assert got[0] - got[1] == 2 * 4096 * 128 * size and got[1] > 0
+    assert B.basa_diff_attn_bwd_workspace_bytes(norm, _p(head_dim=64)) == 0
+    assert B.basa_diff_attn_bwd_workspace_bytes(norm, _p(head_dim=64, dtype="f32")) > 0
+    assert B.basa_diff_attn_bwd_workspace_bytes(_diff(eps=0.0), _p()) == 0
+
+
+def test_diff_text_checks():
+    def call(p=None, dp=None, **kw):
+        return B.basa_diff_text_attn_fwd(*[kw.get(n, FAKE) for n in ("q", "k", "v")], dp or _diff(), kw.get("out", FAKE),
+                                         kw.get("ws", FAKE), p or _p(), stream=0, check=False)
+
+    for name in ("q", "k", "v", "out", "ws"):
+        assert call(**{name: None}) == 1 and call(**{name: FAKE + 8}) == 1, name
+    assert call(_p(n_text=0)) == 1 and call(_p(head_dim=64)) == 3 and call(dp=_diff(lam=None)) == 1
+    assert call(_p(B=0), q=None) == 0
+    assert B.basa_diff_text_attn_workspace_bytes(_p(n_text=0)) == 0
+    assert B.basa_diff_text_attn_workspace_bytes(_p(dtype="f32")) == 4 * 16 * 128 * 4
