@@ -447,23 +447,21 @@ basa_status basa_diff_pool_kv(const void *k, const void *v, void *kp, void *vp, 
                               basa_stream_t stream);
 
 /*
- * basa_diff_attn_fwd — forward. For a backward, `lse` receives the maps' log-sum-exp
- * (float32 [B, 2 heads, N]), `ratio` and `second` what O2 consists of,
- *   O2 = ratio a + second,  ratio = O2 . a / a . a   (float32 [B, heads, N]; 0 where a is 0)
- * (`second` [B, heads, N, head_dim], element type), and `pre` a itself (nullable: without
- * a weight `out` is a). Otherwise they may be NULL, `ratio` and `second` together.
+ * basa_diff_attn_fwd — forward. For a backward, `second` and `lse` receive O2
+ * [B, heads, N, head_dim] and the maps' log-sum-exp (float32 [B, 2 heads, N]); `pre`
+ * receives a (nullable: without a weight `out` is a). All three may be NULL otherwise.
  * `workspace`: basa_diff_attn_workspace_bytes(p) bytes (0 with bfloat16: pass NULL;
  * float32: the two maps' outputs), 16-byte aligned, contents ignored.
  */
 size_t basa_diff_attn_workspace_bytes(const basa_params *p);
 basa_status basa_diff_attn_fwd(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                const int32_t *route_idx, const basa_diff_params *dp, void *out, void *pre,
-                               void *second, float *ratio, float *lse, void *workspace, const basa_params *p,
+                               void *second, float *lse, void *workspace, const basa_params *p,
                                basa_stream_t stream);
 
 /*
  * basa_diff_attn_bwd — gradients with respect to q, k, v, lambda and weight. `pre` is a
- * (the forward's `pre`, or `out` without a weight), `second`, `ratio` and `lse` are the forward's.
+ * (the forward's `pre`, or `out` without a weight), `second` and `lse` the forward's.
  * As in basa_window_attn_bwd pooled keys and values pass their gradients on to their
  * patch's tokens and routing passes none. dlambda [heads] and dweight [head_dim] (NULL
  * iff there is no weight) have the element type; they are summed in float32 in a fixed
@@ -477,7 +475,7 @@ basa_status basa_diff_attn_fwd(const void *q, const void *k, const void *v, cons
 size_t basa_diff_attn_bwd_workspace_bytes(const basa_diff_params *dp, const basa_params *p);
 basa_status basa_diff_attn_bwd(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                const int32_t *route_idx, const basa_diff_params *dp, const void *pre,
-                               const void *second, const float *ratio, const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                               const void *second, const float *lse, const void *dout, void *dq, void *dk, void *dv,
                                void *dlambda, void *dweight, void *workspace, const basa_params *p,
                                basa_stream_t stream);
 

@@ -156,11 +156,11 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.basa_diff_pool_kv.restype = ctypes.c_int
     lib.basa_diff_attn_workspace_bytes.argtypes = [P]
     lib.basa_diff_attn_workspace_bytes.restype = ctypes.c_size_t
-    lib.basa_diff_attn_fwd.argtypes = [vp] * 6 + [D] + [vp] * 6 + [P, vp]
+    lib.basa_diff_attn_fwd.argtypes = [vp] * 6 + [D] + [vp] * 5 + [P, vp]
     lib.basa_diff_attn_fwd.restype = ctypes.c_int
     lib.basa_diff_attn_bwd_workspace_bytes.argtypes = [D, P]
     lib.basa_diff_attn_bwd_workspace_bytes.restype = ctypes.c_size_t
-    lib.basa_diff_attn_bwd.argtypes = [vp] * 6 + [D] + [vp] * 11 + [P, vp]
+    lib.basa_diff_attn_bwd.argtypes = [vp] * 6 + [D] + [vp] * 10 + [P, vp]
     lib.basa_diff_attn_bwd.restype = ctypes.c_int
     lib.basa_diff_text_attn_workspace_bytes.argtypes = [P]
     lib.basa_diff_text_attn_workspace_bytes.restype = ctypes.c_size_t
@@ -386,10 +386,10 @@ def basa_diff_attn_workspace_bytes(params: basa_params) -> int:
     return _lib.basa_diff_attn_workspace_bytes(ctypes.byref(params))
 
 
-def basa_diff_attn_fwd(q, k, v, kp, vp, route_idx, diff_params: basa_diff_params, out, pre, second, ratio, lse,
-                       workspace, params: basa_params, stream=None, check=True) -> int:
+def basa_diff_attn_fwd(q, k, v, kp, vp, route_idx, diff_params: basa_diff_params, out, pre, second, lse, workspace,
+                       params: basa_params, stream=None, check=True) -> int:
     st = _lib.basa_diff_attn_fwd(*[_ptr(x) for x in (q, k, v, kp, vp, route_idx)], ctypes.byref(diff_params),
-                                 *[_ptr(x) for x in (out, pre, second, ratio, lse, workspace)], ctypes.byref(params),
+                                 *[_ptr(x) for x in (out, pre, second, lse, workspace)], ctypes.byref(params),
                                  _stream(stream))
     if check:
         _check(st, "basa_diff_attn_fwd")
@@ -400,10 +400,10 @@ def basa_diff_attn_bwd_workspace_bytes(diff_params: basa_diff_params, params: ba
     return _lib.basa_diff_attn_bwd_workspace_bytes(ctypes.byref(diff_params), ctypes.byref(params))
 
 
-def basa_diff_attn_bwd(q, k, v, kp, vp, route_idx, diff_params: basa_diff_params, pre, second, ratio, lse, dout, dq, dk,
-                       dv, dlam, dweight, workspace, params: basa_params, stream=None, check=True) -> int:
+def basa_diff_attn_bwd(q, k, v, kp, vp, route_idx, diff_params: basa_diff_params, pre, second, lse, dout, dq, dk, dv,
+                       dlam, dweight, workspace, params: basa_params, stream=None, check=True) -> int:
     st = _lib.basa_diff_attn_bwd(*[_ptr(x) for x in (q, k, v, kp, vp, route_idx)], ctypes.byref(diff_params),
-                                 *[_ptr(x) for x in (pre, second, ratio, lse, dout, dq, dk, dv, dlam, dweight, workspace)],
+                                 *[_ptr(x) for x in (pre, second, lse, dout, dq, dk, dv, dlam, dweight, workspace)],
                                  ctypes.byref(params), _stream(stream))
     if check:
         _check(st, "basa_diff_attn_bwd")

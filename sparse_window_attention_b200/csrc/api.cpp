@@ -405,19 +405,17 @@ size_t basa_diff_attn_workspace_bytes(const basa_params *p) {
 
 basa_status basa_diff_attn_fwd(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                const int32_t *route_idx, const basa_diff_params *dp, void *out, void *pre, void *second,
-                               float *ratio, float *lse, void *workspace, const basa_params *p, basa_stream_t stream) {
+                               float *lse, void *workspace, const basa_params *p, basa_stream_t stream) {
   basa_status st = check_diff(dp, p);
   if (st != BASA_OK) return st;
   if (empty_batch(p)) return BASA_OK;
   if ((st = check_diff_inputs(q, k, v, kp, vp, route_idx, dp, p)) != BASA_OK) return st;
-  if (!out || !aligned16(out) || !aligned16(pre) || !aligned16(second) || !aligned4(lse) || !aligned4(ratio) ||
-      (second != nullptr) != (ratio != nullptr))
-    return BASA_ERR_INVALID_ARG;
+  if (!out || !aligned16(out) || !aligned16(pre) || !aligned16(second) || !aligned4(lse)) return BASA_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (p->dtype == BASA_BF16)
-    return basa::launch_diff_attn_bf16(q, k, v, kp, vp, route_idx, *dp, out, pre, second, lse, ratio, *p, s);
+    return basa::launch_diff_attn_bf16(q, k, v, kp, vp, route_idx, *dp, out, pre, second, lse, *p, s);
   if (!workspace || !aligned16(workspace)) return BASA_ERR_INVALID_ARG;
-  return basa::launch_diff_attn_f32(q, k, v, kp, vp, route_idx, *dp, out, pre, second, lse, ratio, workspace, *p, s);
+  return basa::launch_diff_attn_f32(q, k, v, kp, vp, route_idx, *dp, out, pre, second, lse, workspace, *p, s);
 }
 
 size_t basa_diff_attn_bwd_workspace_bytes(const basa_diff_params *dp, const basa_params *p) {
@@ -428,7 +426,7 @@ size_t basa_diff_attn_bwd_workspace_bytes(const basa_diff_params *dp, const basa
 
 basa_status basa_diff_attn_bwd(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                const int32_t *route_idx, const basa_diff_params *dp, const void *pre, const void *second,
-                               const float *ratio, const float *lse, const void *dout, void *dq, void *dk, void *dv, void *dlambda,
+                               const float *lse, const void *dout, void *dq, void *dk, void *dv, void *dlambda,
                                void *dweight, void *workspace, const basa_params *p, basa_stream_t stream) {
   basa_status st = check_diff(dp, p);
   if (st != BASA_OK) return st;
@@ -436,20 +434,20 @@ basa_status basa_diff_attn_bwd(const void *q, const void *k, const void *v, cons
     return BASA_ERR_UNSUPPORTED;
   if (empty_batch(p)) return p->heads > 0 || dp->weight ? BASA_ERR_INVALID_ARG : BASA_OK;
   if ((st = check_diff_inputs(q, k, v, kp, vp, route_idx, dp, p)) != BASA_OK) return st;
-  for (const void *x : {pre, second, static_cast<const void *>(ratio), static_cast<const void *>(lse), dout, static_cast<const void *>(dq),
+  for (const void *x : {pre, second, static_cast<const void *>(lse), dout, static_cast<const void *>(dq),
                         static_cast<const void *>(dk), static_cast<const void *>(dv)})
     if (!x) return BASA_ERR_INVALID_ARG;
   for (const void *x : {pre, second, dout, static_cast<const void *>(dq), static_cast<const void *>(dk),
                         static_cast<const void *>(dv), static_cast<const void *>(dweight)})
     if (!aligned16(x)) return BASA_ERR_INVALID_ARG;
-  if (!dlambda || !aligned_element(dlambda, p) || !aligned4(lse) || !aligned4(ratio)) return BASA_ERR_INVALID_ARG;
+  if (!dlambda || !aligned_element(dlambda, p) || !aligned4(lse)) return BASA_ERR_INVALID_ARG;
   if ((dweight != nullptr) != (dp->weight != nullptr)) return BASA_ERR_INVALID_ARG;
   const size_t need = basa_diff_attn_bwd_workspace_bytes(dp, p);
   if (need == 0) return BASA_ERR_UNSUPPORTED;  // the tiling plan does not fit the kernel's limits
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return BASA_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const auto launch = p->dtype == BASA_BF16 ? basa::launch_diff_attn_bwd_bf16 : basa::launch_diff_attn_bwd_f32;
-  return launch(q, k, v, kp, vp, route_idx, *dp, pre, second, ratio, lse, dout, dq, dk, dv, dlambda, dweight, workspace, *p, s);
+  return launch(q, k, v, kp, vp, route_idx, *dp, pre, second, lse, dout, dq, dk, dv, dlambda, dweight, workspace, *p, s);
 }
 
 size_t basa_diff_text_attn_workspace_bytes(const basa_params *p) {

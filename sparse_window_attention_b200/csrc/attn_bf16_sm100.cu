@@ -34,10 +34,9 @@
 // tiles for the same four MMAs. Each map is normalised by its own sum only at the end,
 // so both products with V are needed (P1/l1 - lambda P2/l2 is not known while the sums
 // run); the difference and the norm are taken from TMEM in float32 and rounded once.
-// For a backward the difference a before the norm is stored too, and the second map's
-// output as O2 = ratio a + second, ratio = O2 . a / a . a (float32): the norm's gradient is
-// orthogonal to a, so what it sees of O2 is `second`, rounded relative to its own size. With
-// maps that are nearly alike O2 itself, rounded, would leave lambda's gradient 5% off.
+// For a backward the difference before the norm and the second map's output are stored
+// too: with those two, rounded relative to their own size, the first map's follows as
+// their sum, where a difference of two rounded maps would lose what cancels in it.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -109,8 +108,7 @@ struct alignas(64) AttnParams {
   int v_shift;   // v and vp belong to unit bh >> v_shift (two maps that share their values)
   // differential form: a CTA's unit is a (batch, differential head); map g's q, k, kp are unit 2 * unit + g
   const __nv_bfloat16 *lambda, *norm_weight;  // [heads]; nullable [128]
-  int heads, store_pre;
-  float *ratio;  // nullable [B*heads][N]: with it map_o2 is stored
+  int heads, store_pre, store_o2;
   float gain, eps;
   float *part;  // FORM kPart: float32 outputs [split][b*head][n_text][128]
   uint32_t flags;
@@ -612,12 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
       // The ring is free by now: out is staged in its slot 0, row sums in its slot 1;
       // the difference before the norm and O2 / l2, when asked for, over the query tiles.
       float *inv_l = reinterpret_cast<float *>(smem + kSmemRing + kTileBytes);  // [2][128]
-      float *sq = inv_l + 2 * kTileRows, *so = sq + 2 * kTileRows;               // [2][128] each
+      float *sq = inv_l + 2 * kTileRows;                                         // [2][128]
       if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.o_full[0], 0) && wt.wait(&c.o_full[1], 0));
       if (ok) inv_l[g * kTileRows + row] = 1.0f / l;
       ptx::named_barrier(3, 256);
       float a[64];
-      float ss = 0.f, sa = 0.f;  // this half row's a . a and O2 . a
+      float ss = 0.f;
       if (ok) {
         ptx::tc_fence_after();
         const float i0 = inv_l[row], i1 = inv_l[kTileRows + row];
@@ -630,38 +628,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
           ptx::tmem_ld32(tmem + lane_off + 384 + cc * 32, r1);
           ptx::tmem_ld_wait(r0);
           ptx::tmem_ld_wait(r1);
+          float o1[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float o1 = __uint_as_float(r1[i]) * i1;
-            a[32 * h + i] = fmaf(-lam, o1, __uint_as_float(r0[i]) * i0);
+            o1[i] = __uint_as_float(r1[i]) * i1;
+            a[32 * h + i] = fmaf(-lam, o1[i], __uint_as_float(r0[i]) * i0);
             ss = fmaf(a[32 * h + i], a[32 * h + i], ss);
-            sa = fmaf(o1, a[32 * h + i], sa);
           }
           if (P.store_pre) stage_cols32(smem + kSmemQ, row, cc, a + 32 * h);
+          if (P.store_o2) stage_cols32(smem + kSmemQ + kTileBytes, row, cc, o1);
         }
         sq[g * kTileRows + row] = ss;
-        so[g * kTileRows + row] = sa;
       }
-      if (P.norm_weight != nullptr || P.ratio != nullptr) ptx::named_barrier(3, 256);
+      if (P.norm_weight != nullptr) ptx::named_barrier(3, 256);
       if (ok) {
-        if (P.ratio != nullptr) {
-          const float i1 = inv_l[kTileRows + row], aa = sq[row] + sq[kTileRows + row];
-          const float ratio = aa > 0.f ? (so[row] + so[kTileRows + row]) / aa : 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t r1[32];
-            ptx::tmem_ld32(tmem + lane_off + 384 + (2 * g + h) * 32, r1);
-            ptx::tmem_ld_wait(r1);
-            float o1[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o1[i] = fmaf(-ratio, a[32 * h + i], __uint_as_float(r1[i]) * i1);
-            stage_cols32(smem + kSmemQ + kTileBytes, row, 2 * g + h, o1);
-          }
-          int t, y, x;
-          const int org[3] = {ot, oy, ox};
-          if (g == 0 && sm100::tile_row_token(P.plan, P.g, P.plan.tile[ty.first_tile + q_tile0], org, row, &t, &y, &x))
-            P.ratio[(long long)bh * P.g.N + ((long long)t * P.g.H + y) * P.g.W + x] = ratio;
-        }
         if (P.norm_weight != nullptr) {
           const float f = rsqrtf((sq[row] + sq[kTileRows + row]) * (1.0f / 128.0f) + P.eps) * P.gain;
           const uint4 *w4 = reinterpret_cast<const uint4 *>(P.norm_weight + 64 * g);
@@ -752,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
         const PlanTile &tile = P.plan.tile[ty.first_tile + q_tile0];
         if (g == 0) sm100::store_window_tile(P.plan, P.g, P.map_o, tile, org, bh, smem + kSmemRing);
         if (g == 0 && P.store_pre) sm100::store_window_tile(P.plan, P.g, P.map_pre, tile, org, bh, q_tile);
-        if (g == 1 && P.ratio != nullptr) sm100::store_window_tile(P.plan, P.g, P.map_o2, tile, org, bh, q_tile);
+        if (g == 1 && P.store_o2) sm100::store_window_tile(P.plan, P.g, P.map_o2, tile, org, bh, q_tile);
         ptx::tma_store_commit();
         ptx::tma_store_wait_read_all();
       }
@@ -978,7 +958,7 @@ basa_status launch_attn_bf16(const void *q, const void *k, const void *v, const 
 
 basa_status launch_diff_attn_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                   const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
-                                  void *second, float *lse, float *ratio, const basa_params &p, cudaStream_t s) {
+                                  void *second, float *lse, const basa_params &p, cudaStream_t s) {
   AttnParams P;
   basa_status st = window_params(P, q, k, v, kp, vp, route_idx, out, lse, BASA_KEYS_ALL, p, 2);
   if (st != BASA_OK) return st;
@@ -988,7 +968,7 @@ basa_status launch_diff_attn_bf16(const void *q, const void *k, const void *v, c
   P.eps = dp.eps;
   P.heads = p.heads;
   P.store_pre = pre != nullptr;
-  P.ratio = ratio;
+  P.store_o2 = second != nullptr;
   for (int i = 0; i < P.plan.n_shapes; ++i)
     if ((pre && !encode_grid_map(&P.map_pre[i], pre, p, P.g.N, P.plan.shape[i])) ||
         (second && !encode_grid_map(&P.map_o2[i], second, p, P.g.N, P.plan.shape[i])))
@@ -1098,7 +1078,7 @@ basa_status launch_diff_text_bf16(const void *q_text, const void *k, const void 
   const long long blocks = (long long)P.bh_count * P.dense_pairs * P.n_splits;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
   if ((st = run_attn<kPart>(P, blocks, s)) != BASA_OK) return st;
-  return launch_diff_combine(P.n_splits, P.part, P.lse, p.n_text, dp, out_text, nullptr, nullptr, nullptr, p, s);
+  return launch_diff_combine(P.n_splits, P.part, P.lse, p.n_text, dp, out_text, nullptr, nullptr, p, s);
 }
 
 }  // namespace basa

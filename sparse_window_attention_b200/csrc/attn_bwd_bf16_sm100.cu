@@ -1128,7 +1128,7 @@ size_t diff_attn_bwd_bf16_workspace(bool norm, const basa_params &p) {
 
 basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                       const int32_t *route_idx, const basa_diff_params &dp, const void *pre,
-                                      const void *second, const float *ratio, const float *lse, const void *dout, void *dq, void *dk,
+                                      const void *second, const float *lse, const void *dout, void *dq, void *dk,
                                       void *dv, void *dlambda, void *dweight, void *workspace, const basa_params &p,
                                       cudaStream_t s) {
   static thread_local BwdParams P;
@@ -1143,7 +1143,7 @@ basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *
   P.lambda = static_cast<const __nv_bfloat16 *>(dp.lambda);
   P.heads = p.heads;
   P.dk = static_cast<__nv_bfloat16 *>(dk);
-  st = launch_diff_prep(pre, second, ratio, lse, dout, dp, g, reinterpret_cast<float4 *>(ws), nullptr, dlambda, dweight,
+  st = launch_diff_prep(pre, second, lse, dout, dp, g, reinterpret_cast<float4 *>(ws), nullptr, dlambda, dweight,
                         reinterpret_cast<float *>(part), p, s);
   if (st != BASA_OK) return st;
   return run_passes<true>(P, L, dk, dv, p, s);

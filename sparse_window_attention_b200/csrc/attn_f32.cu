@@ -460,14 +460,13 @@ size_t diff_f32_workspace(const basa_params &p, long long rows) {
 
 basa_status launch_diff_attn_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                  const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
-                                 void *second, float *lse, float *ratio, void *workspace, const basa_params &p,
-                                 cudaStream_t s) {
+                                 void *second, float *lse, void *workspace, const basa_params &p, cudaStream_t s) {
   basa_params pm = p;
   pm.heads = 2 * p.heads;
   basa_status st = launch_attn_f32(q, k, v, kp, vp, route_idx, workspace, lse, BASA_KEYS_ALL, pm, s, 1);
   if (st != BASA_OK) return st;
   return launch_diff_combine(1, static_cast<const float *>(workspace), nullptr, (long long)p.T * p.H * p.W, dp, out, pre,
-                             second, ratio, p, s);
+                             second, p, s);
 }
 
 basa_status launch_diff_text_f32(const void *q_text, const void *k, const void *v, const basa_diff_params &dp,
@@ -477,7 +476,7 @@ basa_status launch_diff_text_f32(const void *q_text, const void *k, const void *
   basa_status st = launch_attn_text_f32(q_text, k, v, workspace, pm, s, 1);
   if (st != BASA_OK) return st;
   return launch_diff_combine(1, static_cast<const float *>(workspace), nullptr, p.n_text, dp, out_text, nullptr, nullptr,
-                             nullptr, p, s);
+                             p, s);
 }
 
 namespace {
@@ -493,7 +492,7 @@ size_t diff_attn_bwd_f32_workspace(bool norm, const basa_params &p) {
 
 basa_status launch_diff_attn_bwd_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                      const int32_t *route_idx, const basa_diff_params &dp, const void *pre,
-                                     const void *second, const float *ratio, const float *lse, const void *dout, void *dq, void *dk,
+                                     const void *second, const float *lse, const void *dout, void *dq, void *dk,
                                      void *dv, void *dlambda, void *dweight, void *workspace, const basa_params &p,
                                      cudaStream_t s) {
   const size_t rows = size_t(p.B) * p.heads * p.T * p.H * p.W;
@@ -504,7 +503,7 @@ basa_status launch_diff_attn_bwd_f32(const void *q, const void *k, const void *v
   ws += align256(2 * rows * sizeof(float));
   float *g = reinterpret_cast<float *>(ws);
   if (dp.weight) ws += align256(rows * p.head_dim * sizeof(float));
-  basa_status st = launch_diff_prep(pre, second, ratio, lse, dout, dp, g, nullptr, drow, dlambda, dweight,
+  basa_status st = launch_diff_prep(pre, second, lse, dout, dp, g, nullptr, drow, dlambda, dweight,
                                     reinterpret_cast<float *>(ws), p, s);
   if (st != BASA_OK) return st;
   BwdArgs b{};

@@ -167,12 +167,11 @@ basa_status launch_attn_text_f32(const void *q_text, const void *k, const void *
 // Differential attention: p.heads heads of two maps each (q, k, kp: 2 heads units).
 basa_status launch_diff_attn_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                   const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
-                                  void *second, float *lse, float *ratio, const basa_params &p, cudaStream_t s);
+                                  void *second, float *lse, const basa_params &p, cudaStream_t s);
 size_t diff_f32_workspace(const basa_params &p, long long rows);  // the maps' outputs of `rows` rows
 basa_status launch_diff_attn_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                  const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
-                                 void *second, float *lse, float *ratio, void *workspace, const basa_params &p,
-                                 cudaStream_t s);
+                                 void *second, float *lse, void *workspace, const basa_params &p, cudaStream_t s);
 size_t diff_text_workspace(const basa_params &p, int sms);  // bf16 path
 basa_status launch_diff_text_bf16(const void *q_text, const void *k, const void *v, const basa_diff_params &dp,
                                   void *out_text, void *workspace, const basa_params &p, int sms, cudaStream_t s);
@@ -180,23 +179,23 @@ basa_status launch_diff_text_f32(const void *q_text, const void *k, const void *
                                  void *out_text, void *workspace, const basa_params &p, cudaStream_t s);
 // out (and pre, second) from the maps' float32 outputs, joined over n_splits key ranges.
 basa_status launch_diff_combine(int n_splits, const float *part, const float *part_lse, long long rows,
-                                const basa_diff_params &dp, void *out, void *pre, void *second, float *ratio,
-                                const basa_params &p, cudaStream_t s);
+                                const basa_diff_params &dp, void *out, void *pre, void *second, const basa_params &p,
+                                cudaStream_t s);
 // Start of the backward: g, the rows' records (or D alone), dlambda and dweight.
 size_t diff_prep_workspace(const basa_params &p);
-basa_status launch_diff_prep(const void *pre, const void *second, const float *ratio, const float *lse, const void *dout,
+basa_status launch_diff_prep(const void *pre, const void *second, const float *lse, const void *dout,
                              const basa_diff_params &dp, void *g, float4 *rec, float *drow, void *dlambda, void *dweight,
                              float *part, const basa_params &p, cudaStream_t s);
 size_t diff_attn_bwd_bf16_workspace(bool norm, const basa_params &p);
 basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                       const int32_t *route_idx, const basa_diff_params &dp, const void *pre,
-                                      const void *second, const float *ratio, const float *lse, const void *dout, void *dq, void *dk,
+                                      const void *second, const float *lse, const void *dout, void *dq, void *dk,
                                       void *dv, void *dlambda, void *dweight, void *workspace, const basa_params &p,
                                       cudaStream_t s);
 size_t diff_attn_bwd_f32_workspace(bool norm, const basa_params &p);
 basa_status launch_diff_attn_bwd_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                      const int32_t *route_idx, const basa_diff_params &dp, const void *pre,
-                                     const void *second, const float *ratio, const float *lse, const void *dout, void *dq, void *dk,
+                                     const void *second, const float *lse, const void *dout, void *dq, void *dk,
                                      void *dv, void *dlambda, void *dweight, void *workspace, const basa_params &p,
                                      cudaStream_t s);
 // Means over the pool patches of `units` units of one tensor.

@@ -6,9 +6,7 @@
 //           joined by log-sum-exp) to out: the text-query rows and the float32 layers.
 // prepare   the start of the backward: with xh = a r and G = gain * dout
 //             dweight = sum G xh,  g = r (G w - xh mean(G w xh)),
-//             D2 = g . O2,  D1 = g . O1 = g . a + lambda D2,  dlambda = -sum g . O2
-//           with O2 = second + ratio a, and g . a = mean(G w xh) d eps r^2 (the norm's
-//           gradient is orthogonal to a but for eps) in dlambda, where it would cancel;
+//             D2 = g . O2,  D1 = g . O1 = g . a + lambda D2,  dlambda = -sum g . O2;
 //           g goes on as the output gradient of both maps (map 2's factor -lambda is put
 //           on its dq, dK and dV sums), D1 and D2 as their rows' softmax corrections.
 // reduce    the blocks' partial sums of dlambda and dweight, in a fixed order.
@@ -69,7 +67,6 @@ struct CombineArgs {
   const float *lse;   // [n_splits][B][2 heads][rows] (n_splits > 1)
   const void *lambda, *weight;
   void *out, *pre, *second;  // [B][heads][rows][d]
-  float *ratio;              // [B][heads][rows], with second
   int n_splits, heads;
   long long rows, units;  // rows of a unit; B * heads
   float gain, eps;
@@ -112,28 +109,19 @@ __global__ void __launch_bounds__(kDiffThreads) diff_combine_kernel(const __grid
   joined_row<D>(a, (2 * unit) * a.rows + row, c, x);
   joined_row<D>(a, (2 * unit + 1) * a.rows + row, c, o2);
   const float lam = to_float(static_cast<const T *>(a.lambda)[unit % a.heads]);
-  float ss = 0.f, so = 0.f;
+  float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[i] = fmaf(-lam, o2[i], x[i]);
     ss = fmaf(x[i], x[i], ss);
-    so = fmaf(o2[i], x[i], so);
   }
-  ss = row_sum<LPR>(ss);
-  so = row_sum<LPR>(so);
   const long long at = (unit * a.rows + row) * D + 8 * c;
-  if (valid && a.second) {
-    const float ratio = ss > 0.f ? so / ss : 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o2[i] = fmaf(-ratio, x[i], o2[i]);
-    store8(static_cast<T *>(a.second) + at, o2);
-    if (c == 0) a.ratio[unit * a.rows + row] = ratio;
-  }
+  if (valid && a.second) store8(static_cast<T *>(a.second) + at, o2);
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = x[i];
   if (a.weight) {
-    const float f = rsqrtf(ss * (1.f / D) + a.eps) * a.gain;
+    const float f = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps) * a.gain;
     float w[8];
     load8(static_cast<const T *>(a.weight) + 8 * c, w);
 #pragma unroll
@@ -151,11 +139,11 @@ constexpr int kPrepRows = 64;
 
 struct PrepArgs {
   const void *pre, *second, *dout, *lambda, *weight;
-  const float *lse, *ratio;  // [units][2][rows], [units][rows]
+  const float *lse;  // [units][2][rows]
   void *g;           // [units][rows][d]; unused without weight (g = dout)
   float4 *rec;       // nullable: records {-L log2 e, -D, 0, 0} [units][2][rows]
   float *drow;       // nullable: D alone, [units][2][rows]
-  float *part;       // [blocks][1 + d]: sum of g . O2, then the weight's gradient
+  float *part;       // [blocks][1 + d]: sum g . O2, then the weight's gradient
   int heads, blocks_per_unit;
   long long rows;
   float gain, eps;
@@ -186,8 +174,6 @@ __global__ void __launch_bounds__(kDiffThreads) diff_prep_kernel(const __grid_co
       load8(static_cast<const T *>(a.second) + at, o2);
       load8(static_cast<const T *>(a.dout) + at, g);
     }
-    const float ratio = valid ? __ldg(a.ratio + unit * a.rows + r) : 0.f;
-    float ga = 0.f;  // this lane's part of g . a
     if (a.weight) {
       float ss = 0.f, dot = 0.f, xh[8];
 #pragma unroll
@@ -204,28 +190,20 @@ __global__ void __launch_bounds__(kDiffThreads) diff_prep_kernel(const __grid_co
       dot = row_sum<LPR>(dot) * (1.f / D);
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = rms * (g[i] - xh[i] * dot);
-      if (c == 0) ga = dot * (float(D) * a.eps * rms * rms);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ga = fmaf(g[i], x[i], ga);
     }
-    dl = fmaf(ratio, ga, dl);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dl = fmaf(g[i], o2[i], dl);
-    // D1 and D2 are those of the rounded g, which the products with V see (the rows of dS
-    // then sum to zero up to the products' own error): its product with a is g's, known
-    // from above, and that of the rounding's remainder, where a's own rounding is second order.
-    float d2 = 0.f, da = ga, g0[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g0[i] = g[i];
+    // D1 and D2 from the rounded g, which the products with V see: the rows of dS then
+    // sum to zero up to the products' own error
     if (a.weight && valid) store8(static_cast<T *>(a.g) + at, g);
+    float d2 = 0.f, da = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       d2 = fmaf(g[i], o2[i], d2);
-      da = fmaf(g[i] - g0[i], x[i], da);
+      da = fmaf(g[i], x[i], da);
     }
+    d2 = row_sum<LPR>(d2);
     da = row_sum<LPR>(da);
-    d2 = fmaf(ratio, da, row_sum<LPR>(d2));
     if (valid && c < 2) {
       const long long m = (2 * unit + c) * a.rows + r;
       const float d = c == 0 ? fmaf(lam, d2, da) : d2;
@@ -314,8 +292,8 @@ long long prep_blocks_per_unit(const basa_params &p) {
 }  // namespace
 
 basa_status launch_diff_combine(int n_splits, const float *part, const float *part_lse, long long rows,
-                                const basa_diff_params &dp, void *out, void *pre, void *second, float *ratio,
-                                const basa_params &p, cudaStream_t s) {
+                                const basa_diff_params &dp, void *out, void *pre, void *second, const basa_params &p,
+                                cudaStream_t s) {
   CombineArgs a{};
   a.part = part;
   a.lse = part_lse;
@@ -324,7 +302,6 @@ basa_status launch_diff_combine(int n_splits, const float *part, const float *pa
   a.out = out;
   a.pre = pre;
   a.second = second;
-  a.ratio = ratio;
   a.n_splits = n_splits;
   a.heads = p.heads;
   a.rows = rows;
@@ -339,13 +316,12 @@ size_t diff_prep_workspace(const basa_params &p) {
   return size_t(p.B) * p.heads * prep_blocks_per_unit(p) * (p.head_dim + 1) * sizeof(float);
 }
 
-basa_status launch_diff_prep(const void *pre, const void *second, const float *ratio, const float *lse, const void *dout,
+basa_status launch_diff_prep(const void *pre, const void *second, const float *lse, const void *dout,
                              const basa_diff_params &dp, void *g, float4 *rec, float *drow, void *dlambda, void *dweight,
                              float *part, const basa_params &p, cudaStream_t s) {
   PrepArgs a{};
   a.pre = pre;
   a.second = second;
-  a.ratio = ratio;
   a.dout = dout;
   a.lambda = dp.lambda;
   a.weight = dp.weight;

@@ -122,11 +122,11 @@ class BasaDiffLayer:
             route_idx = self._route(q, k, shift)
         return kp, vp, route_idx
 
-    def _forward(self, q, k, v, lam, shift, weight, kp, vp, route_idx, out, pre, second, ratio, lse, extra):
+    def _forward(self, q, k, v, lam, shift, weight, kp, vp, route_idx, out, pre, second, lse, extra):
         params = self.params(shift, **extra)
         dp = B.make_diff_params(lam, weight, self.gain, self.eps)
         ws = self._workspace(B.basa_diff_attn_workspace_bytes(params))
-        B.basa_diff_attn_fwd(q, k, v, kp, vp, route_idx, dp, out, pre, second, ratio, lse, ws, params)
+        B.basa_diff_attn_fwd(q, k, v, kp, vp, route_idx, dp, out, pre, second, lse, ws, params)
 
     def attention(self, q, k, v, lam, shift, weight=None, kp=None, vp=None, route_idx=None, out=None, stream=None,
                   **extra):
@@ -139,13 +139,13 @@ class BasaDiffLayer:
             kp, vp, route_idx = self._keys(q, k, v, shift, kp, vp, route_idx)
             if out is None:
                 out = self._new(self.batch, self.heads, self.N, self.head_dim)
-            self._forward(q, k, v, lam, shift, weight, kp, vp, route_idx, out, None, None, None, None, extra)
+            self._forward(q, k, v, lam, shift, weight, kp, vp, route_idx, out, None, None, None, extra)
         return out
 
     def attention_train(self, q, k, v, lam, shift, weight=None, kp=None, vp=None, route_idx=None, stream=None, **extra):
         """(out, saved): ``saved`` is what ``backward`` needs beside the inputs, the
-        difference before the norm, the second maps' output (by its ratio to the difference
-        and the rest), the log-sum-exps and the pooled and routed keys that were used."""
+        difference before the norm, the second maps' output, the log-sum-exps and the
+        pooled and routed keys that were used."""
         self._check_inputs(q, k, v, lam, weight, kp, vp, route_idx)
         with streams.on(self.device, stream):
             kp, vp, route_idx = self._keys(q, k, v, shift, kp, vp, route_idx)
@@ -153,10 +153,9 @@ class BasaDiffLayer:
             out, second = self._new(*shape), self._new(*shape)
             pre = out if weight is None else self._new(*shape)
             lse = self._new(self.batch, 2 * self.heads, self.N, dtype=torch.float32)
-            ratio = self._new(self.batch, self.heads, self.N, dtype=torch.float32)
             self._forward(q, k, v, lam, shift, weight, kp, vp, route_idx, out, None if weight is None else pre, second,
-                          ratio, lse, extra)
-        return out, (pre, second, ratio, lse, kp, vp, route_idx)
+                          lse, extra)
+        return out, (pre, second, lse, kp, vp, route_idx)
 
     def backward(self, q, k, v, lam, shift, saved, dout, weight=None, kp=None, vp=None, route_idx=None, stream=None,
                  **extra):
@@ -164,12 +163,11 @@ class BasaDiffLayer:
         dweight None without a norm. Without a norm ``out`` is part of ``saved`` and must
         not have been overwritten. Pooled and routed keys default to those in ``saved``."""
         self._check_inputs(q, k, v, lam, weight, kp, vp, route_idx)
-        pre, second, ratio, lse, kp0, vp0, route0 = saved
+        pre, second, lse, kp0, vp0, route0 = saved
         shape = (self.batch, self.heads, self.N, self.head_dim)
         self._check("dout", dout, *shape)
         self._check("saved", pre, *shape)
         self._check("saved", second, *shape)
-        self._check("saved", ratio, *shape[:3], dtype=torch.float32)
         self._check("saved", lse, self.batch, 2 * self.heads, self.N, dtype=torch.float32)
         if kp is None:
             kp, vp = kp0, vp0
@@ -182,7 +180,7 @@ class BasaDiffLayer:
             dlam = self._new(self.heads)
             dweight = None if weight is None else self._new(self.head_dim)
             ws = self._workspace(B.basa_diff_attn_bwd_workspace_bytes(dp, params))
-            B.basa_diff_attn_bwd(q, k, v, kp, vp, route_idx, dp, pre, second, ratio, lse, dout, dq, dk, dv, dlam, dweight, ws,
+            B.basa_diff_attn_bwd(q, k, v, kp, vp, route_idx, dp, pre, second, lse, dout, dq, dk, dv, dlam, dweight, ws,
                                  params)
         return dq, dk, dv, dlam, dweight
 

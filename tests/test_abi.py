@@ -327,9 +327,8 @@ def _diff(lam=FAKE, weight=FAKE, gain=1.0, eps=1e-6):
 
 
 def _diff_fwd(dp=None, p=None, q=FAKE, k=FAKE, v=FAKE, kp=FAKE, vp=FAKE, route=None, out=FAKE, pre=None, second=None,
-              ratio=None, lse=None, ws=None):
-    return B.basa_diff_attn_fwd(q, k, v, kp, vp, route, dp or _diff(), out, pre, second, ratio, lse, ws, p or _p(),
-                                stream=0,
+              lse=None, ws=None):
+    return B.basa_diff_attn_fwd(q, k, v, kp, vp, route, dp or _diff(), out, pre, second, lse, ws, p or _p(), stream=0,
                                 check=False)
 
 
@@ -343,7 +342,7 @@ def test_diff_forward_checks():
         assert _diff_fwd(_diff(**kw)) == 1, kw
     for kw in (dict(q=None), dict(k=None), dict(v=None), dict(kp=None), dict(vp=None), dict(out=None), dict(route=FAKE),
                dict(q=FAKE + 8), dict(kp=FAKE + 8), dict(out=FAKE + 8), dict(pre=FAKE + 8), dict(second=FAKE + 8),
-               dict(lse=FAKE + 2), dict(second=FAKE), dict(ratio=FAKE), dict(second=FAKE, ratio=FAKE + 2)):
+               dict(lse=FAKE + 2)):
         assert _diff_fwd(**kw) == 1, kw
     assert _diff_fwd(p=_p(routed_k=2)) == 1 and _diff_fwd(p=_p(routed_k=2), route=FAKE + 2) == 1
     assert _diff_fwd(p=_p(pool=(0, 0, 0))) == 1  # pooled keys without a pool patch
@@ -365,7 +364,7 @@ def test_diff_pool_checks():
 
 
 def test_diff_backward_checks():
-    names = ("pre", "second", "ratio", "lse", "dout", "dq", "dk", "dv", "dlam", "dweight", "ws")
+    names = ("pre", "second", "lse", "dout", "dq", "dk", "dv", "dlam", "dweight", "ws")
 
     def call(dp=None, p=None, route=None, **kw):
         return B.basa_diff_attn_bwd(*[kw.get(n, FAKE) for n in ("q", "k", "v", "kp", "vp")], route, dp or _diff(),
@@ -375,7 +374,7 @@ def test_diff_backward_checks():
         assert call(**{name: None}) == 1, name
     for name in ("q", "k", "v", "kp", "vp", "pre", "second", "dout", "dq", "dk", "dv", "dweight", "ws"):
         assert call(**{name: FAKE + 8}) == 1, name
-    assert call(lse=FAKE + 2) == 1 and call(ratio=FAKE + 2) == 1 and call(dlam=FAKE + 1) == 1 and call(ws=FAKE + 16) == 1
+    assert call(lse=FAKE + 2) == 1 and call(dlam=FAKE + 1) == 1 and call(ws=FAKE + 16) == 1
     assert call(_diff(weight=None)) == 1  # a gradient without its weight
     assert call(p=_p(head_dim=64)) == 3 and call(p=_p(routed_k=1)) == 1
     assert call(p=_p(window=(1, 1, 1), pool=(0, 0, 0), grid=(1, 128, 64), routed_k=1), kp=None, vp=None, route=FAKE) == 3
