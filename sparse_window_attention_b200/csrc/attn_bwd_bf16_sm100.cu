@@ -30,7 +30,8 @@
 //
 // Differential form (template argument DIFF; out = O1 - lambda O2 of two maps that share
 // their values, the norm's gradient g taken beforehand and D per map in the records): the
-// dq pass runs over the maps, with map 2's sums scaled by -lambda in its epilogue. The
+// dq pass runs over the maps, with map 2's sums scaled by -lambda in its epilogue, and adds
+// up each row's dS (what its D was off by), which lambda's gradient takes in. The
 // dK/dV passes run both maps of a (batch, head) in ONE CTA, map 2 first: its dK leaves,
 // the dV accumulator is multiplied by -lambda in TMEM, and map 1 adds to it, so the two
 // maps' dV meet without a buffer or an atomic. (Both maps at once, sharing dout V^T, would
@@ -99,6 +100,7 @@ struct alignas(64) BwdParams {
   float *part;        // long key tiles: [bh][tile][chunk][dK (of each map) | dV][128][128] partial sums
   const __nv_bfloat16 *lambda;  // differential form: [heads]
   __nv_bfloat16 *dk;            // differential form: dk itself, for map 2's rows
+  float *dr;                    // differential form: [map][window][query tile] sums of rec.z (sum dS)
   int heads;
   Geo g;
   int bh_count;  // units of v, dout and the routes (differential form: q, k have two for each)
@@ -284,7 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     w = (blockIdx.x / P.max_tiles) % P.g.nWin;
     bh = blockIdx.x / (P.max_tiles * P.g.nWin);
     window_origin(P.g, w, &ot, &oy, &ox, &wtype);
-    if (tile_idx >= P.plan.type[wtype].n_tiles) return;  // whole CTA: this window type has fewer tiles
+    if (tile_idx >= P.plan.type[wtype].n_tiles) {  // whole CTA: this window type has fewer tiles
+      if (DIFF && MODE == kDq && threadIdx.x == 0) P.dr[blockIdx.x] = 0.f;
+      return;
+    }
   }
   // Units: bh counts maps in the dq pass and values (two maps each) in the dK/dV passes.
   const int bh_v = DIFF && MODE == kDq ? bh >> 1 : bh;       // unit of v, dout and the routes
@@ -633,12 +638,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     bool ok = true;
     if (MODE == kDq) {
       const uint32_t tS = tmem + lane_off + col, tDP = tmem + lane_off + 128 + col;
+      float dr_weight = 0.f;
+      uint64_t dr2 = 0;            // sums of this row's dS (even and odd columns)
       uint64_t nl2 = 0, nd2 = 0;  // this row's -L log2 e and -D, paired for packed arithmetic
       int t, y, x;                // (a padding row keeps 0, 0: its dS is 0 as its dout row is 0)
       if (n_cols > 0 && tile_row_token(P.plan, P.g, row_tile, row_org, row, &t, &y, &x)) {
         const float4 rec = P.rec[(long long)bh * P.g.N + ((long long)t * P.g.H + y) * P.g.W + x];
         nl2 = ptx::f2_pack(rec.x, rec.x);
         nd2 = ptx::f2_pack(rec.y, rec.y);
+        dr_weight = rec.z;
       }
       if (n_cols > 0) {
         // This row's q and dout (this group's 64 of the head dims) into TMEM, where the
@@ -689,6 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           s[i + 1] = d1;
         }
         if ((m0 & m1) != 0xFFFFFFFFu) zero_masked(s, m0, m1);  // warp-uniform: a partial key tile
+        if (DIFF) {
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) dr2 = ptx::fadd2(dr2, ptx::f2_pack(s[i], s[i + 1]));
+        }
         uint32_t pk[32];
         pack64(s, pk);
         ptx::tmem_st32(tDP, pk);  // dS (bf16) over the first half of this thread's dP columns
@@ -706,8 +718,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
         for (int i = 0; i < 64; ++i) x[i] *= DIFF && (bh & 1) ? P.scale * neg_lambda : P.scale;
         stage_row_half(row0, row, g, x);  // the q tile is no longer read
         ptx::fence_proxy_async_smem();
+        if (DIFF) {  // the 256 half rows' weighted sums, in a fixed order (the dout tile is no longer read)
+          float even, odd;
+          ptx::f2_unpack(dr2, even, odd);
+          float d = (even + odd) * dr_weight;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+          if (lane == 0) reinterpret_cast<float *>(row1)[warp - 2] = d;
+        }
       }
       ptx::named_barrier(1, 256);
+      if (DIFF && threadIdx.x == 64) {
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d += reinterpret_cast<const float *>(row1)[i];
+        P.dr[blockIdx.x] = d;  // [map][window][query tile]
+      }
       if (threadIdx.x == 64 && ok && !*reinterpret_cast<volatile int *>(&c.abort)) {
         store_window_tile(P.plan, P.g, P.map_dq, row_tile, row_org, bh, row0);
         ptx::tma_store_commit();
@@ -1118,12 +1144,18 @@ basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, co
 }
 
 // Differential form: the layout of two maps, then g (with a norm), then the partial sums
-// of dlambda and dweight.
+// of dlambda and dweight, then the dq pass's.
+size_t dr_count(const basa_params &p, const WindowPlan &plan) {
+  int tiles = 0;
+  for (int t = 0; t < 8; ++t) tiles = std::max<int>(tiles, plan.type[t].n_tiles);
+  return 2 * size_t(p.B) * p.heads * make_geo(p).nWin * tiles;
+}
+
 size_t diff_attn_bwd_bf16_workspace(bool norm, const basa_params &p) {
   static thread_local WindowPlan plan;
   if (build_window_plan(p, &plan) != BASA_OK) return 0;
   const size_t g = norm ? align256(size_t(p.B) * p.heads * p.T * p.H * p.W * p.head_dim * 2) : 0;
-  return bwd_layout(p, plan, 2).total + g + align256(diff_prep_workspace(p));
+  return bwd_layout(p, plan, 2).total + g + align256(diff_prep_workspace(p)) + align256(dr_count(p, plan) * sizeof(float));
 }
 
 basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
@@ -1143,10 +1175,11 @@ basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *
   P.lambda = static_cast<const __nv_bfloat16 *>(dp.lambda);
   P.heads = p.heads;
   P.dk = static_cast<__nv_bfloat16 *>(dk);
-  st = launch_diff_prep(pre, second, lse, dout, dp, g, reinterpret_cast<float4 *>(ws), nullptr, dlambda, dweight,
-                        reinterpret_cast<float *>(part), p, s);
-  if (st != BASA_OK) return st;
-  return run_passes<true>(P, L, dk, dv, p, s);
+  P.dr = reinterpret_cast<float *>(part + align256(diff_prep_workspace(p)));
+  float *sums = reinterpret_cast<float *>(part);
+  st = launch_diff_prep(pre, second, lse, dout, dp, g, reinterpret_cast<float4 *>(ws), nullptr, sums, p, s);
+  if (st != BASA_OK || (st = run_passes<true>(P, L, dk, dv, p, s)) != BASA_OK) return st;
+  return launch_diff_sums(sums, P.dr, 2 * P.g.nWin * P.max_tiles, dp, dlambda, dweight, p, s);
 }
 
 }  // namespace basa

@@ -503,9 +503,9 @@ basa_status launch_diff_attn_bwd_f32(const void *q, const void *k, const void *v
   ws += align256(2 * rows * sizeof(float));
   float *g = reinterpret_cast<float *>(ws);
   if (dp.weight) ws += align256(rows * p.head_dim * sizeof(float));
-  basa_status st = launch_diff_prep(pre, second, lse, dout, dp, g, nullptr, drow, dlambda, dweight,
-                                    reinterpret_cast<float *>(ws), p, s);
-  if (st != BASA_OK) return st;
+  float *part = reinterpret_cast<float *>(ws);
+  basa_status st = launch_diff_prep(pre, second, lse, dout, dp, g, nullptr, drow, part, p, s);
+  if (st != BASA_OK || (st = launch_diff_sums(part, nullptr, 0, dp, dlambda, dweight, p, s)) != BASA_OK) return st;
   BwdArgs b{};
   b.lse = lse;
   b.dout = dp.weight ? g : static_cast<const float *>(dout);

@@ -7,6 +7,14 @@
 // prepare   the start of the backward: with xh = a r and G = gain * dout
 //             dweight = sum G xh,  g = r (G w - xh mean(G w xh)),
 //             D2 = g . O2,  D1 = g . O1 = g . a + lambda D2,  dlambda = -sum g . O2;
+//           the maps' outputs are rounded here, so D is a little off the rows' true sum
+//           R = sum_j P dP. The dq pass, which has P in float32, finds by how much: sum_j dS
+//           = R - D. And where a stands in for the true one, g is orthogonal to a up to eps
+//           (g . a = mean(G w xh) d eps r^2) but not to the true one, R1 - lambda R2, so with
+//           c = O2 . a / a . a what is summed is
+//             g . O2 - c (g . a) + c mean(G w xh) d eps r^2  +  (1 + c lambda) dR2 - c dR1
+//           (dR of the dq pass, weighted by the records). Maps that are nearly alike would
+//           otherwise leave dlambda 5% off, and a sum over rows that cancels 2%;
 //           g goes on as the output gradient of both maps (map 2's factor -lambda is put
 //           on its dq, dK and dV sums), D1 and D2 as their rows' softmax corrections.
 // reduce    the blocks' partial sums of dlambda and dweight, in a fixed order.
@@ -141,7 +149,7 @@ struct PrepArgs {
   const void *pre, *second, *dout, *lambda, *weight;
   const float *lse;  // [units][2][rows]
   void *g;           // [units][rows][d]; unused without weight (g = dout)
-  float4 *rec;       // nullable: records {-L log2 e, -D, 0, 0} [units][2][rows]
+  float4 *rec;       // nullable: records {-L log2 e, -D, weight of dR in -dlambda, 0} [units][2][rows]
   float *drow;       // nullable: D alone, [units][2][rows]
   float *part;       // [blocks][1 + d]: sum g . O2, then the weight's gradient
   int heads, blocks_per_unit;
@@ -174,11 +182,18 @@ __global__ void __launch_bounds__(kDiffThreads) diff_prep_kernel(const __grid_co
       load8(static_cast<const T *>(a.second) + at, o2);
       load8(static_cast<const T *>(a.dout) + at, g);
     }
+    float ga = 0.f, c2 = 0.f;  // this lane's part of g . a; c
     if (a.weight) {
-      float ss = 0.f, dot = 0.f, xh[8];
+      float ss = 0.f, so = 0.f, dot = 0.f, xh[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-      const float rms = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(x[i], x[i], ss);
+        so = fmaf(x[i], o2[i], so);
+      }
+      ss = row_sum<LPR>(ss);
+      so = row_sum<LPR>(so);
+      c2 = ss > 0.f ? so / ss : 0.f;
+      const float rms = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         xh[i] = x[i] * rms;
@@ -190,24 +205,30 @@ __global__ void __launch_bounds__(kDiffThreads) diff_prep_kernel(const __grid_co
       dot = row_sum<LPR>(dot) * (1.f / D);
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = rms * (g[i] - xh[i] * dot);
+      if (c == 0) ga = dot * (float(D) * a.eps * rms * rms);
+      dl = fmaf(c2, ga, dl);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ga = fmaf(g[i], x[i], ga);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dl = fmaf(g[i], o2[i], dl);
-    // D1 and D2 from the rounded g, which the products with V see: the rows of dS then
-    // sum to zero up to the products' own error
+    for (int i = 0; i < 8; ++i) dl = fmaf(g[i], fmaf(-c2, x[i], o2[i]), dl);
+    // D1 and D2 are those of the rounded g, which the products with V see
+    float d2 = 0.f, da = ga, g0[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g0[i] = g[i];
     if (a.weight && valid) store8(static_cast<T *>(a.g) + at, g);
-    float d2 = 0.f, da = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       d2 = fmaf(g[i], o2[i], d2);
-      da = fmaf(g[i], x[i], da);
+      da = fmaf(g[i] - g0[i], x[i], da);
     }
     d2 = row_sum<LPR>(d2);
     da = row_sum<LPR>(da);
     if (valid && c < 2) {
       const long long m = (2 * unit + c) * a.rows + r;
       const float d = c == 0 ? fmaf(lam, d2, da) : d2;
-      if (a.rec) a.rec[m] = make_float4(-a.lse[m] * 1.4426950408889634f, -d, 0.f, 0.f);
+      if (a.rec) a.rec[m] = make_float4(-a.lse[m] * 1.4426950408889634f, -d, c == 0 ? -c2 : fmaf(c2, lam, 1.f), 0.f);
       if (a.drow) a.drow[m] = d;
     }
   }
@@ -231,11 +252,12 @@ __global__ void __launch_bounds__(kDiffThreads) diff_prep_kernel(const __grid_co
   }
 }
 
-// One CTA per head: dlambda[h] = -(its blocks' sums); then one per 32 channels of dweight.
+// One CTA per head: dlambda[h] = -(its blocks' sums, and the dq pass's); then one per 32
+// channels of dweight.
 struct SumArgs {
-  const float *part;
+  const float *part, *dr;  // dr nullable: [B][heads][dr_per_unit] sums of weighted dR
   void *dlambda, *dweight;
-  int B, heads, blocks_per_unit, d;
+  int B, heads, blocks_per_unit, dr_per_unit, d;
 };
 
 template <typename T>
@@ -249,6 +271,10 @@ __global__ void __launch_bounds__(1024) diff_sum_kernel(const __grid_constant__ 
     for (int i = threadIdx.x; i < n; i += 1024) {
       const long long unit = (long long)(i / a.blocks_per_unit) * a.heads + blockIdx.x;
       s += a.part[(unit * a.blocks_per_unit + i % a.blocks_per_unit) * stride];
+    }
+    for (int b = 0; a.dr != nullptr && b < a.B; ++b) {
+      const float *p = a.dr + ((long long)b * a.heads + blockIdx.x) * a.dr_per_unit;
+      for (int i = threadIdx.x; i < a.dr_per_unit; i += 1024) s += p[i];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -317,8 +343,8 @@ size_t diff_prep_workspace(const basa_params &p) {
 }
 
 basa_status launch_diff_prep(const void *pre, const void *second, const float *lse, const void *dout,
-                             const basa_diff_params &dp, void *g, float4 *rec, float *drow, void *dlambda, void *dweight,
-                             float *part, const basa_params &p, cudaStream_t s) {
+                             const basa_diff_params &dp, void *g, float4 *rec, float *drow, float *part,
+                             const basa_params &p, cudaStream_t s) {
   PrepArgs a{};
   a.pre = pre;
   a.second = second;
@@ -340,8 +366,12 @@ basa_status launch_diff_prep(const void *pre, const void *second, const float *l
   if (p.dtype == BASA_BF16) diff_prep_kernel<__nv_bfloat16, 128><<<unsigned(blocks), kDiffThreads, 0, s>>>(a);
   else if (p.head_dim == 128) diff_prep_kernel<float, 128><<<unsigned(blocks), kDiffThreads, 0, s>>>(a);
   else diff_prep_kernel<float, 64><<<unsigned(blocks), kDiffThreads, 0, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
-  SumArgs r{part, dlambda, dweight, p.B, p.heads, a.blocks_per_unit, p.head_dim};
+  return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
+}
+
+basa_status launch_diff_sums(const float *part, const float *dr, int dr_per_unit, const basa_diff_params &dp,
+                             void *dlambda, void *dweight, const basa_params &p, cudaStream_t s) {
+  SumArgs r{part, dr, dlambda, dweight, p.B, p.heads, int(prep_blocks_per_unit(p)), dr_per_unit, p.head_dim};
   const unsigned ctas = unsigned(p.heads + (dp.weight ? p.head_dim / 32 : 0));
   if (p.dtype == BASA_BF16) diff_sum_kernel<__nv_bfloat16><<<ctas, 1024, 0, s>>>(r);
   else diff_sum_kernel<float><<<ctas, 1024, 0, s>>>(r);

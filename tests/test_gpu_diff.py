@@ -226,6 +226,39 @@ def test_text_rows(c):
     _assert_forward(c, out, ref, o1, o2, a1, a2, qt, k, lam64, w64)
 
 
+def test_gradient_of_lambda_where_the_maps_are_nearly_alike():
+    """Behind the norm only the part of O2 that is orthogonal to a counts. Each of its
+    channels is off by the probabilities' roundings (h / sqrt(3) of sqrt(sum P^2 v^2),
+    independent, of both maps over 1 - lambda) and by h / sqrt(3) of itself; 16 standard
+    deviations of the sum of g O2."""
+    c = Case("alike", "bf16", 1, 3, 128, (1, 32, 32), (1, 16, 16), (0, 8, 8))
+    q, k, v, lam, w, dout, gen = c.inputs(3)
+    rnd = lambda x, s: (x[:, 0::2] + s * torch.randn(x[:, 0::2].shape, generator=gen, device="cuda")).to(x.dtype)  # noqa: E731
+    q[:, 1::2], k[:, 1::2] = rnd(q, 0.05), rnd(k, 0.05)
+    v += 1  # a common part
+    layer = c.layer()
+    _, saved = layer.attention_train(q, k, v, lam, c.shift, w)
+    dlam = layer.backward(q, k, v, lam, c.shift, saved, dout, w)[3]
+    q64, k64, v64, lam64, w64, do64 = _f64(q, k, v, lam, w, dout)
+    ref = D.backward(q64, k64, v64, lam64, w64, c.geo, do64, gain=c.gain, eps=c.eps)[3]
+    _, rows = D.forward(q64, k64, v64, lam64, w64, c.geo, sizes=True)
+    ids = D.window_tokens(c.geo).cuda()
+    quad = torch.zeros_like(rows["o1"])
+    for b in range(c.B):
+        for j in range(c.heads):
+            for m in (0, 1):
+                p = torch.softmax(q64[b, 2 * j + m][ids] @ k64[b, 2 * j + m][ids].transpose(1, 2) / c.d**0.5, -1)
+                quad[b, j, ids.flatten()] += (p.square() @ v64[b, j][ids].square()).sqrt().flatten(0, 1)
+    a = rows["o1"] - lam64[:, None, None] * rows["o2"]
+    r = (a.square().mean(-1, keepdim=True) + c.eps).rsqrt()
+    xh, G = a * r, c.gain * do64 * w64
+    g = r * (G - xh * (G * xh).mean(-1, keepdim=True))
+    rest = rows["o2"] - (rows["o2"] * a).sum(-1, keepdim=True) / a.square().sum(-1, keepdim=True) * a
+    size = g.abs() * (quad / (1 - lam64)[:, None, None] + rest.abs())
+    bound = 16 * 2.0**-8 / 3**0.5 * size.square().sum((0, 2, 3)).sqrt() + 2.0**-8 * ref.abs()
+    assert ((dlam.double() - ref).abs() <= bound).all(), (dlam, ref, bound)
+
+
 def test_pooled_and_routed_keys():
     """The layer's own pooled keys and routes are those of the window layer's operators."""
     from sparse_window_attention_b200.layer import BasaLayer
