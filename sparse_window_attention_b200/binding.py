@@ -105,7 +105,7 @@ class basa_diff_params(ctypes.Structure):
 
 # basa_rope_tensor: x, its strides, y, its strides, dy, its strides, weight, dweight,
 # heads, rows, first_row, rotate
-_ROPE_TENSOR = struct.Struct("=Q3qQ3qQ3qQQ4i")
+rope_record = struct.Struct("=Q3qQ3qQ3qQQ4i").pack
 
 
 def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
@@ -205,6 +205,8 @@ def _stream(stream):
     if stream is None:
         import torch
 
+        if torch.cuda.is_initialized():
+            return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     return stream if isinstance(stream, int) else stream.cuda_stream
 
@@ -332,8 +334,8 @@ def rope_tensor(x, y, heads, rows, first_row=0, rotate=1, weight=None, dy=None, 
         s = strides[name] if isinstance(t, int) else t.stride()
         return _ptr(t), s[0], s[1], s[2]
 
-    return _ROPE_TENSOR.pack(*view("x", x), *view("y", y), *view("dy", dy), _ptr(weight) or 0, _ptr(dweight) or 0,
-                             heads, rows, first_row, rotate)
+    return rope_record(*view("x", x), *view("y", y), *view("dy", dy), _ptr(weight) or 0, _ptr(dweight) or 0,
+                       heads, rows, first_row, rotate)
 
 
 def basa_rope_table_bytes(rope_params: basa_rope_params, params: basa_params) -> int:

@@ -33,6 +33,7 @@ class BasaDiffLayer:
         self.dtype_name, self.dtype = dtype, torch.bfloat16 if dtype == "bf16" else torch.float32
         self.gain, self.eps = float(gain), float(eps)
         self.device = streams.resolve_device(device)
+        self.index = self.device.index
         T, H, W = self.grid
         self.N = T * H * W
         self.n_win = (T // window[0]) * (H // window[1]) * (W // window[2])
@@ -44,7 +45,7 @@ class BasaDiffLayer:
         self._params = {}
 
     def params(self, shift, heads=None, **extra) -> B.basa_params:
-        key = (tuple(shift), heads, tuple(sorted(extra.items())))
+        key = (tuple(shift), heads, tuple(sorted(extra.items())) if extra else ())
         if key not in self._params:
             self._params[key] = B.make_params(self.batch, heads or self.heads, self.head_dim, self.grid, self.window,
                                               shift, self.pool, self.n_text, self.routed_k, self.dtype_name,
@@ -53,12 +54,10 @@ class BasaDiffLayer:
 
     def _check(self, name, t, *shape, dtype=None):
         dtype = dtype or self.dtype
-        if t.dtype != dtype or t.device != self.device:
+        if t.dtype is not dtype or t.get_device() != self.index:
             raise ValueError(f"{name}: {dtype} on {self.device}, got {t.dtype} on {t.device}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name}: {shape}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous {shape}, got {tuple(t.shape)} with strides {t.stride()}")
 
     def _check_inputs(self, q, k, v, lam, weight, kp, vp, route_idx):
         b, h, d = self.batch, self.heads, self.head_dim

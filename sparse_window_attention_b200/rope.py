@@ -56,6 +56,7 @@ class GridRope:
         self.params = B.make_params(batch, 1, head_dim, self.grid, (1, 1, 1), n_text=n_text, dtype=dtype)
         self.rope_params = B.make_rope_params(self.axes, float(theta), PAIRS[pairs], origin, step)
         self.device = streams.resolve_device(device)
+        self.index, self.weight_shape = self.device.index, (head_dim,)
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("GridRope computes its tables when it is made: make it before a capture")
         nbytes = B.basa_rope_table_bytes(self.rope_params, self.params)
@@ -67,29 +68,43 @@ class GridRope:
             # the tables may be used on any stream from here on
             torch.cuda.current_stream().synchronize()
 
-    def _check(self, name, t, shape=None):
+    def _refuse(self, name, t, shape=None):
+        """Raises for a tensor that _fits turned down."""
         if t.dtype != self.dtype or t.device != self.device:
             raise ValueError(f"{name}: {self.dtype} on {self.device}, got {t.dtype} on {t.device}")
         if shape is None:
-            if t.dim() != 4 or t.shape[0] != self.batch or t.shape[3] != self.head_dim:
-                raise ValueError(f"{name}: [{self.batch}, heads, rows, {self.head_dim}], got {tuple(t.shape)}")
-        elif t.shape != shape:
-            raise ValueError(f"{name}: {tuple(shape)}, got {tuple(t.shape)}")
-        if t.stride(-1) != 1:
-            raise ValueError(f"{name}: channels must be contiguous")
+            shape = (self.batch, "heads", "rows", self.head_dim)
+        raise ValueError(f"{name}: {tuple(shape)} with contiguous channels, got {tuple(t.shape)} with strides {t.stride()}")
 
-    def _checked(self, part: RopePart):
-        self._check("x", part.x)
-        if part.weight is not None:
-            self._check("weight", part.weight, (self.head_dim,))
+    def _record(self, part: RopePart, dy=None, dx=None, dweight=None):
+        """The C record of a part, checked. Written out flat: it runs for every tensor of
+        every call, and a call of one token is bound by it."""
+        x, y, weight, first_row, rotate = part
+        dtype, index, shape, xs = self.dtype, self.index, x.shape, x.stride()
+        if (x.dtype is not dtype or x.get_device() != index or len(shape) != 4 or shape[0] != self.batch
+                or shape[3] != self.head_dim or xs[3] != 1):
+            self._refuse("x", x)
+        wp = 0
+        if weight is not None:
+            if weight.dtype is not dtype or weight.get_device() != index or weight.shape != self.weight_shape or weight.stride(0) != 1:
+                self._refuse("weight", weight, self.weight_shape)
+            wp = weight.data_ptr()
+        dp = ds0 = ds1 = ds2 = 0
+        name = "y"
+        if dy is not None:
+            ds0, ds1, ds2, ds3 = dy.stride() if dy.dim() == 4 else (0, 0, 0, 0)
+            if dy.dtype is not dtype or dy.get_device() != index or dy.shape != shape or ds3 != 1:
+                self._refuse("grads", dy, shape)
+            dp, y, name = dy.data_ptr(), dx, "dx"
+        ys = y.stride()
+        if y.dtype is not dtype or y.get_device() != index or y.shape != shape or ys[3] != 1:
+            self._refuse(name, y, shape)
+        return B.rope_record(x.data_ptr(), xs[0], xs[1], xs[2], y.data_ptr(), ys[0], ys[1], ys[2], dp, ds0, ds1, ds2, wp,
+                             0 if dweight is None else dweight.data_ptr(), shape[1], shape[2], first_row, 1 if rotate else 0)
 
     def forward(self, parts, stream=None):
         """Norm and rotation of every part in one launch; returns their ``y``."""
-        records = []
-        for p in parts:
-            self._checked(p)
-            self._check("y", p.y, p.x.shape)
-            records.append(B.rope_tensor(p.x, p.y, p.x.shape[1], p.x.shape[2], p.first_row, int(p.rotate), p.weight))
+        records = [self._record(p) for p in parts]
         with streams.on(self.device, stream):
             B.basa_rope_fwd(records, self.table, self.eps, self.rope_params, self.params)
         return [p.y for p in parts]
@@ -102,15 +117,9 @@ class GridRope:
         if not len(parts) == len(grads) == len(dx):
             raise ValueError("one gradient and one output for each part")
         with streams.on(self.device, stream):
-            records, dweights = [], []
-            for p, dy, out in zip(parts, grads, dx):
-                self._checked(p)
-                self._check("grads", dy, p.x.shape)
-                self._check("dx", out, p.x.shape)
-                dw = None if p.weight is None else torch.empty(self.head_dim, dtype=self.dtype, device=self.device)
-                dweights.append(dw)
-                records.append(B.rope_tensor(p.x, out, p.x.shape[1], p.x.shape[2], p.first_row, int(p.rotate), p.weight,
-                                             dy, dw))
+            dweights = [None if p.weight is None else torch.empty(self.head_dim, dtype=self.dtype, device=self.device)
+                        for p in parts]
+            records = [self._record(*r) for r in zip(parts, grads, dx, dweights)]
             nbytes = B.basa_rope_bwd_workspace_bytes(records, self.params)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
             B.basa_rope_bwd(records, self.table, self.eps, ws, self.rope_params, self.params)
