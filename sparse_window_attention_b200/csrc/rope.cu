@@ -10,20 +10,25 @@
 // (batch, head) units of its row: the angle tables are read once per row and not once
 // per head. A thread owns two 16-byte chunks of a row, half a head apart, so both
 // pairings (adjacent channels, or channel i with i + d/2) find their partners in the
-// thread's own registers, and the norm's sum of squares is a few shuffles.
+// thread's own registers, and the norm's sum of squares is a few shuffles. The arithmetic
+// is in packed float32 pairs, two channel pairs an instruction, with the norm's weight
+// multiplied into the cos and sin beforehand: element by element, and with the unit's
+// index divided out for every load, the kernel was bound by its instructions (half of
+// all issue slots, 4.6 TB/s).
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cmath>
 
 #include "basa_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace basa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-// Units a thread loads before it works on the first: 2 * 16 bytes each.
-constexpr int kUnroll = 4;
+// Units a thread loads before it works on the first: 2 * 16 bytes each (backward: twice that).
+constexpr int kUnrollFwd = 4, kUnrollBwd = 2, kUnrollCopy = 8;
 
 struct RopeTensorArgs {
   const void *x, *dy, *weight;
@@ -49,48 +54,68 @@ struct Vec {
   static constexpr int n = 16 / sizeof(T);
 };
 
-__device__ __forceinline__ void unpack(const uint4 &u, float *v, const __nv_bfloat16 *) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// A thread's channels: VEC pairs (a, b), held as VEC / 2 packed float32 pairs of a's and
+// of b's. With HALVES the first chunk holds the a's and the second the b's; with adjacent
+// pairs each 32-bit word of bfloat16 (or each two floats) is a pair.
+template <bool HALVES>
+__device__ __forceinline__ void unpack(const uint4 &u, const uint4 &v, uint64_t *a, uint64_t *b, const __nv_bfloat16 *) {
+  const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  const auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
+  const auto hi = [](uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    a[i] = HALVES ? ptx::f2_pack(lo(w[i]), hi(w[i])) : ptx::f2_pack(lo(w[2 * i]), lo(w[2 * i + 1]));
+    b[i] = HALVES ? ptx::f2_pack(lo(w[4 + i]), hi(w[4 + i])) : ptx::f2_pack(hi(w[2 * i]), hi(w[2 * i + 1]));
   }
 }
-__device__ __forceinline__ void unpack(const uint4 &u, float *v, const float *) {
-  v[0] = __uint_as_float(u.x);
-  v[1] = __uint_as_float(u.y);
-  v[2] = __uint_as_float(u.z);
-  v[3] = __uint_as_float(u.w);
+template <bool HALVES>
+__device__ __forceinline__ void unpack(const uint4 &u, const uint4 &v, uint64_t *a, uint64_t *b, const float *) {
+  const auto f = [](uint32_t x) { return __uint_as_float(x); };
+  a[0] = HALVES ? ptx::f2_pack(f(u.x), f(u.y)) : ptx::f2_pack(f(u.x), f(u.z));
+  a[1] = HALVES ? ptx::f2_pack(f(u.z), f(u.w)) : ptx::f2_pack(f(v.x), f(v.z));
+  b[0] = HALVES ? ptx::f2_pack(f(v.x), f(v.y)) : ptx::f2_pack(f(u.y), f(u.w));
+  b[1] = HALVES ? ptx::f2_pack(f(v.z), f(v.w)) : ptx::f2_pack(f(v.y), f(v.w));
 }
 // The only rounding: float32 results to the element type, to nearest even.
-__device__ __forceinline__ uint4 pack(const float *v, const __nv_bfloat16 *) {
-  uint32_t r[4];
+template <bool HALVES>
+__device__ __forceinline__ void pack(const uint64_t *a, const uint64_t *b, uint4 &u, uint4 &v, const __nv_bfloat16 *) {
+  uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
-  return make_uint4(r[0], r[1], r[2], r[3]);
+  for (int i = 0; i < 4; ++i) {
+    float a0, a1, b0, b1;
+    ptx::f2_unpack(a[i], a0, a1);
+    ptx::f2_unpack(b[i], b0, b1);
+    w[HALVES ? i : 2 * i] = HALVES ? ptx::pack_bf16x2(a0, a1) : ptx::pack_bf16x2(a0, b0);
+    w[HALVES ? 4 + i : 2 * i + 1] = HALVES ? ptx::pack_bf16x2(b0, b1) : ptx::pack_bf16x2(a1, b1);
+  }
+  u = make_uint4(w[0], w[1], w[2], w[3]);
+  v = make_uint4(w[4], w[5], w[6], w[7]);
 }
-__device__ __forceinline__ uint4 pack(const float *v, const float *) {
-  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+template <bool HALVES>
+__device__ __forceinline__ void pack(const uint64_t *a, const uint64_t *b, uint4 &u, uint4 &v, const float *) {
+  float x[8];  // a0 a1 a2 a3 b0 b1 b2 b3
+  ptx::f2_unpack(a[0], x[0], x[1]);
+  ptx::f2_unpack(a[1], x[2], x[3]);
+  ptx::f2_unpack(b[0], x[4], x[5]);
+  ptx::f2_unpack(b[1], x[6], x[7]);
+  const auto w = [&](int i) { return __float_as_uint(x[i]); };
+  u = HALVES ? make_uint4(w(0), w(1), w(2), w(3)) : make_uint4(w(0), w(4), w(1), w(5));
+  v = HALVES ? make_uint4(w(4), w(5), w(6), w(7)) : make_uint4(w(2), w(6), w(3), w(7));
 }
 
-// Pair index of a thread's i-th pair (chunk column c): its channels are v[i] and
-// v[VEC + i] when the pairs are halves, v[2i] and v[2i + 1] when they are adjacent.
+// Pair index of a thread's i-th pair (chunk column c).
 template <int D, int VEC, bool HALVES>
 __device__ __forceinline__ int pair_index(int c, int i) {
   if (HALVES) return VEC * c + i;
   return i < VEC / 2 ? VEC / 2 * c + i : D / 4 + VEC / 2 * c + (i - VEC / 2);
 }
 
-template <int VEC, bool HALVES>
-__device__ __forceinline__ void rotate_pairs(float *v, const float *cs, const float *sn) {
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    float &a = v[HALVES ? i : 2 * i], &b = v[HALVES ? VEC + i : 2 * i + 1];
-    const float ra = a * cs[i] - b * sn[i], rb = a * sn[i] + b * cs[i];
-    a = ra;
-    b = rb;
-  }
+__device__ __forceinline__ uint64_t f2_both(float x) { return ptx::f2_pack(x, x); }
+__device__ __forceinline__ uint64_t f2_neg(uint64_t x) { return x ^ 0x8000000080000000ull; }
+__device__ __forceinline__ float f2_sum(uint64_t x) {
+  float a, b;
+  ptx::f2_unpack(x, a, b);
+  return a + b;
 }
 
 // Sum over the LPR lanes that share a row (aligned groups of lanes).
@@ -101,12 +126,13 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// cos and sin of a thread's pairs in row `row` of the key sequence; the backward turns
-// the other way. Pairs behind the axes' channels are left as they are.
-template <int D, int VEC, bool HALVES, bool BWD>
-__device__ __forceinline__ void load_angles(const RopeArgs &a, int row, int c, float *cs, float *sn) {
+// cos and sin of a thread's pairs in row `row` of the key sequence. Pairs behind the axes'
+// channels are left as they are.
+template <int D, int VEC, bool HALVES>
+__device__ __forceinline__ void load_angles(const RopeArgs &a, int row, int c, uint64_t *cs, uint64_t *sn) {
   const int P = a.nt + a.nh + a.nw;
   const int t = row / (a.H * a.W), y = (row / a.W) % a.H, x = row % a.W;
+  float co[VEC], si[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
     const int p = pair_index<D, VEC, HALVES>(c, i);
@@ -117,10 +143,34 @@ __device__ __forceinline__ void load_angles(const RopeArgs &a, int row, int c, f
     else at = a.tab_x + (long long)x * a.nw + (p - a.nt - a.nh);
     float2 e = make_float2(1.f, 0.f);
     if (p < P) e = __ldg(a.table + at);
-    cs[i] = e.x;
-    sn[i] = BWD ? -e.y : e.y;
+    co[i] = e.x;
+    si[i] = e.y;
+  }
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) {
+    cs[i] = ptx::f2_pack(co[2 * i], co[2 * i + 1]);
+    sn[i] = ptx::f2_pack(si[2 * i], si[2 * i + 1]);
   }
 }
+
+// The walk over a group's (batch, head) units: element offsets without a division a step.
+struct UnitWalk {
+  long long at, step, wrap;
+  int h, heads;
+  __device__ UnitWalk(const long long *stride, int unit, int n_heads) {
+    heads = n_heads;
+    h = unit % n_heads;
+    at = (unit / n_heads) * stride[0] + h * stride[1];
+    step = stride[1];
+    wrap = stride[0] - (n_heads - 1) * stride[1];
+  }
+  __device__ __forceinline__ long long next() {
+    const long long here = at;
+    at += ++h == heads ? wrap : step;
+    if (h == heads) h = 0;
+    return here;
+  }
+};
 
 // One CTA = (tensor, block of 256 / LPR rows, group of (batch, head) units); a thread
 // owns chunk column c of one row and walks the group's units.
@@ -130,8 +180,8 @@ __device__ __forceinline__ void load_angles(const RopeArgs &a, int row, int c, f
 // dx = r * (g w - xh * mean(g w * xh)). Each block sums its rows' weight gradients in a
 // fixed order; rope_dweight_kernel adds the blocks, so nothing depends on timing.
 template <typename T, int D, bool HALVES, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int VEC = Vec<T>::n, LPR = D / 2 / VEC, ROWS = kRopeThreads / LPR;
+__global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int VEC = Vec<T>::n, LPR = D / 2 / VEC, ROWS = kRopeThreads / LPR, H2 = VEC / 2;
   int ti = 0;
   while (ti + 1 < a.n && int(blockIdx.x) >= a.t[ti + 1].first_block) ++ti;
   const RopeTensorArgs &t = a.t[ti];
@@ -141,112 +191,172 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int r = (blk % t.row_blocks) * ROWS + threadIdx.x / LPR;
   const bool valid = r < t.rows;
   const bool norm = t.weight != nullptr;
-  const int u0 = group * t.group_units, u1 = min(u0 + t.group_units, a.B * t.heads);
+  const int u0 = group * t.group_units, n_units = min(t.group_units, a.B * t.heads - u0);
   const T *kind = nullptr;
+  // A row past the end reads row 0 (shuffles want every lane) and writes nothing.
+  const long long row = valid ? r : 0;
+  const T *x0 = static_cast<const T *>(t.x) + row * t.xs[2] + c * VEC;
+  T *y0 = static_cast<T *>(t.y) + row * t.ys[2] + c * VEC;
+  const T *d0 = static_cast<const T *>(t.dy) + row * t.ds[2] + c * VEC;
+  UnitWalk yw(t.ys, u0, t.heads);
+  const auto load = [](const T *p, uint4 &u, uint4 &v) {
+    u = __ldcs(reinterpret_cast<const uint4 *>(p));
+    v = __ldcs(reinterpret_cast<const uint4 *>(p + D / 2));
+  };
+  const auto store = [&](const uint4 &u, const uint4 &v) {
+    T *p = y0 + yw.next();
+    if (valid) {
+      *reinterpret_cast<uint4 *>(p) = u;
+      *reinterpret_cast<uint4 *>(p + D / 2) = v;
+    }
+  };
 
-  float cs[VEC], sn[VEC], w[2 * VEC], dw[2 * VEC];
+  if (!norm && !t.rotate) {  // a tensor that is only laid out: its bits
+    const T *s0 = BWD ? d0 : x0;
+    UnitWalk sw(BWD ? t.ds : t.xs, u0, t.heads);
+    for (int u = 0; u < n_units; u += kUnrollCopy) {
+      uint4 p[kUnrollCopy], q[kUnrollCopy];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
+      for (int k = 0; k < kUnrollCopy; ++k)
+        if (u + k < n_units) load(s0 + sw.next(), p[k], q[k]);
+#pragma unroll
+      for (int k = 0; k < kUnrollCopy; ++k)
+        if (u + k < n_units) store(p[k], q[k]);
+    }
+    return;
   }
-  if (t.rotate && valid) load_angles<D, VEC, HALVES, BWD>(a, t.first_row + r, c, cs, sn);
+
+  uint64_t cs[H2], sn[H2], wa[H2], wb[H2];
+#pragma unroll
+  for (int i = 0; i < H2; ++i) {
+    cs[i] = wa[i] = wb[i] = f2_both(1.f);
+    sn[i] = f2_both(0.f);
+  }
+  if (t.rotate) load_angles<D, VEC, HALVES>(a, t.first_row + int(row), c, cs, sn);
   if (norm) {
     const uint4 *wp = reinterpret_cast<const uint4 *>(t.weight);
-    unpack(__ldg(wp + c), w, kind);
-    unpack(__ldg(wp + LPR + c), w + VEC, kind);
+    unpack<HALVES>(__ldg(wp + c), __ldg(wp + LPR + c), wa, wb, kind);
   }
-#pragma unroll
-  for (int i = 0; i < 2 * VEC; ++i) dw[i] = 0.f;
+  UnitWalk xw(t.xs, u0, t.heads);
 
-  const T *x0 = static_cast<const T *>(t.x) + (long long)r * t.xs[2] + c * VEC;
-  T *y0 = static_cast<T *>(t.y) + (long long)r * t.ys[2] + c * VEC;
-  const T *d0 = static_cast<const T *>(t.dy) + (long long)r * t.ds[2] + c * VEC;
-  // Both loops below have the same trip count in every lane (shuffles).
-  for (int u = u0; u < u1; u += kUnroll) {
-    uint4 xa[kUnroll], xb[kUnroll], ga[kUnroll], gb[kUnroll];
+  if (!BWD) {
+    // y_a = x_a (w_a cos) - x_b (w_b sin), y_b = x_a (w_a sin) + x_b (w_b cos), times r
+    uint64_t ac[H2], as[H2], bc[H2], bs[H2];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      xa[k] = xb[k] = ga[k] = gb[k] = make_uint4(0, 0, 0, 0);
-      if (!valid || u + k >= u1) continue;
-      const int b = (u + k) / t.heads, h = (u + k) % t.heads;
-      if (!BWD || norm) {
-        const T *p = x0 + b * t.xs[0] + h * t.xs[1];
-        xa[k] = __ldcs(reinterpret_cast<const uint4 *>(p));
-        xb[k] = __ldcs(reinterpret_cast<const uint4 *>(p + D / 2));
-      }
-      if (BWD) {
-        const T *p = d0 + b * t.ds[0] + h * t.ds[1];
-        ga[k] = __ldcs(reinterpret_cast<const uint4 *>(p));
-        gb[k] = __ldcs(reinterpret_cast<const uint4 *>(p + D / 2));
+    for (int i = 0; i < H2; ++i) {
+      ac[i] = ptx::fmul2(wa[i], cs[i]);
+      as[i] = ptx::fmul2(wa[i], sn[i]);
+      bc[i] = ptx::fmul2(wb[i], cs[i]);
+      bs[i] = f2_neg(ptx::fmul2(wb[i], sn[i]));
+    }
+    for (int u = 0; u < n_units; u += kUnrollFwd) {
+      uint4 p[kUnrollFwd], q[kUnrollFwd];
+#pragma unroll
+      for (int k = 0; k < kUnrollFwd; ++k)
+        if (u + k < n_units) load(x0 + xw.next(), p[k], q[k]);
+#pragma unroll
+      for (int k = 0; k < kUnrollFwd; ++k) {
+        if (u + k >= n_units) break;
+        uint64_t xa[H2], xb[H2];
+        unpack<HALVES>(p[k], q[k], xa, xb, kind);
+        if (norm) {
+          uint64_t ss = f2_both(0.f);
+#pragma unroll
+          for (int i = 0; i < H2; ++i) ss = ptx::ffma2(xb[i], xb[i], ptx::ffma2(xa[i], xa[i], ss));
+          const uint64_t rms = f2_both(rsqrtf(row_sum<LPR>(f2_sum(ss)) * (1.f / D) + a.eps));
+#pragma unroll
+          for (int i = 0; i < H2; ++i) {
+            xa[i] = ptx::fmul2(xa[i], rms);
+            xb[i] = ptx::fmul2(xb[i], rms);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < H2; ++i) {
+          const uint64_t ya = ptx::ffma2(xa[i], ac[i], ptx::fmul2(xb[i], bs[i]));
+          xb[i] = ptx::ffma2(xa[i], as[i], ptx::fmul2(xb[i], bc[i]));
+          xa[i] = ya;
+        }
+        pack<HALVES>(xa, xb, p[k], q[k], kind);
+        store(p[k], q[k]);
       }
     }
+    return;
+  }
+
+  uint64_t dwa[H2], dwb[H2];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      if (u + k >= u1) break;
-      float v[2 * VEC], g[2 * VEC];
-      if (!BWD || norm) {
-        unpack(xa[k], v, kind);
-        unpack(xb[k], v + VEC, kind);
+  for (int i = 0; i < H2; ++i) dwa[i] = dwb[i] = f2_both(0.f);
+  UnitWalk dw(t.ds, u0, t.heads);
+  for (int u = 0; u < n_units; u += kUnrollBwd) {
+    uint4 p[kUnrollBwd], q[kUnrollBwd], gp[kUnrollBwd], gq[kUnrollBwd];
+#pragma unroll
+    for (int k = 0; k < kUnrollBwd; ++k) {
+      if (u + k >= n_units) break;
+      if (norm) load(x0 + xw.next(), p[k], q[k]);
+      load(d0 + dw.next(), gp[k], gq[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnrollBwd; ++k) {
+      if (u + k >= n_units) break;
+      uint64_t ga[H2], gb[H2];
+      unpack<HALVES>(gp[k], gq[k], ga, gb, kind);
+#pragma unroll
+      for (int i = 0; i < H2; ++i) {  // the turn by -angle
+        const uint64_t g = ptx::ffma2(ga[i], cs[i], ptx::fmul2(gb[i], sn[i]));
+        gb[i] = ptx::ffma2(gb[i], cs[i], ptx::fmul2(ga[i], f2_neg(sn[i])));
+        ga[i] = g;
       }
-      float rms = 0.f;
       if (norm) {
-        float ss = 0.f;
+        uint64_t xa[H2], xb[H2], ss = f2_both(0.f), dot = f2_both(0.f);
+        unpack<HALVES>(p[k], q[k], xa, xb, kind);
 #pragma unroll
-        for (int i = 0; i < 2 * VEC; ++i) ss = fmaf(v[i], v[i], ss);
-        rms = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
-      }
-      if (!BWD) {
-        if (norm) {
+        for (int i = 0; i < H2; ++i) ss = ptx::ffma2(xb[i], xb[i], ptx::ffma2(xa[i], xa[i], ss));
+        const float rms = rsqrtf(row_sum<LPR>(f2_sum(ss)) * (1.f / D) + a.eps);
+        const uint64_t rms2 = f2_both(valid ? rms : 0.f);  // a row past the end adds nothing to dweight
 #pragma unroll
-          for (int i = 0; i < 2 * VEC; ++i) v[i] = v[i] * rms * w[i];
+        for (int i = 0; i < H2; ++i) {
+          const uint64_t pa = ptx::fmul2(ga[i], xa[i]), pb = ptx::fmul2(gb[i], xb[i]);
+          dwa[i] = ptx::ffma2(pa, rms2, dwa[i]);
+          dwb[i] = ptx::ffma2(pb, rms2, dwb[i]);
+          dot = ptx::ffma2(pb, wb[i], ptx::ffma2(pa, wa[i], dot));
         }
-        if (t.rotate) rotate_pairs<VEC, HALVES>(v, cs, sn);
-      } else {
-        unpack(ga[k], g, kind);
-        unpack(gb[k], g + VEC, kind);
-        if (t.rotate) rotate_pairs<VEC, HALVES>(g, cs, sn);
-        if (norm) {
-          float dot = 0.f;
+        // dx = r g w - x r^3 mean(g w x)
+        const float mean = row_sum<LPR>(f2_sum(dot)) * (1.f / D);
+        const uint64_t kx = f2_both(-(rms * rms) * (rms * mean));
 #pragma unroll
-          for (int i = 0; i < 2 * VEC; ++i) {
-            v[i] *= rms;
-            dw[i] = fmaf(g[i], v[i], dw[i]);
-            g[i] *= w[i];
-            dot = fmaf(g[i], v[i], dot);
-          }
-          dot = row_sum<LPR>(dot) * (1.f / D);
-#pragma unroll
-          for (int i = 0; i < 2 * VEC; ++i) g[i] = rms * (g[i] - v[i] * dot);
+        for (int i = 0; i < H2; ++i) {
+          ga[i] = ptx::ffma2(xa[i], kx, ptx::fmul2(ptx::fmul2(ga[i], wa[i]), rms2));
+          gb[i] = ptx::ffma2(xb[i], kx, ptx::fmul2(ptx::fmul2(gb[i], wb[i]), rms2));
         }
-#pragma unroll
-        for (int i = 0; i < 2 * VEC; ++i) v[i] = g[i];
       }
-      if (valid) {
-        const int b = (u + k) / t.heads, h = (u + k) % t.heads;
-        T *p = y0 + b * t.ys[0] + h * t.ys[1];
-        *reinterpret_cast<uint4 *>(p) = pack(v, kind);
-        *reinterpret_cast<uint4 *>(p + D / 2) = pack(v + VEC, kind);
+      pack<HALVES>(ga, gb, gp[k], gq[k], kind);
+      store(gp[k], gq[k]);
+    }
+  }
+  if (t.part == nullptr) return;  // the same in the whole block
+  __shared__ float red[kRopeThreads / 32][D];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+  for (int i = 0; i < H2; ++i) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float v[2];
+      ptx::f2_unpack(half ? dwb[i] : dwa[i], v[0], v[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = LPR; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xFFFFFFFFu, v[e], o);
+        const int pair = pair_index<D, VEC, HALVES>(c, 2 * i + e);
+        if (lane < LPR) red[warp][HALVES ? pair + half * (D / 2) : 2 * pair + half] = v[e];
       }
     }
   }
-  if (BWD) {
-    if (t.part == nullptr) return;  // the same in the whole block
-    __shared__ float red[kRopeThreads / 32][D];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * VEC; ++i) {
-#pragma unroll
-      for (int o = LPR; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xFFFFFFFFu, dw[i], o);
-      if (lane < LPR) red[warp][(i < VEC ? 0 : D / 2) + c * VEC + i % VEC] = dw[i];
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float s = 0.f;
-#pragma unroll
-      for (int k = 0; k < kRopeThreads / 32; ++k) s += red[k][threadIdx.x];
-      t.part[(long long)blk * D + threadIdx.x] = s;
-    }
+    for (int k = 0; k < kRopeThreads / 32; ++k) s += red[k][threadIdx.x];
+    t.part[(long long)blk * D + threadIdx.x] = s;
   }
 }
 
