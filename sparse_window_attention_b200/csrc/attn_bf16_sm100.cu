@@ -25,18 +25,8 @@
 // the window, pooled or text segments from the key stream, and an optional
 // epilogue writes each query row's log-sum-exp; and the text-query rows, where the
 // queries are 128-row boxes of the text rows and the key stream is every k/v row,
-// split over CTA groups whose partial results are merged by log-sum-exp.
-//
-// Differential form (FORM kDiff): out = softmax(q1 K1^T) V - lambda
-// softmax(q2 K2^T) V over the same key list, optionally RMS-normalised per row. The two
-// softmax groups take the two maps of ONE query tile instead of two query tiles: key
-// tiles come in pairs K1, K2 and one V tile serves both maps, so a key step loads three
-// tiles for the same four MMAs. Each map is normalised by its own sum only at the end,
-// so both products with V are needed (P1/l1 - lambda P2/l2 is not known while the sums
-// run); the difference and the norm are taken from TMEM in float32 and rounded once.
-// For a backward the difference before the norm and the second map's output are stored
-// too: with those two, rounded relative to their own size, the first map's follows as
-// their sum, where a difference of two rounded maps would lose what cancels in it.
+// split over CTA groups whose partial results are merged by log-sum-exp. With PART the
+// text rows' (partial) outputs leave in float32, for a difference of maps taken afterwards.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -45,18 +35,12 @@
 #include <cstring>
 #include <mutex>
 
-#include "attn_sm100_common.cuh"
-#include "basa_internal.h"
-#include "sm100_ptx.cuh"
+#include "attn_fwd_sm100.cuh"
 
 namespace basa {
 namespace {
 
-using sm100::kHalfBytes;
-using sm100::kTileBytes;
-using sm100::kTileDesc;
-using sm100::Waiter;
-using sm100::wrap;
+using namespace sm100;
 
 // 12 warps = three warpgroups: warp 0 loads, warp 1 issues MMAs (warps 2-3 idle),
 // warps 4-7 and 8-11 run the softmax of query tile 0 and 1. Each SM sub-partition
@@ -74,224 +58,22 @@ constexpr uint32_t kSmemBytes = kSmemMask + kMaskTable * 16 + 1024;  // + alignm
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxTextSplits = 8;  // key-range splits of the text-query rows
 
-struct alignas(64) AttnParams {
-  CUtensorMap map_q[kMaxShapes];
-  CUtensorMap map_k[kMaxShapes];
-  CUtensorMap map_v[kMaxShapes];
-  CUtensorMap map_o[kMaxShapes];
-  CUtensorMap map_kp, map_vp, map_kt, map_vt;
-  CUtensorMap map_kp8, map_vp8;  // pooled rows in 8-row boxes (the pooled tail, see below)
-  CUtensorMap map_qd, map_od;  // text-query mode: query rows and output rows (d, row, b*head)
-  CUtensorMap map_pre[kMaxShapes], map_o2[kMaxShapes];  // differential form: what a backward needs
-  WindowPlan plan;
-  const int32_t *route;
-  int32_t *dev_err;
-  Geo g;
-  int routed_k, n_pool, n_text, n_pool_tiles, n_text_tiles;
-  // Pooled tail: when the pooled keys past the last full 128-row tile (pool_tail rows,
-  // at most 16) fit in free 8-row blocks of the own window's key tile tail_tile[type],
-  // they are loaded there (8-row boxes at rows tail_dest[type][b]) instead of taking a
-  // key tile of their own; tail_mask[type] marks their rows.
-  int pool_tail, tail_blocks;
-  int8_t tail_tile[8];
-  uint8_t tail_dest[8][2];
-  uint32_t tail_mask[8][4];
-  float scale_log2;
-  int use_windows;  // own and routed windows are keys (else pooled and/or text only)
-  // Text-query mode: the queries are the n_text text rows and attend densely to
-  // every k/v row, which are streamed as the "text" segment starting at row 0.
-  // The key tiles are split into n_splits ranges, one per CTA group.
-  int dense, dense_rows, dense_q_tiles, dense_pairs, n_splits, split_tiles, bh_count;
-  int text_row0;  // first k/v row of the text segment: N (window mode) or 0
-  float *lse;       // nullable: log-sum-exp of each query row's scaled scores [B*heads][N]
-  int all_full;  // every key tile of the launch is full: no column masks
-  int v_shift;   // v and vp belong to unit bh >> v_shift (two maps that share their values)
-  // differential form: a CTA's unit is a (batch, differential head); map g's q, k, kp are unit 2 * unit + g
-  const __nv_bfloat16 *lambda, *norm_weight;  // [heads]; nullable [128]
-  int heads, store_pre, store_o2;
-  float gain, eps;
-  float *part;  // FORM kPart: float32 outputs [split][b*head][n_text][128]
-  uint32_t flags;
-  unsigned long long timeout_ns;
-};
-
-// __grid_constant__ kernel parameters are limited to 32764 bytes.
-static_assert(sizeof(AttnParams) <= 32764, "window plan too large for the kernel parameter space");
-
 struct Ctrl {
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
   uint32_t tmem_base;
   int abort;
-  int tile0, ntile;  // text-query mode: this CTA's range of key tiles
-  int wtype[1 + kMaxRouted];
-  int org[1 + kMaxRouted][3];
+  KeyList keys;
 };
 static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block too large");
 
-// Position in the key-tile stream: segments 0..routed_k are windows (own, then
-// routed), then the pooled tokens, then the text tokens.
-struct KeyIter {
-  int seg, t;
-};
 
-__device__ __forceinline__ int seg_tiles(const AttnParams &P, const Ctrl &c, int seg) {
-  if (seg <= P.routed_k) return P.use_windows ? P.plan.type[c.wtype[seg]].n_tiles : 0;
-  if (seg == P.routed_k + 1) return P.n_pool_tiles;
-  return P.dense ? c.ntile : P.n_text_tiles;
-}
-__device__ __forceinline__ void advance(const AttnParams &P, const Ctrl &c, KeyIter &it) {
-  ++it.t;
-  while (it.seg <= P.routed_k + 2 && it.t >= seg_tiles(P, c, it.seg)) {
-    ++it.seg;
-    it.t = 0;
-  }
-}
-
-// First key tile of the stream (segments without tiles are skipped).
-__device__ __forceinline__ KeyIter first_key(const AttnParams &P, const Ctrl &c) {
-  KeyIter it{0, 0};
-  while (it.seg <= P.routed_k + 2 && seg_tiles(P, c, it.seg) == 0) ++it.seg;
-  return it;
-}
-
-// The own window's key tile that also carries the pooled tail.
-__device__ __forceinline__ bool has_pool_tail(const AttnParams &P, const Ctrl &c, const KeyIter &it) {
-  return P.pool_tail > 0 && it.seg == 0 && it.t == P.tail_tile[c.wtype[0]];
-}
-
-// Bytes the TMA loads of one key (or value) tile deliver.
-__device__ __forceinline__ uint32_t key_tile_bytes(const AttnParams &P, const Ctrl &c, const KeyIter &it) {
-  if (it.seg > P.routed_k) return kTileBytes;  // whole 128-row boxes (rows past the end read as zero)
-  uint32_t b = uint32_t(P.plan.tile[P.plan.type[c.wtype[it.seg]].first_tile + it.t].valid_rows) * 256u;
-  if (has_pool_tail(P, c, it)) b += uint32_t(P.tail_blocks) * 8u * 256u;
-  return b;
-}
-
-__device__ __forceinline__ uint32_t load_key_tile(const AttnParams &P, const Ctrl &c, const KeyIter &it, bool is_v,
-                                                  int bh, uint8_t *dst, uint64_t *bar) {
-  if (it.seg <= P.routed_k) {
-    const PlanTile &tile = P.plan.tile[P.plan.type[c.wtype[it.seg]].first_tile + it.t];
-    uint32_t b = sm100::load_window_tile(P.plan, P.g, is_v ? P.map_v : P.map_k, tile, c.org[it.seg], bh, dst, bar);
-    if (has_pool_tail(P, c, it)) {
-      const CUtensorMap *map = is_v ? &P.map_vp8 : &P.map_kp8;
-      for (int i = 0; i < P.tail_blocks; ++i) {
-        uint8_t *d = dst + uint32_t(P.tail_dest[c.wtype[0]][i]) * 128u;
-        const int row = P.n_pool_tiles * kTileRows + 8 * i;  // rows past n_pool read as zero
-        ptx::tma_load_3d(d, map, bar, 0, row, bh);
-        ptx::tma_load_3d(d + kHalfBytes, map, bar, 64, row, bh);
-        b += 8u * 256u;
-      }
-    }
-    return b;
-  }
-  const bool pooled = it.seg == P.routed_k + 1;
-  const CUtensorMap *map = pooled ? (is_v ? &P.map_vp : &P.map_kp) : (is_v ? &P.map_vt : &P.map_kt);
-  const int row = pooled ? it.t * kTileRows : P.text_row0 + (c.tile0 + it.t) * kTileRows;
-  ptx::tma_load_3d(dst, map, bar, 0, row, bh);
-  ptx::tma_load_3d(dst + kHalfBytes, map, bar, 64, row, bh);
-  return kTileBytes;
-}
-
-// Column mask of a key tile; returns true when all 128 rows hold keys.
-__device__ __forceinline__ bool key_tile_mask(const AttnParams &P, const Ctrl &c, const KeyIter &it, uint32_t *m) {
-  if (it.seg <= P.routed_k) {
-    const PlanTile &tile = P.plan.tile[P.plan.type[c.wtype[it.seg]].first_tile + it.t];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = tile.mask[i];
-    if (has_pool_tail(P, c, it)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m[i] |= P.tail_mask[c.wtype[0]][i];
-      return false;
-    }
-    return tile.valid_rows == kTileRows;
-  }
-  const bool pooled = it.seg == P.routed_k + 1;
-  const int total = pooled ? P.n_pool : (P.dense ? P.dense_rows : P.n_text);
-  const int valid = min(kTileRows, total - (pooled ? it.t : c.tile0 + it.t) * kTileRows);
-  sm100::prefix_mask(valid, m);
-  return valid == kTileRows;
-}
-
-// The running row max is only raised when a tile's max exceeds it by more than
-// 2^8 (log2 units); otherwise the old max is kept and P values up to 256 are
-// produced, which float32 sums and bfloat16 P hold exactly as well. This skips
-// most rescales of the O accumulator in TMEM.
-constexpr float kRescaleLog2 = 8.0f;
-// P = 2^x (x = s * scale_log2 - m) for the 128 scores of a row (MUFU ex2), written
-// in place as the 64 bfloat16 pairs the P V MMA reads (s[i] = pair (2i, 2i+1), low
-// half = even key); each pair is packed as soon as it is computed, so the live
-// register set shrinks along the row. Returns the float32 row sum.
-__device__ __forceinline__ float exp2_row_packed(uint32_t (&s)[128], float scale_log2, float m) {
-  using namespace ptx;
-  const uint64_t sc2 = f2_pack(scale_log2, scale_log2), negm2 = f2_pack(-m, -m);
-  uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-  for (int pr = 0; pr < 64; ++pr) {
-    const uint64_t x = ffma2(f2_pack(__uint_as_float(s[2 * pr]), __uint_as_float(s[2 * pr + 1])), sc2, negm2);
-    float x0, x1;
-    f2_unpack(x, x0, x1);
-    const float r0 = ex2(x0), r1 = ex2(x1);
-    const uint64_t pp = f2_pack(r0, r1);
-    if (pr & 1) acc1 = fadd2(acc1, pp);
-    else acc0 = fadd2(acc0, pp);
-    s[pr] = pack_bf16x2(r0, r1);  // s[pr] was read at pair pr / 2
-  }
-  float a, b, c, d;
-  f2_unpack(acc0, a, b);
-  f2_unpack(acc1, c, d);
-  return (a + b) + (c + d);
-}
-
-// Row max of the N entries of s (raw scores).
-template <int N>
-__device__ __forceinline__ float row_max(const uint32_t (&s)[N]) {
-  float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]), c = __uint_as_float(s[2]), d = __uint_as_float(s[3]);
-#pragma unroll
-  for (int i = 4; i < N; i += 8) {
-    a = ptx::fmax3(a, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-    b = ptx::fmax3(b, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-    c = ptx::fmax3(c, __uint_as_float(s[i + 4]), __uint_as_float(s[i + 5]));
-    d = ptx::fmax3(d, __uint_as_float(s[i + 6]), __uint_as_float(s[i + 7]));
-  }
-  return fmaxf(fmaxf(a, b), fmaxf(c, d));
-}
-
-// Sets every column whose mask bit is clear to -inf.
-template <int N>
-__device__ __forceinline__ void apply_mask(uint32_t (&s)[N], const uint32_t *mask) {
-#pragma unroll
-  for (int wd = 0; wd < N / 32; ++wd) {
-    const uint32_t mw = mask[wd];
-    if (mw != 0xFFFFFFFFu) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (!((mw >> i) & 1u)) s[32 * wd + i] = __float_as_uint(-INFINITY);
-    }
-  }
-}
-
-// Writes 32 bf16 values (columns [32 cc, 32 cc + 32) of row `row`) into a swizzled tile.
-__device__ __forceinline__ void stage_cols32(uint8_t *tile, int row, int cc, const float *x) {
-  const uint32_t base = ptx::smem_u32(tile) + uint32_t(cc >> 1) * kHalfBytes + uint32_t(row) * 128u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    ptx::st_shared_v4(base + ((uint32_t((cc & 1) * 4 + i) ^ uint32_t(row & 7)) << 4),
-                      ptx::pack_bf16x2(x[8 * i], x[8 * i + 1]), ptx::pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
-                      ptx::pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), ptx::pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
-}
-
-// kPlain: one softmax map; kDiff: differential attention; kPart: text-query rows whose
-// (partial) outputs leave in float32, for a difference of maps taken afterwards.
-enum Form { kPlain = 0, kDiff = 1, kPart = 2 };
-
-template <int FORM>
+template <bool PART>
 __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_constant__ AttnParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + kSmemCtrl);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  constexpr bool DIFF = FORM == kDiff;
 
   int pair, w = 0, bh, split = 0, ot = 0, oy = 0, ox = 0, wtype = 0, n_q_tiles;
   PlanType ty{0, 0};
@@ -301,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
     bh = blockIdx.x / (P.dense_pairs * P.n_splits);
     n_q_tiles = P.dense_q_tiles;
   } else {
-    const int pairs = DIFF ? P.dense_q_tiles : P.plan.max_pairs;  // DIFF: query tiles of a window
+    const int pairs = P.plan.max_pairs;
     pair = blockIdx.x % pairs;
     w = (blockIdx.x / pairs) % P.g.nWin;
     bh = blockIdx.x / (pairs * P.g.nWin);
@@ -309,12 +91,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
     ty = P.plan.type[wtype];
     n_q_tiles = ty.n_tiles;
   }
-  const int q_tile0 = DIFF ? pair : 2 * pair;
+  const int q_tile0 = 2 * pair;
   if (q_tile0 >= n_q_tiles) return;  // whole CTA: this window type has fewer query tiles
-  const bool has_q1 = DIFF || q_tile0 + 1 < n_q_tiles;
-  constexpr int kPer = DIFF ? 3 : 2;  // ring items of a key step: K, V, or K1, K2, V
-  // unit of map g's queries and keys, and of the values
-  const int unit0 = DIFF ? 2 * bh : bh, unit_step = DIFF ? 1 : 0, unit_v = DIFF ? bh : bh >> P.v_shift;
+  const bool has_q1 = q_tile0 + 1 < n_q_tiles;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -329,20 +108,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
     }
     ptx::mbar_init(&c.drain, 1);
     c.abort = 0;
-    c.tile0 = P.dense ? split * P.split_tiles : 0;
-    c.ntile = P.dense ? min(P.split_tiles, (P.dense_rows + kTileRows - 1) / kTileRows - c.tile0) : 0;
-    c.wtype[0] = wtype;
-    c.org[0][0] = ot; c.org[0][1] = oy; c.org[0][2] = ox;
-    for (int r = 0; r < P.routed_k; ++r) {
-      int u = P.route[((long long)bh * P.g.nWin + w) * P.routed_k + r];
-      if (u < 0 || u >= P.g.nWin) {  // reported, and replaced by the own window: accesses stay in bounds
-        if (P.dev_err) atomicOr(P.dev_err, BASA_DEVERR_BAD_ROUTE);
-        u = w;
-      }
-      int a, b, d, t;
-      window_origin(P.g, u, &a, &b, &d, &t);
-      c.wtype[1 + r] = t;
-      c.org[1 + r][0] = a; c.org[1 + r][1] = b; c.org[1 + r][2] = d;
+    if (P.dense) {
+      c.keys.tile0 = split * P.split_tiles;
+      c.keys.ntile = min(P.split_tiles, (P.dense_rows + kTileRows - 1) / kTileRows - c.keys.tile0);
+      c.keys.wtype[0] = 0;
+    } else {
+      fill_windows(P, c.keys, bh, w);
     }
     ptx::fence_mbar_init();
   }
@@ -365,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
   const uint32_t tmem = c.tmem_base;
 
   int n_kt = 0;
-  for (int s = 0; s <= P.routed_k + 2; ++s) n_kt += seg_tiles(P, c, s);
+  for (int s = 0; s <= P.routed_k + 2; ++s) n_kt += seg_tiles(P, c.keys, s);
 
   if (warp == 0) {
     // ------------------------------------------------------------- TMA loader
@@ -383,32 +154,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
       } else {
         // a tile's TMA boxes deliver 256 bytes per valid row (two 128-byte halves)
         uint32_t qbytes = uint32_t(P.plan.tile[ty.first_tile + q_tile0].valid_rows) * 256u;
-        if (has_q1) qbytes += DIFF ? qbytes : uint32_t(P.plan.tile[ty.first_tile + q_tile0 + 1].valid_rows) * 256u;
+        if (has_q1) qbytes += uint32_t(P.plan.tile[ty.first_tile + q_tile0 + 1].valid_rows) * 256u;
         ptx::mbar_arrive_expect_tx(&c.q_full, qbytes);
         for (int g = 0; g < (has_q1 ? 2 : 1); ++g)
-          sm100::load_window_tile(P.plan, P.g, P.map_q, P.plan.tile[ty.first_tile + q_tile0 + (DIFF ? 0 : g)], c.org[0],
-                                  unit0 + g * unit_step, smem + kSmemQ + g * kTileBytes, &c.q_full);
+          load_window_tile(P.plan, P.g, P.map_q, P.plan.tile[ty.first_tile + q_tile0 + g], c.keys.org[0], bh,
+                                  smem + kSmemQ + g * kTileBytes, &c.q_full);
       }
-      KeyIter it = first_key(P, c);
+      KeyIter it = first_key(P, c.keys);
       int last = -1;
       bool skipped0 = false;
       for (int j = 0; j < n_kt; ++j) {
         bool ok = true;
-        for (int kv = 0; kv < kPer; ++kv) {
-          const int item = kPer * j + kv;
+        for (int kv = 0; kv < 2; ++kv) {
+          const int item = 2 * j + kv;
           const int slot = item % kStages;
           if (!wt.wait(&c.empty[slot], ((item / kStages) & 1) ^ 1)) { ok = false; break; }
           if (item == 0 && (P.flags & BASA_FLAG_TEST_SKIP_FIRST_KEY_LOAD)) { skipped0 = true; last = item; continue; }
           uint8_t *dst = smem + kSmemRing + slot * kTileBytes;
           // Arm the barrier with the byte count before issuing the copies.
-          const uint32_t bytes = key_tile_bytes(P, c, it);
+          const uint32_t bytes = key_tile_bytes(P, c.keys, it);
           ptx::mbar_arrive_expect_tx(&c.full[slot], bytes);
-          const bool is_v = kv == kPer - 1;
-          load_key_tile(P, c, it, is_v, is_v ? unit_v : unit0 + kv * unit_step, dst, &c.full[slot]);
+          load_key_tile(P, c.keys, it, kv == 1, kv == 1 ? bh >> P.v_shift : bh, dst, &c.full[slot]);
           last = item;
         }
         if (!ok) break;
-        advance(P, c, it);
+        advance(P, c.keys, it);
       }
       // Drain: wait for the copies still in flight (immediate when all were consumed).
       drain.wait(&c.q_full, 0);
@@ -424,73 +194,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
       Waiter wt{&c.abort, P.dev_err, P.timeout_ns, BASA_DEVERR_TIMEOUT_MMA, true};
       Waiter drain{&c.abort, P.dev_err, P.timeout_ns, BASA_DEVERR_TIMEOUT_MMA, false};
       // low descriptor halves of the query tiles and the ring slots
-      const uint32_t sQ = sm100::kDescLoK | (ptx::smem_u32(smem + kSmemQ) >> 4);
-      const uint32_t sRk = sm100::kDescLoK | (ptx::smem_u32(smem + kSmemRing) >> 4);
-      const uint32_t sRv = sm100::kDescLoMn | (ptx::smem_u32(smem + kSmemRing) >> 4);
+      const uint32_t sQ = kDescLoK | (ptx::smem_u32(smem + kSmemQ) >> 4);
+      const uint32_t sRk = kDescLoK | (ptx::smem_u32(smem + kSmemRing) >> 4);
+      const uint32_t sRv = kDescLoMn | (ptx::smem_u32(smem + kSmemRing) >> 4);
       const uint32_t tS0 = tmem, tS1 = tmem + 128, tO0 = tmem + 256, tO1 = tmem + 384;
       if (wt.wait(&c.q_full, 0) && wt.wait(&c.full[0], 0)) {
         ptx::tc_fence_after();
-        sm100::issue_ss(tS0, sQ, sRk);
+        issue_ss(tS0, sQ, sRk);
         ptx::mma_commit(&c.s_full[0]);
-        if (has_q1 && !DIFF) {
-          sm100::issue_ss(tS1, sQ + kTileDesc, sRk);
+        if (has_q1) {
+          issue_ss(tS1, sQ + kTileDesc, sRk);
           ptx::mma_commit(&c.s_full[1]);
         }
         ptx::mma_commit(&c.empty[0]);
-        bool started = true;
-        if (DIFF) {
-          started = wt.wait(&c.full[1], 0);
-          if (started) {
-            ptx::tc_fence_after();
-            sm100::issue_ss(tS1, sQ + kTileDesc, sRk + kTileDesc);
-            ptx::mma_commit(&c.s_full[1]);
-            ptx::mma_commit(&c.empty[1]);
-          }
-        }
-        for (int j = 0; DIFF && started && j < n_kt; ++j) {
-          // items of this step's V and of the next step's K1, K2
-          const int vi = 3 * j + 2, k0 = vi + 1, k1 = vi + 2;
-          const uint32_t vaddr = sRv + (vi % kStages) * kTileDesc;
-          const bool more = j + 1 < n_kt;
-          if (!wt.wait(&c.full[vi % kStages], (vi / kStages) & 1)) break;
-          if (!wt.wait(&c.p_full[0], j & 1)) break;
-          ptx::tc_fence_after();
-          sm100::issue_ts(tO0, tS0, vaddr, j > 0);
-          if (more) {
-            if (!wt.wait(&c.full[k0 % kStages], (k0 / kStages) & 1)) break;
-            ptx::tc_fence_after();
-            sm100::issue_ss(tS0, sQ, sRk + (k0 % kStages) * kTileDesc);
-            ptx::mma_commit(&c.s_full[0]);
-            ptx::mma_commit(&c.empty[k0 % kStages]);
-          } else {
-            ptx::mma_commit(&c.o_full[0]);
-          }
-          if (!wt.wait(&c.p_full[1], j & 1)) break;
-          ptx::tc_fence_after();
-          sm100::issue_ts(tO1, tS1, vaddr, j > 0);
-          ptx::mma_commit(&c.empty[vi % kStages]);
-          if (more) {
-            if (!wt.wait(&c.full[k1 % kStages], (k1 / kStages) & 1)) break;
-            ptx::tc_fence_after();
-            sm100::issue_ss(tS1, sQ + kTileDesc, sRk + (k1 % kStages) * kTileDesc);
-            ptx::mma_commit(&c.s_full[1]);
-            ptx::mma_commit(&c.empty[k1 % kStages]);
-          } else {
-            ptx::mma_commit(&c.o_full[1]);
-          }
-        }
-        for (int j = 0; !DIFF && j < n_kt; ++j) {
+        for (int j = 0; j < n_kt; ++j) {
           const int vi = 2 * j + 1, ki = 2 * j + 2;
           const uint32_t vaddr = sRv + (vi % kStages) * kTileDesc, kaddr = sRk + (ki % kStages) * kTileDesc;
           const bool more = j + 1 < n_kt;
           if (!wt.wait(&c.full[vi % kStages], (vi / kStages) & 1)) break;
           if (!wt.wait(&c.p_full[0], j & 1)) break;
           ptx::tc_fence_after();
-          sm100::issue_ts(tO0, tS0, vaddr, j > 0);
+          issue_ts(tO0, tS0, vaddr, j > 0);
           if (more) {
             if (!wt.wait(&c.full[ki % kStages], (ki / kStages) & 1)) break;
             ptx::tc_fence_after();
-            sm100::issue_ss(tS0, sQ, kaddr);
+            issue_ss(tS0, sQ, kaddr);
             ptx::mma_commit(&c.s_full[0]);
           } else {
             ptx::mma_commit(&c.o_full[0]);
@@ -498,12 +226,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
           if (has_q1) {
             if (!wt.wait(&c.p_full[1], j & 1)) break;
             ptx::tc_fence_after();
-            sm100::issue_ts(tO1, tS1, vaddr, j > 0);
+            issue_ts(tO1, tS1, vaddr, j > 0);
           }
           ptx::mma_commit(&c.empty[vi % kStages]);
           if (more) {
             if (has_q1) {
-              sm100::issue_ss(tS1, sQ + kTileDesc, kaddr);
+              issue_ss(tS1, sQ + kTileDesc, kaddr);
               ptx::mma_commit(&c.s_full[1]);
             }
             ptx::mma_commit(&c.empty[ki % kStages]);
@@ -536,19 +264,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
       const int j = threadIdx.x - 128;
       if (j < kMaskTable && j < n_kt) {
         KeyIter t{0, j};
-        while (t.seg <= P.routed_k + 2 && t.t >= seg_tiles(P, c, t.seg)) {
-          t.t -= seg_tiles(P, c, t.seg);
+        while (t.seg <= P.routed_k + 2 && t.t >= seg_tiles(P, c.keys, t.seg)) {
+          t.t -= seg_tiles(P, c.keys, t.seg);
           ++t.seg;
         }
         uint32_t mk[4];
-        key_tile_mask(P, c, t, mk);
+        key_tile_mask(P, c.keys, t, mk);
         reinterpret_cast<uint4 *>(smem + kSmemMask)[j] = make_uint4(mk[0], mk[1], mk[2], mk[3]);
       }
       ptx::named_barrier(3, 256);  // the 256 softmax threads
     }
     float m = -INFINITY, l = 0.f;
     bool ok = active;
-    KeyIter it = first_key(P, c);
+    KeyIter it = first_key(P, c.keys);
     for (int j = 0; ok && j < n_kt; ++j) {
       ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.s_full[g], j & 1));
       if (!ok) break;
@@ -565,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
         }
       } else {
         uint32_t mask[4];
-        if (!key_tile_mask(P, c, it, mask)) apply_mask(s, mask);
+        if (!key_tile_mask(P, c.keys, it, mask)) apply_mask(s, mask);
       }
       const float m_tile = row_max(s) * sl2;
       const bool need = m_tile > m + kRescaleLog2;  // always true on the first tile (m = -inf)
@@ -599,68 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
       ptx::mbar_arrive(&c.p_full[g]);
       if (j + 1 >= kMaskTable) {
         if (j + 1 == kMaskTable)  // past the table: walk the stream from its start once
-          for (int t = 0; t < kMaskTable; ++t) advance(P, c, it);
+          for (int t = 0; t < kMaskTable; ++t) advance(P, c.keys, it);
         else
-          advance(P, c, it);
+          advance(P, c.keys, it);
       }
     }
-    if (DIFF) {
-      // Both maps' outputs are read by both groups: group g takes columns [64 g, 64 g + 64)
-      // of O1 / l1 - lambda O2 / l2 (a TMEM lane holds the same query row of both).
-      // The ring is free by now: out is staged in its slot 0, row sums in its slot 1;
-      // the difference before the norm and O2 / l2, when asked for, over the query tiles.
-      float *inv_l = reinterpret_cast<float *>(smem + kSmemRing + kTileBytes);  // [2][128]
-      float *sq = inv_l + 2 * kTileRows;                                         // [2][128]
-      if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.o_full[0], 0) && wt.wait(&c.o_full[1], 0));
-      if (ok) inv_l[g * kTileRows + row] = 1.0f / l;
-      ptx::named_barrier(3, 256);
-      float a[64];
-      float ss = 0.f;
-      if (ok) {
-        ptx::tc_fence_after();
-        const float i0 = inv_l[row], i1 = inv_l[kTileRows + row];
-        const float lam = __bfloat162float(P.lambda[bh % P.heads]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int cc = 2 * g + h;
-          uint32_t r0[32], r1[32];
-          ptx::tmem_ld32(tmem + lane_off + 256 + cc * 32, r0);
-          ptx::tmem_ld32(tmem + lane_off + 384 + cc * 32, r1);
-          ptx::tmem_ld_wait(r0);
-          ptx::tmem_ld_wait(r1);
-          float o1[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            o1[i] = __uint_as_float(r1[i]) * i1;
-            a[32 * h + i] = fmaf(-lam, o1[i], __uint_as_float(r0[i]) * i0);
-            ss = fmaf(a[32 * h + i], a[32 * h + i], ss);
-          }
-          if (P.store_pre) stage_cols32(smem + kSmemQ, row, cc, a + 32 * h);
-          if (P.store_o2) stage_cols32(smem + kSmemQ + kTileBytes, row, cc, o1);
-        }
-        sq[g * kTileRows + row] = ss;
-      }
-      if (P.norm_weight != nullptr) ptx::named_barrier(3, 256);
-      if (ok) {
-        if (P.norm_weight != nullptr) {
-          const float f = rsqrtf((sq[row] + sq[kTileRows + row]) * (1.0f / 128.0f) + P.eps) * P.gain;
-          const uint4 *w4 = reinterpret_cast<const uint4 *>(P.norm_weight + 64 * g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 u = __ldg(w4 + i);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              a[8 * i + 2 * e] *= f * __uint_as_float(w[e] << 16);
-              a[8 * i + 2 * e + 1] *= f * __uint_as_float(w[e] & 0xFFFF0000u);
-            }
-          }
-        }
-        stage_cols32(smem + kSmemRing, row, 2 * g, a);
-        stage_cols32(smem + kSmemRing, row, 2 * g + 1, a + 32);
-        ptx::fence_proxy_async_smem();
-      }
-    } else if (FORM == kPart) {
+    if (PART) {
       // this thread's row of O / l as it is, 512 bytes (rows past n_text are not written)
       if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.o_full[g], 0));
       const int qrow = (q_tile0 + g) * kTileRows + row;
@@ -722,24 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
       // log-sum-exp of this row: m and l are in base 2 of the scaled scores
       int t, y, x;
       const int org[3] = {ot, oy, ox};
-      if (sm100::tile_row_token(P.plan, P.g, P.plan.tile[ty.first_tile + q_tile0 + (DIFF ? 0 : g)], org, row, &t, &y, &x))
-        P.lse[(long long)(unit0 + g * unit_step) * P.g.N + ((long long)t * P.g.H + y) * P.g.W + x] = (m + log2f(l)) * 0.6931471805599453f;
+      if (tile_row_token(P.plan, P.g, P.plan.tile[ty.first_tile + q_tile0 + g], org, row, &t, &y, &x))
+        P.lse[(long long)bh * P.g.N + ((long long)t * P.g.H + y) * P.g.W + x] = (m + log2f(l)) * 0.6931471805599453f;
     }
-    if (DIFF) {
-      ptx::named_barrier(3, 256);  // both groups have staged their columns
-      if (row == 0 && !*reinterpret_cast<volatile int *>(&c.abort)) {
-        const int org[3] = {ot, oy, ox};
-        const PlanTile &tile = P.plan.tile[ty.first_tile + q_tile0];
-        if (g == 0) sm100::store_window_tile(P.plan, P.g, P.map_o, tile, org, bh, smem + kSmemRing);
-        if (g == 0 && P.store_pre) sm100::store_window_tile(P.plan, P.g, P.map_pre, tile, org, bh, q_tile);
-        if (g == 1 && P.store_o2) sm100::store_window_tile(P.plan, P.g, P.map_o2, tile, org, bh, q_tile);
-        ptx::tma_store_commit();
-        ptx::tma_store_wait_read_all();
-      }
-    } else if (FORM == kPlain) {
-      ptx::named_barrier(1 + g, 128);
-    }
-    if (FORM != kPlain) {
+    if (!PART) ptx::named_barrier(1 + g, 128);
+    if (PART) {
     } else if (P.dense && active && row == 0 && !*reinterpret_cast<volatile int *>(&c.abort)) {
       // rows past n_text fall outside the output map and are not written
       const int orow = (q_tile0 + g) * kTileRows, ob = split * P.bh_count + bh;
@@ -749,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
       ptx::tma_store_wait_read_all();
     } else if (active && row == 0 && !*reinterpret_cast<volatile int *>(&c.abort)) {
       const int org[3] = {ot, oy, ox};
-      sm100::store_window_tile(P.plan, P.g, P.map_o, P.plan.tile[ty.first_tile + q_tile0 + g], org, bh, q_tile);
+      store_window_tile(P.plan, P.g, P.map_o, P.plan.tile[ty.first_tile + q_tile0 + g], org, bh, q_tile);
       ptx::tma_store_commit();
       ptx::tma_store_wait_read_all();
     }
@@ -807,15 +466,14 @@ bool plan_pool_tail(AttnParams &P) {
   return true;
 }
 
-template <int FORM>
+template <bool PART>
 basa_status run_attn(const AttnParams &P, long long blocks, cudaStream_t s) {
-  if (cudaFuncSetAttribute(attn_bf16_kernel<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+  if (cudaFuncSetAttribute(attn_bf16_kernel<PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
       cudaSuccess)
     return BASA_ERR_CUDA;
-  attn_bf16_kernel<FORM><<<unsigned(blocks), kThreads, kSmemBytes, s>>>(P);
+  attn_bf16_kernel<PART><<<unsigned(blocks), kThreads, kSmemBytes, s>>>(P);
   return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
 }
-
 
 // Number of key-range splits for the text-query rows: enough CTAs to cover the SMs
 // once (one CTA per SM fits), at least 4 key tiles per split.
@@ -893,9 +551,6 @@ int device_sm_count() {
   return n[dev];
 }
 
-namespace {
-// Parameters of a window-mode launch. `maps` softmax maps share a head's values: q, k, kp
-// have maps * heads heads, v, vp and out have heads.
 basa_status window_params(AttnParams &P, const void *q, const void *k, const void *v, const void *kp, const void *vp,
                           const int32_t *route_idx, void *out, float *lse, uint32_t keys, const basa_params &p,
                           int maps) {
@@ -943,7 +598,6 @@ basa_status window_params(AttnParams &P, const void *q, const void *k, const voi
   P.timeout_ns = (p.wait_timeout_us ? (unsigned long long)p.wait_timeout_us : 2000000ull) * 1000ull;
   return BASA_OK;
 }
-}  // namespace
 
 basa_status launch_attn_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                              const int32_t *route_idx, void *out, float *lse, uint32_t keys, const basa_params &p,
@@ -953,30 +607,7 @@ basa_status launch_attn_bf16(const void *q, const void *k, const void *v, const 
   if (st != BASA_OK) return st;
   const long long blocks = (long long)p.B * p.heads * P.g.nWin * P.plan.max_pairs;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  return run_attn<kPlain>(P, blocks, s);
-}
-
-basa_status launch_diff_attn_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
-                                  const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
-                                  void *second, float *lse, const basa_params &p, cudaStream_t s) {
-  AttnParams P;
-  basa_status st = window_params(P, q, k, v, kp, vp, route_idx, out, lse, BASA_KEYS_ALL, p, 2);
-  if (st != BASA_OK) return st;
-  P.lambda = static_cast<const __nv_bfloat16 *>(dp.lambda);
-  P.norm_weight = static_cast<const __nv_bfloat16 *>(dp.weight);
-  P.gain = dp.gain;
-  P.eps = dp.eps;
-  P.heads = p.heads;
-  P.store_pre = pre != nullptr;
-  P.store_o2 = second != nullptr;
-  for (int i = 0; i < P.plan.n_shapes; ++i)
-    if ((pre && !encode_grid_map(&P.map_pre[i], pre, p, P.g.N, P.plan.shape[i])) ||
-        (second && !encode_grid_map(&P.map_o2[i], second, p, P.g.N, P.plan.shape[i])))
-      return BASA_ERR_CUDA;
-  for (int t = 0; t < 8; ++t) P.dense_q_tiles = std::max<int>(P.dense_q_tiles, P.plan.type[t].n_tiles);
-  const long long blocks = (long long)p.B * p.heads * P.g.nWin * P.dense_q_tiles;
-  if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  return run_attn<kDiff>(P, blocks, s);
+  return run_attn<false>(P, blocks, s);
 }
 
 size_t text_attn_workspace(const basa_params &p, int sms) {
@@ -1044,7 +675,7 @@ basa_status launch_attn_text_bf16(const void *q_text, const void *k, const void 
   P.lse = P.n_splits > 1 ? part_lse : nullptr;
   const long long blocks = (long long)bh * P.dense_pairs * P.n_splits;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  st = run_attn<kPlain>(P, blocks, s);
+  st = run_attn<false>(P, blocks, s);
   if (st != BASA_OK || P.n_splits == 1) return st;
   const void *outs[kMaxTextSplits];
   const float *lses[kMaxTextSplits];
@@ -1077,7 +708,7 @@ basa_status launch_diff_text_bf16(const void *q_text, const void *k, const void 
   P.lse = P.part + rows * p.head_dim;
   const long long blocks = (long long)P.bh_count * P.dense_pairs * P.n_splits;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  if ((st = run_attn<kPart>(P, blocks, s)) != BASA_OK) return st;
+  if ((st = run_attn<true>(P, blocks, s)) != BASA_OK) return st;
   return launch_diff_combine(P.n_splits, P.part, P.lse, p.n_text, dp, out_text, nullptr, nullptr, p, s);
 }
 

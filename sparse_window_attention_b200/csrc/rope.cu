@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 // Units a thread loads before it works on the first: 2 * 16 bytes each (backward: twice that).
-constexpr int kUnrollFwd = 4, kUnrollBwd = 2, kUnrollCopy = 8;
+constexpr int kUnrollFwd = 4, kUnrollBwd = 3, kUnrollCopy = 8;
 
 struct RopeTensorArgs {
   const void *x, *dy, *weight;
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const _
   }
   UnitWalk xw(t.xs, u0, t.heads);
 
-  if (!BWD) {
+  if constexpr (!BWD) {
     // y_a = x_a (w_a cos) - x_b (w_b sin), y_b = x_a (w_a sin) + x_b (w_b cos), times r
     uint64_t ac[H2], as[H2], bc[H2], bs[H2];
 #pragma unroll
@@ -280,83 +280,82 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const _
         store(p[k], q[k]);
       }
     }
-    return;
-  }
-
-  uint64_t dwa[H2], dwb[H2];
+  } else {
+    uint64_t dwa[H2], dwb[H2];
 #pragma unroll
-  for (int i = 0; i < H2; ++i) dwa[i] = dwb[i] = f2_both(0.f);
-  UnitWalk dw(t.ds, u0, t.heads);
-  for (int u = 0; u < n_units; u += kUnrollBwd) {
-    uint4 p[kUnrollBwd], q[kUnrollBwd], gp[kUnrollBwd], gq[kUnrollBwd];
+    for (int i = 0; i < H2; ++i) dwa[i] = dwb[i] = f2_both(0.f);
+    UnitWalk dw(t.ds, u0, t.heads);
+    for (int u = 0; u < n_units; u += kUnrollBwd) {
+      uint4 p[kUnrollBwd], q[kUnrollBwd], gp[kUnrollBwd], gq[kUnrollBwd];
 #pragma unroll
-    for (int k = 0; k < kUnrollBwd; ++k) {
-      if (u + k >= n_units) break;
-      if (norm) load(x0 + xw.next(), p[k], q[k]);
-      load(d0 + dw.next(), gp[k], gq[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kUnrollBwd; ++k) {
-      if (u + k >= n_units) break;
-      uint64_t ga[H2], gb[H2];
-      unpack<HALVES>(gp[k], gq[k], ga, gb, kind);
-#pragma unroll
-      for (int i = 0; i < H2; ++i) {  // the turn by -angle
-        const uint64_t g = ptx::ffma2(ga[i], cs[i], ptx::fmul2(gb[i], sn[i]));
-        gb[i] = ptx::ffma2(gb[i], cs[i], ptx::fmul2(ga[i], f2_neg(sn[i])));
-        ga[i] = g;
+      for (int k = 0; k < kUnrollBwd; ++k) {
+        if (u + k >= n_units) break;
+        if (norm) load(x0 + xw.next(), p[k], q[k]);
+        load(d0 + dw.next(), gp[k], gq[k]);
       }
-      if (norm) {
-        uint64_t xa[H2], xb[H2], ss = f2_both(0.f), dot = f2_both(0.f);
-        unpack<HALVES>(p[k], q[k], xa, xb, kind);
 #pragma unroll
-        for (int i = 0; i < H2; ++i) ss = ptx::ffma2(xb[i], xb[i], ptx::ffma2(xa[i], xa[i], ss));
-        const float rms = rsqrtf(row_sum<LPR>(f2_sum(ss)) * (1.f / D) + a.eps);
-        const uint64_t rms2 = f2_both(valid ? rms : 0.f);  // a row past the end adds nothing to dweight
+      for (int k = 0; k < kUnrollBwd; ++k) {
+        if (u + k >= n_units) break;
+        uint64_t ga[H2], gb[H2];
+        unpack<HALVES>(gp[k], gq[k], ga, gb, kind);
 #pragma unroll
-        for (int i = 0; i < H2; ++i) {
-          const uint64_t pa = ptx::fmul2(ga[i], xa[i]), pb = ptx::fmul2(gb[i], xb[i]);
-          dwa[i] = ptx::ffma2(pa, rms2, dwa[i]);
-          dwb[i] = ptx::ffma2(pb, rms2, dwb[i]);
-          dot = ptx::ffma2(pb, wb[i], ptx::ffma2(pa, wa[i], dot));
+        for (int i = 0; i < H2; ++i) {  // the turn by -angle
+          const uint64_t g = ptx::ffma2(ga[i], cs[i], ptx::fmul2(gb[i], sn[i]));
+          gb[i] = ptx::ffma2(gb[i], cs[i], ptx::fmul2(ga[i], f2_neg(sn[i])));
+          ga[i] = g;
         }
-        // dx = r g w - x r^3 mean(g w x)
-        const float mean = row_sum<LPR>(f2_sum(dot)) * (1.f / D);
-        const uint64_t kx = f2_both(-(rms * rms) * (rms * mean));
+        if (norm) {
+          uint64_t xa[H2], xb[H2], ss = f2_both(0.f), dot = f2_both(0.f);
+          unpack<HALVES>(p[k], q[k], xa, xb, kind);
 #pragma unroll
-        for (int i = 0; i < H2; ++i) {
-          ga[i] = ptx::ffma2(xa[i], kx, ptx::fmul2(ptx::fmul2(ga[i], wa[i]), rms2));
-          gb[i] = ptx::ffma2(xb[i], kx, ptx::fmul2(ptx::fmul2(gb[i], wb[i]), rms2));
+          for (int i = 0; i < H2; ++i) ss = ptx::ffma2(xb[i], xb[i], ptx::ffma2(xa[i], xa[i], ss));
+          const float rms = rsqrtf(row_sum<LPR>(f2_sum(ss)) * (1.f / D) + a.eps);
+          const uint64_t rms2 = f2_both(valid ? rms : 0.f);  // a row past the end adds nothing to dweight
+#pragma unroll
+          for (int i = 0; i < H2; ++i) {
+            const uint64_t pa = ptx::fmul2(ga[i], xa[i]), pb = ptx::fmul2(gb[i], xb[i]);
+            dwa[i] = ptx::ffma2(pa, rms2, dwa[i]);
+            dwb[i] = ptx::ffma2(pb, rms2, dwb[i]);
+            dot = ptx::ffma2(pb, wb[i], ptx::ffma2(pa, wa[i], dot));
+          }
+          // dx = r g w - x r^3 mean(g w x)
+          const float mean = row_sum<LPR>(f2_sum(dot)) * (1.f / D);
+          const uint64_t kx = f2_both(-(rms * rms) * (rms * mean));
+#pragma unroll
+          for (int i = 0; i < H2; ++i) {
+            ga[i] = ptx::ffma2(xa[i], kx, ptx::fmul2(ptx::fmul2(ga[i], wa[i]), rms2));
+            gb[i] = ptx::ffma2(xb[i], kx, ptx::fmul2(ptx::fmul2(gb[i], wb[i]), rms2));
+          }
+        }
+        pack<HALVES>(ga, gb, gp[k], gq[k], kind);
+        store(gp[k], gq[k]);
+      }
+    }
+    if (t.part == nullptr) return;  // the same in the whole block
+    __shared__ float red[kRopeThreads / 32][D];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+    for (int i = 0; i < H2; ++i) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float v[2];
+        ptx::f2_unpack(half ? dwb[i] : dwa[i], v[0], v[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int o = LPR; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xFFFFFFFFu, v[e], o);
+          const int pair = pair_index<D, VEC, HALVES>(c, 2 * i + e);
+          if (lane < LPR) red[warp][HALVES ? pair + half * (D / 2) : 2 * pair + half] = v[e];
         }
       }
-      pack<HALVES>(ga, gb, gp[k], gq[k], kind);
-      store(gp[k], gq[k]);
     }
-  }
-  if (t.part == nullptr) return;  // the same in the whole block
-  __shared__ float red[kRopeThreads / 32][D];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < H2; ++i) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float v[2];
-      ptx::f2_unpack(half ? dwb[i] : dwa[i], v[0], v[1]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int o = LPR; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xFFFFFFFFu, v[e], o);
-        const int pair = pair_index<D, VEC, HALVES>(c, 2 * i + e);
-        if (lane < LPR) red[warp][HALVES ? pair + half * (D / 2) : 2 * pair + half] = v[e];
-      }
+      for (int k = 0; k < kRopeThreads / 32; ++k) s += red[k][threadIdx.x];
+      t.part[(long long)blk * D + threadIdx.x] = s;
     }
-  }
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kRopeThreads / 32; ++k) s += red[k][threadIdx.x];
-    t.part[(long long)blk * D + threadIdx.x] = s;
   }
 }
 
