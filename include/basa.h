@@ -450,14 +450,10 @@ basa_status basa_diff_pool_kv(const void *k, const void *v, void *kp, void *vp, 
  * basa_diff_attn_fwd — forward. For a backward, `second` and `lse` receive O2
  * [B, heads, N, head_dim] and the maps' log-sum-exp (float32 [B, 2 heads, N]); `pre`
  * receives a (nullable: without a weight `out` is a). All three may be NULL otherwise.
- * `workspace`: basa_diff_attn_workspace_bytes(p) bytes (0 with bfloat16: pass NULL;
- * float32: the two maps' outputs), 16-byte aligned, contents ignored.
  */
-size_t basa_diff_attn_workspace_bytes(const basa_params *p);
 basa_status basa_diff_attn_fwd(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                const int32_t *route_idx, const basa_diff_params *dp, void *out, void *pre,
-                               void *second, float *lse, void *workspace, const basa_params *p,
-                               basa_stream_t stream);
+                               void *second, float *lse, const basa_params *p, basa_stream_t stream);
 
 /*
  * basa_diff_attn_bwd — gradients with respect to q, k, v, lambda and weight. `pre` is a
@@ -484,7 +480,7 @@ basa_status basa_diff_attn_bwd(const void *q, const void *k, const void *v, cons
  * row of k, v (as basa_text_attn_fwd), then difference and norm as above. q_text
  * [B, 2 heads, n_text, head_dim], out_text [B, heads, n_text, head_dim], n_text >= 1.
  * `workspace`: basa_diff_text_attn_workspace_bytes(p) bytes of float32 map outputs,
- * 16-byte aligned, contents ignored.
+ * 16-byte aligned, contents ignored (0 bytes with float32: pass NULL).
  */
 size_t basa_diff_text_attn_workspace_bytes(const basa_params *p);
 basa_status basa_diff_text_attn_fwd(const void *q_text, const void *k, const void *v, const basa_diff_params *dp,

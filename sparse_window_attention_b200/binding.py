@@ -52,7 +52,6 @@ EXPORTED = (
     "basa_rope_bwd_workspace_bytes",
     "basa_rope_bwd",
     "basa_diff_pool_kv",
-    "basa_diff_attn_workspace_bytes",
     "basa_diff_attn_fwd",
     "basa_diff_attn_bwd_workspace_bytes",
     "basa_diff_attn_bwd",
@@ -154,9 +153,7 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     D = ctypes.POINTER(basa_diff_params)
     lib.basa_diff_pool_kv.argtypes = [vp, vp, vp, vp, P, vp]
     lib.basa_diff_pool_kv.restype = ctypes.c_int
-    lib.basa_diff_attn_workspace_bytes.argtypes = [P]
-    lib.basa_diff_attn_workspace_bytes.restype = ctypes.c_size_t
-    lib.basa_diff_attn_fwd.argtypes = [vp] * 6 + [D] + [vp] * 5 + [P, vp]
+    lib.basa_diff_attn_fwd.argtypes = [vp] * 6 + [D] + [vp] * 4 + [P, vp]
     lib.basa_diff_attn_fwd.restype = ctypes.c_int
     lib.basa_diff_attn_bwd_workspace_bytes.argtypes = [D, P]
     lib.basa_diff_attn_bwd_workspace_bytes.restype = ctypes.c_size_t
@@ -384,14 +381,10 @@ def basa_diff_pool_kv(k, v, kp, vp, params: basa_params, stream=None, check=True
     return st
 
 
-def basa_diff_attn_workspace_bytes(params: basa_params) -> int:
-    return _lib.basa_diff_attn_workspace_bytes(ctypes.byref(params))
-
-
-def basa_diff_attn_fwd(q, k, v, kp, vp, route_idx, diff_params: basa_diff_params, out, pre, second, lse, workspace,
+def basa_diff_attn_fwd(q, k, v, kp, vp, route_idx, diff_params: basa_diff_params, out, pre, second, lse,
                        params: basa_params, stream=None, check=True) -> int:
     st = _lib.basa_diff_attn_fwd(*[_ptr(x) for x in (q, k, v, kp, vp, route_idx)], ctypes.byref(diff_params),
-                                 *[_ptr(x) for x in (out, pre, second, lse, workspace)], ctypes.byref(params),
+                                 *[_ptr(x) for x in (out, pre, second, lse)], ctypes.byref(params),
                                  _stream(stream))
     if check:
         _check(st, "basa_diff_attn_fwd")

@@ -398,14 +398,9 @@ basa_status basa_diff_pool_kv(const void *k, const void *v, void *kp, void *vp, 
   return basa::launch_pool_rows(v, vp, units, *p, s);
 }
 
-size_t basa_diff_attn_workspace_bytes(const basa_params *p) {
-  if (check_diff_shape(p) != BASA_OK || p->dtype == BASA_BF16) return 0;
-  return basa::diff_f32_workspace(*p, int64_t(p->T) * p->H * p->W);
-}
-
 basa_status basa_diff_attn_fwd(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                const int32_t *route_idx, const basa_diff_params *dp, void *out, void *pre, void *second,
-                               float *lse, void *workspace, const basa_params *p, basa_stream_t stream) {
+                               float *lse, const basa_params *p, basa_stream_t stream) {
   basa_status st = check_diff(dp, p);
   if (st != BASA_OK) return st;
   if (empty_batch(p)) return BASA_OK;
@@ -414,8 +409,7 @@ basa_status basa_diff_attn_fwd(const void *q, const void *k, const void *v, cons
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (p->dtype == BASA_BF16)
     return basa::launch_diff_attn_bf16(q, k, v, kp, vp, route_idx, *dp, out, pre, second, lse, *p, s);
-  if (!workspace || !aligned16(workspace)) return BASA_ERR_INVALID_ARG;
-  return basa::launch_diff_attn_f32(q, k, v, kp, vp, route_idx, *dp, out, pre, second, lse, workspace, *p, s);
+  return basa::launch_diff_attn_f32(q, k, v, kp, vp, route_idx, *dp, out, pre, second, lse, false, *p, s);
 }
 
 size_t basa_diff_attn_bwd_workspace_bytes(const basa_diff_params *dp, const basa_params *p) {
@@ -451,9 +445,8 @@ basa_status basa_diff_attn_bwd(const void *q, const void *k, const void *v, cons
 }
 
 size_t basa_diff_text_attn_workspace_bytes(const basa_params *p) {
-  if (check_diff_shape(p) != BASA_OK || p->n_text < 1 || empty_batch(p)) return 0;
-  return p->dtype == BASA_BF16 ? basa::diff_text_workspace(*p, basa::device_sm_count())
-                               : basa::diff_f32_workspace(*p, p->n_text);
+  if (check_diff_shape(p) != BASA_OK || p->n_text < 1 || empty_batch(p) || p->dtype != BASA_BF16) return 0;
+  return basa::diff_text_workspace(*p, basa::device_sm_count());
 }
 
 basa_status basa_diff_text_attn_fwd(const void *q_text, const void *k, const void *v, const basa_diff_params *dp,
@@ -462,11 +455,14 @@ basa_status basa_diff_text_attn_fwd(const void *q_text, const void *k, const voi
   if (st != BASA_OK) return st;
   if (p->n_text < 1) return BASA_ERR_INVALID_ARG;
   if (empty_batch(p)) return BASA_OK;
-  for (const void *x : {q_text, k, v, static_cast<const void *>(out_text), static_cast<const void *>(workspace)})
+  for (const void *x : {q_text, k, v, static_cast<const void *>(out_text)})
     if (!x || !aligned16(x)) return BASA_ERR_INVALID_ARG;
   if (!dp->lambda) return BASA_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (p->dtype == BASA_F32) return basa::launch_diff_text_f32(q_text, k, v, *dp, out_text, workspace, *p, s);
+  if (p->dtype == BASA_F32)
+    return basa::launch_diff_attn_f32(q_text, k, v, nullptr, nullptr, nullptr, *dp, out_text, nullptr, nullptr, nullptr,
+                                      true, *p, s);
+  if (!workspace || !aligned16(workspace)) return BASA_ERR_INVALID_ARG;
   const int sms = basa::device_sm_count();
   if (sms <= 0) return BASA_ERR_CUDA;
   return basa::launch_diff_text_bf16(q_text, k, v, *dp, out_text, workspace, *p, sms, s);

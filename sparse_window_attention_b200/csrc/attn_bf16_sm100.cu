@@ -709,7 +709,7 @@ basa_status launch_diff_text_bf16(const void *q_text, const void *k, const void 
   const long long blocks = (long long)P.bh_count * P.dense_pairs * P.n_splits;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
   if ((st = run_attn<true>(P, blocks, s)) != BASA_OK) return st;
-  return launch_diff_combine(P.n_splits, P.part, P.lse, p.n_text, dp, out_text, nullptr, nullptr, p, s);
+  return launch_diff_combine(P.n_splits, P.part, P.lse, p.n_text, dp, out_text, p, s);
 }
 
 }  // namespace basa

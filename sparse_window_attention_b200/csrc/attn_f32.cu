@@ -5,57 +5,13 @@
 // over key tiles staged in shared memory.
 #include <cfloat>
 
-#include "basa_internal.h"
+#include "attn_f32.cuh"
 
 namespace basa {
 namespace {
 
 constexpr int kThreads = 128;
 constexpr int kKeyTile = 32;
-
-struct F32Args {
-  const float *q, *k, *v, *kp, *vp;
-  const int32_t *route;
-  int32_t *dev_err;  // nullable: BASA_DEVERR_BAD_ROUTE on an out-of-range route id
-  float *out;
-  float *lse;  // nullable [B*heads][N]
-  Geo g;
-  int heads, d, n_text, n_pool, routed_k, win_tok, q_chunks;
-  int n_vis_keys, n_pool_keys, n_text_keys;  // keys taken from each group (0 = group not selected)
-  int v_shift;  // v, vp and the routes belong to unit bh >> v_shift (maps that share their values)
-  int dense;  // text-query rows: queries are q_text rows, keys are all N + n_text rows of k, v
-  float scale;
-};
-
-// A route id outside [0, nWin) is reported (BASA_DEVERR_BAD_ROUTE) and replaced by
-// the query's own window, so every access stays inside the tensors.
-__device__ __forceinline__ int checked_route(const F32Args &a, int u, int w) {
-  if (u >= 0 && u < a.g.nWin) return u;
-  if (a.dev_err) atomicOr(a.dev_err, BASA_DEVERR_BAD_ROUTE);
-  return w;
-}
-
-// Row of key j of window w's key list: [own | routed windows | pooled | text],
-// restricted to the selected groups.
-__device__ __forceinline__ const float *key_row(const F32Args &a, const float *kv, const float *kvp, long long bh,
-                                                const int *wins, int j) {
-  const int nvis = a.n_vis_keys;
-  const long long rows = (long long)a.g.N + a.n_text;
-  if (a.dense) return kv + (bh * rows + j) * a.d;
-  if (j < nvis) {
-    const int u = wins[j / a.win_tok];
-    const int l = j % a.win_tok;
-    int ot, oy, ox, type;
-    window_origin(a.g, u, &ot, &oy, &ox, &type);
-    const int lt = l / (a.g.wh * a.g.ww), ly = (l / a.g.ww) % a.g.wh, lx = l % a.g.ww;
-    const int t = (ot + lt) % a.g.T, y = (oy + ly) % a.g.H, x = (ox + lx) % a.g.W;
-    return kv + (bh * rows + ((long long)t * a.g.H + y) * a.g.W + x) * a.d;
-  }
-  j -= nvis;
-  if (j < a.n_pool_keys) return kvp + (bh * a.n_pool + j) * a.d;
-  j -= a.n_pool_keys;
-  return kv + (bh * rows + a.g.N + j) * a.d;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_f32_kernel(F32Args a) {
@@ -71,7 +27,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(F32Args a) {
   const long long bh = blockIdx.x / (a.q_chunks * n_win);
   if (threadIdx.x == 0) wins[0] = w;
   if (!a.dense && threadIdx.x > 0 && threadIdx.x <= a.routed_k)
-    wins[threadIdx.x] = checked_route(a, a.route[((bh >> a.v_shift) * a.g.nWin + w) * a.routed_k + threadIdx.x - 1], w);
+    wins[threadIdx.x] = checked_route(a, a.route[(bh * a.g.nWin + w) * a.routed_k + threadIdx.x - 1], w);
   __syncthreads();
 
   const int half = threadIdx.x % TPQ;
@@ -104,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(F32Args a) {
       float4 kv4 = make_float4(0.f, 0.f, 0.f, 0.f), vv4 = kv4;
       if (k0 + r < nk) {
         kv4 = reinterpret_cast<const float4 *>(key_row(a, a.k, a.kp, bh, wins, k0 + r))[c4];
-        vv4 = reinterpret_cast<const float4 *>(key_row(a, a.v, a.vp, bh >> a.v_shift, wins, k0 + r))[c4];
+        vv4 = reinterpret_cast<const float4 *>(key_row(a, a.v, a.vp, bh, wins, k0 + r))[c4];
       }
       reinterpret_cast<float4 *>(&ks[r][0])[c4] = kv4;
       reinterpret_cast<float4 *>(&vs[r][0])[c4] = vv4;
@@ -148,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(F32Args a) {
 
 basa_status launch_attn_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                             const int32_t *route_idx, void *out, float *lse, uint32_t keys, const basa_params &p,
-                            cudaStream_t s, int v_shift) {
+                            cudaStream_t s) {
   F32Args a{};
   a.q = static_cast<const float *>(q);
   a.k = static_cast<const float *>(k);
@@ -166,7 +122,6 @@ basa_status launch_attn_f32(const void *q, const void *k, const void *v, const v
   a.routed_k = p.routed_k;
   a.win_tok = p.wt * p.wh * p.ww;
   a.lse = lse;
-  a.v_shift = v_shift;
   a.n_vis_keys = (keys & BASA_KEYS_WINDOWS) ? a.win_tok * (1 + a.routed_k) : 0;
   a.n_pool_keys = (keys & BASA_KEYS_POOLED) ? a.n_pool : 0;
   a.n_text_keys = (keys & BASA_KEYS_TEXT) ? a.n_text : 0;
@@ -181,9 +136,8 @@ basa_status launch_attn_f32(const void *q, const void *k, const void *v, const v
 }
 
 basa_status launch_attn_text_f32(const void *q_text, const void *k, const void *v, void *out_text,
-                                 const basa_params &p, cudaStream_t s, int v_shift) {
+                                 const basa_params &p, cudaStream_t s) {
   F32Args a{};
-  a.v_shift = v_shift;
   a.q = static_cast<const float *>(q_text);
   a.k = static_cast<const float *>(k);
   a.v = static_cast<const float *>(v);
@@ -452,33 +406,6 @@ basa_status launch_attn_bwd_f32(const void *q, const void *k, const void *v, con
 }
 
 // ----------------------------------------------------------------- differential form
-// The maps by themselves (q, k of 2 heads maps, the values of each pair shared), then
-// their difference and norm in one pass over the float32 map outputs.
-size_t diff_f32_workspace(const basa_params &p, long long rows) {
-  return 2 * size_t(p.B) * p.heads * rows * p.head_dim * sizeof(float);
-}
-
-basa_status launch_diff_attn_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
-                                 const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
-                                 void *second, float *lse, void *workspace, const basa_params &p, cudaStream_t s) {
-  basa_params pm = p;
-  pm.heads = 2 * p.heads;
-  basa_status st = launch_attn_f32(q, k, v, kp, vp, route_idx, workspace, lse, BASA_KEYS_ALL, pm, s, 1);
-  if (st != BASA_OK) return st;
-  return launch_diff_combine(1, static_cast<const float *>(workspace), nullptr, (long long)p.T * p.H * p.W, dp, out, pre,
-                             second, p, s);
-}
-
-basa_status launch_diff_text_f32(const void *q_text, const void *k, const void *v, const basa_diff_params &dp,
-                                 void *out_text, void *workspace, const basa_params &p, cudaStream_t s) {
-  basa_params pm = p;
-  pm.heads = 2 * p.heads;
-  basa_status st = launch_attn_text_f32(q_text, k, v, workspace, pm, s, 1);
-  if (st != BASA_OK) return st;
-  return launch_diff_combine(1, static_cast<const float *>(workspace), nullptr, p.n_text, dp, out_text, nullptr, nullptr,
-                             p, s);
-}
-
 namespace {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 }  // namespace

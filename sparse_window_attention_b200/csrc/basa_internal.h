@@ -136,7 +136,7 @@ basa_status launch_pool_route_fused(const void *q, const void *k, const void *v,
 // (BASA_KEYS_* bits).
 basa_status launch_attn_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                             const int32_t *route_idx, void *out, float *lse, uint32_t keys, const basa_params &p,
-                            cudaStream_t s, int v_shift = 0);  // v, vp, routes: units bh >> v_shift
+                            cudaStream_t s);
 basa_status launch_attn_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                              const int32_t *route_idx, void *out, float *lse, uint32_t keys, const basa_params &p,
                              cudaStream_t s);
@@ -163,24 +163,21 @@ basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, co
                                  const int32_t *route_idx, const void *out, const float *lse, const void *dout,
                                  void *dq, void *dk, void *dv, void *workspace, const basa_params &p, cudaStream_t s);
 basa_status launch_attn_text_f32(const void *q_text, const void *k, const void *v, void *out_text,
-                                 const basa_params &p, cudaStream_t s, int v_shift = 0);
+                                 const basa_params &p, cudaStream_t s);
 // Differential attention: p.heads heads of two maps each (q, k, kp: 2 heads units).
 basa_status launch_diff_attn_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                   const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
                                   void *second, float *lse, const basa_params &p, cudaStream_t s);
-size_t diff_f32_workspace(const basa_params &p, long long rows);  // the maps' outputs of `rows` rows
+// The windows' rows, or with `dense` the text queries' (q, out: n_text rows; every row a key).
 basa_status launch_diff_attn_f32(const void *q, const void *k, const void *v, const void *kp, const void *vp,
                                  const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
-                                 void *second, float *lse, void *workspace, const basa_params &p, cudaStream_t s);
+                                 void *second, float *lse, bool dense, const basa_params &p, cudaStream_t s);
 size_t diff_text_workspace(const basa_params &p, int sms);  // bf16 path
 basa_status launch_diff_text_bf16(const void *q_text, const void *k, const void *v, const basa_diff_params &dp,
                                   void *out_text, void *workspace, const basa_params &p, int sms, cudaStream_t s);
-basa_status launch_diff_text_f32(const void *q_text, const void *k, const void *v, const basa_diff_params &dp,
-                                 void *out_text, void *workspace, const basa_params &p, cudaStream_t s);
-// out (and pre, second) from the maps' float32 outputs, joined over n_splits key ranges.
+// out_text from the maps' float32 outputs, joined over n_splits key ranges (bf16 path).
 basa_status launch_diff_combine(int n_splits, const float *part, const float *part_lse, long long rows,
-                                const basa_diff_params &dp, void *out, void *pre, void *second, const basa_params &p,
-                                cudaStream_t s);
+                                const basa_diff_params &dp, void *out, const basa_params &p, cudaStream_t s);
 // Start of the backward: g, the rows' records (or D alone), partial sums of dlambda and
 // dweight; and their end, with the dq pass's sums (`dr`, nullable: dr_per_unit for each unit).
 size_t diff_prep_workspace(const basa_params &p);

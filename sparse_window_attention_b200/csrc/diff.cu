@@ -3,7 +3,7 @@
 //   a = O1 - lambda O2,   out = gain * weight * a * rsqrt(mean(a^2) + eps)   (no weight: out = a)
 //
 // combine   takes the maps' float32 outputs (or their partial results over key ranges,
-//           joined by log-sum-exp) to out: the text-query rows and the float32 layers.
+//           joined by log-sum-exp) to out: the text-query rows.
 // prepare   the start of the backward: with xh = a r and G = gain * dout
 //             dweight = sum G xh,  g = r (G w - xh mean(G w xh)),
 //             D2 = g . O2,  D1 = g . O1 = g . a + lambda D2,  dlambda = -sum g . O2;
@@ -74,7 +74,7 @@ struct CombineArgs {
   const float *part;  // [n_splits][B][2 heads][rows][d]
   const float *lse;   // [n_splits][B][2 heads][rows] (n_splits > 1)
   const void *lambda, *weight;
-  void *out, *pre, *second;  // [B][heads][rows][d]
+  void *out;          // [B][heads][rows][d]
   int n_splits, heads;
   long long rows, units;  // rows of a unit; B * heads
   float gain, eps;
@@ -123,21 +123,15 @@ __global__ void __launch_bounds__(kDiffThreads) diff_combine_kernel(const __grid
     x[i] = fmaf(-lam, o2[i], x[i]);
     ss = fmaf(x[i], x[i], ss);
   }
-  const long long at = (unit * a.rows + row) * D + 8 * c;
-  if (valid && a.second) store8(static_cast<T *>(a.second) + at, o2);
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = x[i];
   if (a.weight) {
     const float f = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps) * a.gain;
     float w[8];
     load8(static_cast<const T *>(a.weight) + 8 * c, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] *= f * w[i];
+    for (int i = 0; i < 8; ++i) x[i] *= f * w[i];
   }
   if (!valid) return;
-  if (a.pre) store8(static_cast<T *>(a.pre) + at, x);
-  store8(static_cast<T *>(a.out) + at, y);
+  store8(static_cast<T *>(a.out) + (unit * a.rows + row) * D + 8 * c, x);
 }
 
 // Rows of one (batch, head) that a block of the backward's start goes through: a few
@@ -302,15 +296,6 @@ __global__ void __launch_bounds__(1024) diff_sum_kernel(const __grid_constant__ 
   }
 }
 
-template <typename T, int D>
-basa_status run_combine(const CombineArgs &a, cudaStream_t s) {
-  constexpr int ROWS = kDiffThreads / (D / 8);
-  const long long blocks = (a.units * a.rows + ROWS - 1) / ROWS;
-  if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  diff_combine_kernel<T, D><<<unsigned(blocks), kDiffThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
-}
-
 long long prep_blocks_per_unit(const basa_params &p) {
   return ((long long)p.T * p.H * p.W + kPrepRows - 1) / kPrepRows;
 }
@@ -318,24 +303,24 @@ long long prep_blocks_per_unit(const basa_params &p) {
 }  // namespace
 
 basa_status launch_diff_combine(int n_splits, const float *part, const float *part_lse, long long rows,
-                                const basa_diff_params &dp, void *out, void *pre, void *second, const basa_params &p,
-                                cudaStream_t s) {
+                                const basa_diff_params &dp, void *out, const basa_params &p, cudaStream_t s) {
   CombineArgs a{};
   a.part = part;
   a.lse = part_lse;
   a.lambda = dp.lambda;
   a.weight = dp.weight;
   a.out = out;
-  a.pre = pre;
-  a.second = second;
   a.n_splits = n_splits;
   a.heads = p.heads;
   a.rows = rows;
   a.units = (long long)p.B * p.heads;
   a.gain = dp.gain;
   a.eps = dp.eps;
-  if (p.dtype == BASA_BF16) return run_combine<__nv_bfloat16, 128>(a, s);
-  return p.head_dim == 128 ? run_combine<float, 128>(a, s) : run_combine<float, 64>(a, s);
+  constexpr int D = 128, ROWS = kDiffThreads / (D / 8);
+  const long long blocks = (a.units * a.rows + ROWS - 1) / ROWS;
+  if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
+  diff_combine_kernel<__nv_bfloat16, D><<<unsigned(blocks), kDiffThreads, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
 }
 
 size_t diff_prep_workspace(const basa_params &p) {

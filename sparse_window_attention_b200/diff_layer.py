@@ -124,8 +124,7 @@ class BasaDiffLayer:
     def _forward(self, q, k, v, lam, shift, weight, kp, vp, route_idx, out, pre, second, lse, extra):
         params = self.params(shift, **extra)
         dp = B.make_diff_params(lam, weight, self.gain, self.eps)
-        ws = self._workspace(B.basa_diff_attn_workspace_bytes(params))
-        B.basa_diff_attn_fwd(q, k, v, kp, vp, route_idx, dp, out, pre, second, lse, ws, params)
+        B.basa_diff_attn_fwd(q, k, v, kp, vp, route_idx, dp, out, pre, second, lse, params)
 
     def attention(self, q, k, v, lam, shift, weight=None, kp=None, vp=None, route_idx=None, out=None, stream=None,
                   **extra):

@@ -327,8 +327,8 @@ def _diff(lam=FAKE, weight=FAKE, gain=1.0, eps=1e-6):
 
 
 def _diff_fwd(dp=None, p=None, q=FAKE, k=FAKE, v=FAKE, kp=FAKE, vp=FAKE, route=None, out=FAKE, pre=None, second=None,
-              lse=None, ws=None):
-    return B.basa_diff_attn_fwd(q, k, v, kp, vp, route, dp or _diff(), out, pre, second, lse, ws, p or _p(), stream=0,
+              lse=None):
+    return B.basa_diff_attn_fwd(q, k, v, kp, vp, route, dp or _diff(), out, pre, second, lse, p or _p(), stream=0,
                                 check=False)
 
 
@@ -347,10 +347,7 @@ def test_diff_forward_checks():
     assert _diff_fwd(p=_p(routed_k=2)) == 1 and _diff_fwd(p=_p(routed_k=2), route=FAKE + 2) == 1
     assert _diff_fwd(p=_p(pool=(0, 0, 0))) == 1  # pooled keys without a pool patch
     f32 = _p(dtype="f32")
-    assert _diff_fwd(p=f32) == 1 and _diff_fwd(p=f32, ws=FAKE + 8) == 1  # float32 needs its workspace
-    assert _diff_fwd(_diff(lam=FAKE + 2), f32, ws=FAKE) == 1
-    assert B.basa_diff_attn_workspace_bytes(_p()) == 0
-    assert B.basa_diff_attn_workspace_bytes(f32) == 4 * 4096 * 128 * 4
+    assert _diff_fwd(_diff(lam=FAKE + 2), f32) == 1
     for heads in (dict(B=0), dict(heads=0)):
         assert _diff_fwd(_diff(None, None), _p(**heads), *[None] * 5) == 0
 
@@ -403,4 +400,4 @@ def test_diff_text_checks():
     assert call(_p(n_text=0)) == 1 and call(_p(head_dim=64)) == 3 and call(dp=_diff(lam=None)) == 1
     assert call(_p(B=0), q=None) == 0
     assert B.basa_diff_text_attn_workspace_bytes(_p(n_text=0)) == 0
-    assert B.basa_diff_text_attn_workspace_bytes(_p(dtype="f32")) == 4 * 16 * 128 * 4
+    assert B.basa_diff_text_attn_workspace_bytes(_p(dtype="f32")) == 0
