@@ -35,7 +35,10 @@
 // dK/dV passes run both maps of a (batch, head) in ONE CTA, map 2 first: its dK leaves,
 // the dV accumulator is multiplied by -lambda in TMEM, and map 1 adds to it, so the two
 // maps' dV meet without a buffer or an atomic. (Both maps at once, sharing dout V^T, would
-// take six 128-column accumulators and TMEM holds four.)
+// take six 128-column accumulators and TMEM holds four.) The passes overlap at their ends by
+// programmatic dependent launch: the long pass runs first, on fewer CTAs than there are SMs
+// as often as not, and the dq pass, which needs nothing of it, fills the rest; the window
+// pass starts under the reduction and waits for it before its epilogue.
 //
 // Warp roles (320 threads): warp 0 TMA loads, warp 1 issues tcgen05 MMAs (one
 // thread), warps 2-9 compute P and dS: two warpgroups, each owning 64 of the 128
@@ -274,6 +277,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + L::ctrl);
   int16_t *list = reinterpret_cast<int16_t *>(smem + L::list);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (DIFF && MODE == kDkvLong) ptx::grid_launch_dependents();
+  // What follows the dq pass needs the long pass's sums: one CTA of it ends after them.
+  const bool last_to_end = DIFF && MODE == kDq && blockIdx.x == gridDim.x - 1 && threadIdx.x == 0;
 
   // ----------------------------------------------------------- unit of this CTA
   int bh, w = 0, tile_idx = 0, kt = 0, chunk = 0, ot = 0, oy = 0, ox = 0, wtype = 0;
@@ -288,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     window_origin(P.g, w, &ot, &oy, &ox, &wtype);
     if (tile_idx >= P.plan.type[wtype].n_tiles) {  // whole CTA: this window type has fewer tiles
       if (DIFF && MODE == kDq && threadIdx.x == 0) P.dr[blockIdx.x] = 0.f;
+      if (last_to_end) ptx::grid_wait();
       return;
     }
   }
@@ -823,6 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
         }
         if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.acc_full, n_cols > 0 ? m : 0));
         if (!ok) continue;
+        if (DIFF && MODE == kDkvWindow) ptx::grid_wait();  // the pooled keys' gradients
         ptx::tc_fence_after();
         const bool last_map = m + 1 == kMaps;
         const int unit = map_unit(m);  // of k and dk
@@ -916,6 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
+  if (last_to_end) ptx::grid_wait();
 }
 
 // Per query token: {-L log2(e), -(dout . out), 0, 0}, two tokens per warp (16 lanes x
@@ -947,6 +956,7 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(const float *part, floa
                                                          __nv_bfloat16 *dv, int bh_count, int maps, int n_long,
                                                          int n_chunks, int n_pool, int n_pool_tiles, int n_text,
                                                          long long N) {
+  if (maps == 2) ptx::grid_launch_dependents();
   const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;  // (bh, tile, row, 4-column group)
   const long long total = (long long)bh_count * n_long * kTileRows * 32;
   if (idx >= total) return;
@@ -1034,14 +1044,23 @@ BwdLayout bwd_layout(const basa_params &p, const WindowPlan &plan, int maps) {
 }
 
 template <int MODE, bool DIFF>
-basa_status run_bwd(const BwdParams &P, long long blocks, cudaStream_t s) {
+basa_status run_bwd(const BwdParams &P, long long blocks, cudaStream_t s, bool early = false) {
   if (blocks <= 0) return BASA_OK;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(attn_bwd_bf16_kernel<MODE, DIFF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Smem<MODE>::bytes) != cudaSuccess)
     return BASA_ERR_CUDA;
-  attn_bwd_bf16_kernel<MODE, DIFF><<<unsigned(blocks), kThreads, Smem<MODE>::bytes, s>>>(P);
-  return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<MODE>::bytes;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_bwd_bf16_kernel<MODE, DIFF>, P) == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
 }
 
 // Parameters of a backward over p.heads units of v with `maps` maps each; the
@@ -1103,21 +1122,23 @@ basa_status bwd_params(BwdParams &P, BwdLayout &L, const void *q, const void *k,
 }
 
 // The passes after the records: dq, pooled and text dK/dV, their chunks' sums, window dK/dV.
+// In the differential form `early` launches start under the one before them, see above.
 template <bool DIFF>
 basa_status run_passes(const BwdParams &P, const BwdLayout &L, void *dk, void *dv, const basa_params &p, cudaStream_t s) {
   constexpr int maps = DIFF ? 2 : 1;
   const long long bh = P.bh_count, window_blocks = bh * P.g.nWin * P.max_tiles;
-  basa_status st = run_bwd<kDq, DIFF>(P, maps * window_blocks, s);
+  basa_status st = DIFF ? BASA_OK : run_bwd<kDq, DIFF>(P, window_blocks, s);
   if (st != BASA_OK) return st;
+  if (L.n_long > 0 && (st = run_bwd<kDkvLong, DIFF>(P, bh * L.n_long * L.n_chunks, s)) != BASA_OK) return st;
+  if (DIFF && (st = run_bwd<kDq, DIFF>(P, maps * window_blocks, s, L.n_long > 0)) != BASA_OK) return st;
   if (L.n_long > 0) {
-    if ((st = run_bwd<kDkvLong, DIFF>(P, bh * L.n_long * L.n_chunks, s)) != BASA_OK) return st;
     const long long threads = bh * L.n_long * kTileRows * 32;
     bwd_reduce_kernel<<<dim3(unsigned((threads + 255) / 256), maps + 1), 256, 0, s>>>(
         P.part, const_cast<float *>(P.dkvp), static_cast<__nv_bfloat16 *>(dk), static_cast<__nv_bfloat16 *>(dv), int(bh),
         maps, L.n_long, L.n_chunks, P.n_pool, P.n_pool_tiles, p.n_text, P.g.N);
     if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
   }
-  return run_bwd<kDkvWindow, DIFF>(P, window_blocks, s);
+  return run_bwd<kDkvWindow, DIFF>(P, window_blocks, s, DIFF && L.n_long > 0);
 }
 
 }  // namespace

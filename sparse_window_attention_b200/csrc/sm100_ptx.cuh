@@ -53,6 +53,11 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// Programmatic dependent launch: lets the next launch of the stream start (once every CTA
+// has), and waits until the launches before this one are complete and their writes visible.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Named barrier that returns whether any of its threads came with `x` set (the same in all).
 __device__ __forceinline__ bool named_barrier_any(uint32_t id, uint32_t nthreads, bool x) {
   uint32_t r;
