@@ -86,7 +86,8 @@ struct Smem {
   static constexpr uint32_t col_rec = rec + (MODE == kDq ? 0u : 2 * kRecBytes);
   static constexpr uint32_t ctrl = col_rec + (MODE == kDq ? 0u : kColRecBytes);
   static constexpr uint32_t list = ctrl + kCtrlBytes;
-  static constexpr uint32_t bytes = list + (MODE == kDkvWindow ? kMaxList * 2 : 0) + 1024;  // + alignment slack
+  static constexpr uint32_t place = list + (MODE == kDkvWindow ? kMaxList * 2 : 0);  // differential form
+  static constexpr uint32_t bytes = place + (MODE == kDkvWindow ? 256 * 8 : 0) + 1024;  // + alignment slack
   static_assert(bytes <= 227u * 1024u, "shared memory of a pass above the 227 KB a CTA may hold");
 };
 
@@ -602,14 +603,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           }
           if (!ok) break;
           ptx::mma_commit(&c.empty[di % kSlots]);
-          if (more) {
-            if (!wt.wait(&c.full[qn % kSlots], (qn / kSlots) & 1)) break;
-            if (kMaps == 2 && j + 1 == n_cols && !wt.wait(&c.row_full, 1)) break;
+          // Map 2's last tile: its dK first, which does not wait for map 1's key tile.
+          const bool boundary = kMaps == 2 && j + 1 == n_cols;
+          auto next_scores = [&] {
+            if (!wt.wait(&c.full[qn % kSlots], (qn / kSlots) & 1)) return false;
+            if (boundary && !wt.wait(&c.row_full, 1)) return false;
             ptx::tc_fence_after();
             issue_ss(tS, r0, ringK + slot_of(qn));  // S^T(j+1): P^T(j) has been read by dV
             ptx::mma_commit(&c.s_full[0]);
             if (kMaps == 2 && j + 2 == n_cols) ptx::mma_commit(&c.row_free);
-          }
+            return true;
+          };
+          if (more && !boundary && !next_scores()) break;
           for (int g = 0; ok && g < 2; ++g) {
             ok = wt.wait(&c.ds_full[g], j & 1);
             if (!ok) break;
@@ -618,7 +623,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           }
           if (!ok) break;
           ptx::mma_commit(&c.empty[qi % kSlots]);
-          if (kMaps == 2 && j + 1 == n_cols) ptx::mma_commit(&c.acc_full);  // map 2 is complete
+          if (boundary) {
+            ptx::mma_commit(&c.acc_full);  // map 2 is complete
+            if (!next_scores()) break;
+          }
           if (more) {
             if (!wt.wait(&c.full[dn % kSlots], (dn / kSlots) & 1)) break;
             ptx::tc_fence_after();
@@ -750,6 +758,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
       const uint32_t tS = tmem + lane_off + col, tDP = tmem + lane_off + 128 + col;
       float *wrec = reinterpret_cast<float *>(smem + L::col_rec) + (warp - 2) * 128;  // [-L log2 e x 64 | -D x 64]
       const float4 *nl4 = reinterpret_cast<const float4 *>(wrec), *nd4 = reinterpret_cast<const float4 *>(wrec + 64);
+      // Differential form: this row's token (-1: none) and its patch, kept for the two
+      // epilogues in shared memory (registers are full) while the first scores are on their way.
+      int2 *place = reinterpret_cast<int2 *>(smem + L::place) + (threadIdx.x - 64);
+      auto row_place = [&] {
+        int t, y, x;
+        if (!tile_row_token(P.plan, P.g, row_tile, row_org, row, &t, &y, &x)) return make_int2(-1, 0);
+        return make_int2((t * P.g.H + y) * P.g.W + x,
+                         ((t / P.pt) * (P.g.H / P.ph) + y / P.ph) * (P.g.W / P.pw) + x / P.pw);
+      };
+      if (DIFF && MODE == kDkvWindow) *place = row_place();
       // unrolled: the two maps' epilogues differ (a rolled loop spills over 800 bytes a thread)
 #pragma unroll
       for (int m = 0; m < kMaps; ++m) {
@@ -872,14 +890,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
             if (last_map) pv4[i] = make_float4(dv[4 * i], dv[4 * i + 1], dv[4 * i + 2], dv[4 * i + 3]);
           }
         } else {
-          int t, y, x;
-          const bool token = (P.n_pool > 0 || !last_map) && tile_row_token(P.plan, P.g, row_tile, row_org, row, &t, &y, &x);
-          if (P.n_pool > 0 && token) {
+          int2 at = make_int2(-1, 0);
+          if (DIFF) at = *place;
+          else if (P.n_pool > 0) at = row_place();
+          if (P.n_pool > 0 && at.x >= 0) {
             // the pooled keys' gradient of this token's patch, spread evenly
-            const int pidx = ((t / P.pt) * (P.g.H / P.ph) + y / P.ph) * (P.g.W / P.pw) + x / P.pw;
-            const float4 *gk = reinterpret_cast<const float4 *>(P.dkvp + ((long long)unit * P.n_pool + pidx) * 128 + col);
+            const float4 *gk = reinterpret_cast<const float4 *>(P.dkvp + ((long long)unit * P.n_pool + at.y) * 128 + col);
             const float4 *gv = reinterpret_cast<const float4 *>(
-                P.dkvp + (((long long)kMaps * P.bh_count + bh) * P.n_pool + pidx) * 128 + col);
+                P.dkvp + (((long long)kMaps * P.bh_count + bh) * P.n_pool + at.y) * 128 + col);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float4 a = gk[i];
@@ -896,10 +914,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
             stage_row_half(row0, row, g, dk);  // the k and v tiles are no longer read
             stage_row_half(row1, row, g, dv);
             ptx::fence_proxy_async_smem();
-          } else if (token && !*reinterpret_cast<volatile int *>(&c.abort)) {
+          } else if (at.x >= 0 && !*reinterpret_cast<volatile int *>(&c.abort)) {
             // the key tile's place in shared memory is map 1's already: 128 bytes a thread
-            const long long tok = ((long long)t * P.g.H + y) * P.g.W + x;
-            uint4 *dst = reinterpret_cast<uint4 *>(P.dk + ((long long)unit * (P.g.N + P.n_text) + tok) * 128 + col);
+            uint4 *dst = reinterpret_cast<uint4 *>(P.dk + ((long long)unit * (P.g.N + P.n_text) + at.x) * 128 + col);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               dst[i] = make_uint4(ptx::pack_bf16x2(dk[8 * i], dk[8 * i + 1]), ptx::pack_bf16x2(dk[8 * i + 2], dk[8 * i + 3]),
