@@ -916,12 +916,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
             ptx::fence_proxy_async_smem();
           } else if (at.x >= 0 && !*reinterpret_cast<volatile int *>(&c.abort)) {
             // the key tile's place in shared memory is map 1's already: 128 bytes a thread
-            uint4 *dst = reinterpret_cast<uint4 *>(P.dk + ((long long)unit * (P.g.N + P.n_text) + at.x) * 128 + col);
+            __nv_bfloat16 *dst = P.dk + ((long long)unit * (P.g.N + P.n_text) + at.x) * 128 + col;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_uint4(ptx::pack_bf16x2(dk[8 * i], dk[8 * i + 1]), ptx::pack_bf16x2(dk[8 * i + 2], dk[8 * i + 3]),
-                                  ptx::pack_bf16x2(dk[8 * i + 4], dk[8 * i + 5]),
-                                  ptx::pack_bf16x2(dk[8 * i + 6], dk[8 * i + 7]));
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = ptx::pack_bf16x2(dk[16 * i + 2 * e], dk[16 * i + 2 * e + 1]);
+              ptx::st_global_v8(dst + 16 * i, w);
+            }
           }
         }
       }

@@ -22,6 +22,8 @@
 //   warp 0      loads: publishes the item (windows, routes), then its Q1, Q2 and the
 //               K1, K2, V stream through a 5-slot ring that runs on across items
 //   warp 1      issues the MMAs
+//   warps 2, 3  the next item's column masks, and its rows' tokens (1.4-2.5k and 1.4k cycles
+//               of plan lookups that the softmax warps, which bound a step, are spared)
 //   warps 4-11  softmax group g for map g, a thread per query row; then group g finishes
 //               columns [64 g, 64 g + 64) of the output rows
 #include <cudaTypedefs.h>
@@ -41,10 +43,12 @@ constexpr int kStages = 5;
 constexpr uint32_t kSmemQ = 0;                  // Q1, Q2
 constexpr uint32_t kSmemRing = 2 * kTileBytes;  // K1, K2, V ring
 constexpr uint32_t kSmemCtrl = kSmemRing + kStages * kTileBytes;
-constexpr uint32_t kCtrlBytes = 1024;
-constexpr uint32_t kSmemMask = kSmemCtrl + kCtrlBytes;  // 1 KB: an item's column masks, then its rows' sums
-constexpr int kMaskTable = 64;                          // key tiles whose column masks are tabled
-constexpr uint32_t kSmemBytes = kSmemMask + kMaskTable * 16 + 1024;  // + alignment slack
+constexpr uint32_t kCtrlBytes = 896;
+constexpr int kMaskTable = 36;                          // key tiles whose column masks are tabled
+constexpr uint32_t kSmemMask = kSmemCtrl + kCtrlBytes;  // two items' tables
+constexpr uint32_t kSmemRows = kSmemMask + 2 * kMaskTable * 16;  // 1 KB: the rows' tokens, then their sums
+constexpr uint32_t kSmemBytes = kSmemRows + 1024;
+static_assert(kSmemBytes <= 227u * 1024u, "shared memory above the 227 KB a CTA may hold");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSoftmax = 256;  // threads of the two softmax groups
 
@@ -56,25 +60,27 @@ struct Item {
 
 struct Ctrl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full, item_full[2], item_empty[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full, item_full[2], item_empty[2], mask_full[2], tok_full, o_read, drain;
   uint32_t tmem_base;
   int abort;
   Item item[2];
 };
 static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block too large");
 
-// 32 columns of a row, rounded to bfloat16: 64 bytes.
+// 32 columns of a row, rounded to bfloat16: 64 bytes, in whole 32-byte sectors (a warp's rows
+// lie in 32 lines, which is what a store costs: 16 bytes a thread took twice as long).
 __device__ __forceinline__ void store_cols32(__nv_bfloat16 *dst, const float *x) {
-  uint4 *p = reinterpret_cast<uint4 *>(dst);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    p[i] = make_uint4(ptx::pack_bf16x2(x[8 * i], x[8 * i + 1]), ptx::pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
-                      ptx::pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), ptx::pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = ptx::pack_bf16x2(x[16 * i + 2 * e], x[16 * i + 2 * e + 1]);
+    ptx::st_global_v8(dst + 16 * i, w);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __grid_constant__ AttnParams P) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // whole swizzle atoms: no room for a manual alignment
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + kSmemCtrl);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
@@ -86,11 +92,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
     ptx::mbar_init(&c.q_full, 1);
     ptx::mbar_init(&c.q_empty, 1);
     ptx::mbar_init(&c.o_full, 1);
+    ptx::mbar_init(&c.tok_full, 1);
+    ptx::mbar_init(&c.o_read, kSoftmax);
     for (int g = 0; g < 2; ++g) {
       ptx::mbar_init(&c.s_full[g], 1);
       ptx::mbar_init(&c.p_full[g], 128);
       ptx::mbar_init(&c.item_full[g], 1);
       ptx::mbar_init(&c.item_empty[g], kSoftmax + 1);
+      ptx::mbar_init(&c.mask_full[g], 1);
     }
     ptx::mbar_init(&c.drain, 1);
     c.abort = 0;
@@ -200,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
           const uint32_t vaddr = sRv + vslot * kTileDesc;
           const bool more = j + 1 < n_kt;
           ok = wt.wait(&c.full[vslot], (vi / kStages) & 1) && wt.wait(&c.p_full[0], parity);
-          // both groups read both of the previous item's outputs before their first P
-          if (ok && j == 0) ok = wt.wait(&c.p_full[1], parity);
+          // both groups read both of the previous item's outputs
+          if (ok && j == 0 && n > 0) ok = wt.wait(&c.o_read, (n - 1) & 1);
           if (!ok) break;
           ptx::tc_fence_after();
           issue_ts(tmem + 256, tmem, vaddr, j > 0);
@@ -223,7 +232,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
       drain.wait(&c.drain, 0);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp == 2) {
+    // ------------------------------------------------------------- column masks
+    Waiter wt{&c.abort, P.dev_err, P.timeout_ns, BASA_DEVERR_TIMEOUT_SOFTMAX, true};
+    for (int n = 0; !P.all_full; ++n) {
+      // an item is published once the softmax is through with the table of two items before
+      if (!__all_sync(0xFFFFFFFFu, wt.wait(&c.item_full[n & 1], (n >> 1) & 1))) break;
+      const Item &it = c.item[n & 1];
+      if (it.n_kt < 0) break;
+      for (int j = lane; j < min(it.n_kt, kMaskTable); j += 32) {
+        KeyIter t{0, j};
+        while (t.seg <= P.routed_k + 2 && t.t >= seg_tiles(P, it.keys, t.seg)) {
+          t.t -= seg_tiles(P, it.keys, t.seg);
+          ++t.seg;
+        }
+        uint32_t mk[4];
+        key_tile_mask(P, it.keys, t, mk);
+        reinterpret_cast<uint4 *>(smem + kSmemMask)[(n & 1) * kMaskTable + j] = make_uint4(mk[0], mk[1], mk[2], mk[3]);
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&c.mask_full[n & 1]);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------- the rows' tokens (-1: none)
+    Waiter wt{&c.abort, P.dev_err, P.timeout_ns, BASA_DEVERR_TIMEOUT_SOFTMAX, true};
+    for (int n = 0;; ++n) {
+      bool ok = wt.wait(&c.item_full[n & 1], (n >> 1) & 1);
+      // their place holds the previous item's sums until that is finished
+      if (ok && n > 0) ok = wt.wait(&c.item_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      const Item &it = c.item[n & 1];
+      if (it.n_kt < 0) break;
+      for (int r = lane; r < kTileRows; r += 32) {
+        int t, y, x;
+        const bool token = tile_row_token(P.plan, P.g, P.plan.tile[it.tile], it.keys.org[0], r, &t, &y, &x);
+        reinterpret_cast<int *>(smem + kSmemRows)[r] = token ? (t * P.g.H + y) * P.g.W + x : -1;
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&c.tok_full);
+    }
+  } else {
     // ------------------------------------------------------------- softmax
     const int g = (warp - 4) / 4;
     const int sub = warp % 4;  // TMEM lane quarter this warp may access
@@ -232,32 +280,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
     const uint32_t tS = tmem + lane_off + g * 128, tO = tmem + lane_off + 256 + g * 128;
     Waiter wt{&c.abort, P.dev_err, P.timeout_ns, BASA_DEVERR_TIMEOUT_SOFTMAX, true};
     const float sl2 = P.scale_log2;
-    float *sums = reinterpret_cast<float *>(smem + kSmemMask);  // [2][128]
+    float *sums = reinterpret_cast<float *>(smem + kSmemRows);  // [2][128]
     int step = 0;
     for (int n = 0;; ++n) {
       bool ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.item_full[n & 1], (n >> 1) & 1));
-      // Leaving is a common decision: the barriers below are met by all 256 threads or none.
-      if (ptx::named_barrier_any(1, kSoftmax, !ok)) break;
       const Item &it = c.item[n & 1];
-      const int n_kt = it.n_kt;
-      if (n_kt < 0) break;
-      if (!P.all_full) {
-        // Column masks of the item's key tiles in stream order, one tile per thread.
-        const int j = threadIdx.x - 128;
-        if (j < kMaskTable && j < n_kt) {
-          KeyIter t{0, j};
-          while (t.seg <= P.routed_k + 2 && t.t >= seg_tiles(P, it.keys, t.seg)) {
-            t.t -= seg_tiles(P, it.keys, t.seg);
-            ++t.seg;
-          }
-          uint32_t mk[4];
-          key_tile_mask(P, it.keys, t, mk);
-          reinterpret_cast<uint4 *>(smem + kSmemMask)[j] = make_uint4(mk[0], mk[1], mk[2], mk[3]);
-        }
-        ptx::named_barrier(1, kSoftmax);
-      }
+      const int n_kt = ok ? it.n_kt : -1;
+      ok = n_kt >= 0;
+      const uint4 *masks = reinterpret_cast<const uint4 *>(smem + kSmemMask) + (n & 1) * kMaskTable;
+      if (ok && !P.all_full) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.mask_full[n & 1], (n >> 1) & 1));
+      const int bh = ok ? it.bh : 0;
+      const float lam = __bfloat162float(P.lambda[bh % P.heads]);
       float m = -INFINITY, l = 0.f;
-      KeyIter key = first_key(P, it.keys);
+      KeyIter key{0, 0};  // past the table only
       for (int j = 0; ok && j < n_kt; ++j) {
         ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.s_full[g], (step + j) & 1));
         if (!ok) break;
@@ -267,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
         ptx::tmem_ld_wait(s);
         if (P.all_full) {
         } else if (j < kMaskTable) {
-          const uint4 mt = reinterpret_cast<const uint4 *>(smem + kSmemMask)[j];
+          const uint4 mt = masks[j];
           if ((mt.x & mt.y & mt.z & mt.w) != 0xFFFFFFFFu) {
             const uint32_t mask[4] = {mt.x, mt.y, mt.z, mt.w};
             apply_mask(s, mask);
@@ -307,56 +342,55 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
         ptx::tc_fence_before();
         ptx::mbar_arrive(&c.p_full[g]);
         if (j + 1 >= kMaskTable) {
-          if (j + 1 == kMaskTable)  // past the table: walk the stream from its start once
+          if (j + 1 == kMaskTable) {  // past the table: walk the stream from its start once
+            key = first_key(P, it.keys);
             for (int t = 0; t < kMaskTable; ++t) advance(P, it.keys, key);
-          else
+          } else {
             advance(P, it.keys, key);
+          }
         }
       }
       step += n_kt;
-      if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.o_full, n & 1));
+      if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.o_full, n & 1) && wt.wait(&c.tok_full, n & 1));
+      const int tok = ok ? reinterpret_cast<const int *>(smem + kSmemRows)[row] : -1;
+      // Leaving is a common decision (no items left, or a wait has expired): the barriers
+      // from here on are met by all 256 threads or by none.
+      if (ptx::named_barrier_any(1, kSoftmax, !ok)) break;
 
       // Group g: columns [64 g, 64 g + 64) of O1 / l1 - lambda O2 / l2 (a TMEM lane holds
       // the same query row of both). The sums cross over in shared memory, twice.
-      ptx::named_barrier(1, kSoftmax);  // the masks are no longer read
       sums[g * kTileRows + row] = 1.0f / l;
       ptx::named_barrier(1, kSoftmax);
-      const int bh = it.bh;
       const float i0 = sums[row], i1 = sums[kTileRows + row];
-      int t = 0, y = 0, x = 0;
-      const bool token = tile_row_token(P.plan, P.g, P.plan.tile[it.tile], it.keys.org[0], row, &t, &y, &x);
-      ptx::mbar_arrive(&c.item_empty[n & 1]);
-      const long long tok = ((long long)t * P.g.H + y) * P.g.W + x, at = ((long long)bh * P.g.N + tok) * 128 + 64 * g;
-      const float lam = __bfloat162float(P.lambda[bh % P.heads]);
-      float a[64] = {};  // initialised: else it would live on across items in registers
+      // an item cut short has set abort before: nothing of it is stored
+      const bool write = tok >= 0 && !*reinterpret_cast<volatile int *>(&c.abort);
+      const long long at = ((long long)bh * P.g.N + tok) * 128 + 64 * g;
+      ptx::tc_fence_after();
+      float a[64];
       float ss = 0.f;
-      if (ok) {
-        ptx::tc_fence_after();
-        // an item cut short has set abort before: nothing of it is stored
-        const bool write = token && !*reinterpret_cast<volatile int *>(&c.abort);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int cc = 2 * g + h;
-          uint32_t r0[32], r1[32];
-          ptx::tmem_ld32(tmem + lane_off + 256 + cc * 32, r0);
-          ptx::tmem_ld32(tmem + lane_off + 384 + cc * 32, r1);
-          ptx::tmem_ld_wait(r0);
-          ptx::tmem_ld_wait(r1);
-          float o2[32];
+      for (int h = 0; h < 2; ++h) {
+        const int cc = 2 * g + h;
+        uint32_t r0[32], r1[32];
+        ptx::tmem_ld32(tmem + lane_off + 256 + cc * 32, r0);
+        ptx::tmem_ld32(tmem + lane_off + 384 + cc * 32, r1);
+        ptx::tmem_ld_wait(r0);
+        ptx::tmem_ld_wait(r1);
+        float o2[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            o2[i] = __uint_as_float(r1[i]) * i1;
-            a[32 * h + i] = fmaf(-lam, o2[i], __uint_as_float(r0[i]) * i0);
-            ss = fmaf(a[32 * h + i], a[32 * h + i], ss);
-          }
-          if (write && P.second != nullptr) store_cols32(P.second + at + 32 * h, o2);
-          if (write && P.pre != nullptr) store_cols32(P.pre + at + 32 * h, a + 32 * h);
+        for (int i = 0; i < 32; ++i) {
+          o2[i] = __uint_as_float(r1[i]) * i1;
+          a[32 * h + i] = fmaf(-lam, o2[i], __uint_as_float(r0[i]) * i0);
+          ss = fmaf(a[32 * h + i], a[32 * h + i], ss);
         }
-        // log-sum-exp of this row's map: m and l are in base 2 of the scaled scores
-        if (write && P.lse != nullptr)
-          P.lse[(long long)(2 * bh + g) * P.g.N + tok] = (m + log2f(l)) * 0.6931471805599453f;
-        ptx::tc_fence_before();  // O is read: the next item's first P may follow
+        if (write && P.second != nullptr) store_cols32(P.second + at + 32 * h, o2);
+        if (write && P.pre != nullptr) store_cols32(P.pre + at + 32 * h, a + 32 * h);
       }
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(&c.o_read);  // the next item's products with V may start
+      // log-sum-exp of this row's map: m and l are in base 2 of the scaled scores
+      if (write && P.lse != nullptr)
+        P.lse[(long long)(2 * bh + g) * P.g.N + tok] = (m + log2f(l)) * 0.6931471805599453f;
       if (P.norm_weight != nullptr) {
         ptx::named_barrier(1, kSoftmax);
         sums[g * kTileRows + row] = ss;
@@ -374,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
           }
         }
       }
-      if (ok && token && !*reinterpret_cast<volatile int *>(&c.abort)) {
+      ptx::mbar_arrive(&c.item_empty[n & 1]);  // the item and the sums are read
+      if (write) {
         store_cols32(P.out + at, a);
         store_cols32(P.out + at + 32, a + 32);
       }

@@ -72,6 +72,7 @@ CASES = [
     Case("two_tiles_odd", "bf16", 1, 1, 128, (1, 15, 34), (1, 15, 17), (0, 7, 16), (1, 5, 17), 1),
     Case("ragged", "bf16", 1, 2, 128, (1, 48, 48), (1, 16, 16), (0, 8, 8), (1, 4, 4), 200, 0, norm=False),
     Case("routes16", "bf16", 1, 1, 128, (1, 20, 20), (1, 4, 4), (0, 1, 2), (0, 0, 0), 0, 16),
+    Case("many_key_tiles", "bf16", 1, 1, 128, (1, 62, 66), (1, 31, 66), (0, 5, 0), (1, 2, 2), 300, 1),
     Case("f32_d64", "f32", 2, 3, 64, (1, 16, 16), (1, 8, 8), (0, 4, 4), (1, 4, 4), 9, 1),
     Case("f32_d128", "f32", 1, 2, 128, (2, 6, 10), (1, 3, 5), (1, 2, 3), (2, 3, 5), 0, 2, norm=False),
     Case("f32_one_token", "f32", 1, 2, 64, (1, 1, 1), (1, 1, 1), (0, 0, 0)),
@@ -412,6 +413,35 @@ def test_offsets_past_32_bits():
         results.append((out[:, -2:], dq[:, -4:], dk[:, -4:], dv[:, -2:], dlam[-2:]))
         del out, saved, dq, dk, dv
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("c", [CASES[2], CASES[3], CASES[-2]], ids=["small", "wrap3d", "f32"])
+def test_tensors_on_16_byte_boundaries(c):
+    """Every tensor 16 bytes past a 32-byte boundary: the same bits."""
+
+    def moved(*shape, dtype):
+        n, pad = int(np.prod(shape)), 16 // torch.empty((), dtype=dtype).element_size()
+        t = torch.empty(n + pad, dtype=dtype, device="cuda")[pad:].view(shape)
+        assert t.data_ptr() % 32 == 16
+        return t
+
+    q, k, v, lam, w, dout, _ = c.inputs(7)
+
+    def step(args, layer):
+        out, saved = layer.attention_train(*args[:4], c.shift, args[4])
+        return (out, *layer.backward(*args[:4], c.shift, saved, args[5], args[4]))
+
+    args = [q, k, v, lam, w, dout]
+    ref = step(args, c.layer())
+    args = [None if t is None else moved(*t.shape, dtype=t.dtype).copy_(t) for t in args]
+    layer = c.layer()
+    plain = layer._new
+    layer._new = lambda *shape, dtype=None: plain(*shape, dtype=dtype) if dtype is torch.uint8 else moved(*shape, dtype=dtype or layer.dtype)
+    got = step(args, layer)
+    assert layer.device_error() == 0
+    for name, a, b in zip(("out", "dq", "dk", "dv", "dlam", "dweight"), got, ref):
+        if c.dtype == "bf16" or name not in ("dk", "dv"):  # float32 adds dk, dv with atomics
+            assert (a is None and b is None) or torch.equal(a, b), name
 
 
 def test_refused_tensors():
