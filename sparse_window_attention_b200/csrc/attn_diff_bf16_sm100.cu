@@ -23,7 +23,10 @@
 //               K1, K2, V stream through a 5-slot ring that runs on across items
 //   warp 1      issues the MMAs
 //   warps 2, 3  the next item's column masks, and its rows' tokens (1.4-2.5k and 1.4k cycles
-//               of plan lookups that the softmax warps, which bound a step, are spared)
+//               of plan lookups that the softmax warps, which bound a step, are spared);
+//               warp 2 also zeroes the rows of the V tiles that no load writes: P is 0 there,
+//               but what an earlier item left may be infinite or NaN. (The loader doing it
+//               cost 20%: it is within two steps of being late.)
 //   warps 4-11  softmax group g for map g, a thread per query row; then group g finishes
 //               columns [64 g, 64 g + 64) of the output rows
 #include <cudaTypedefs.h>
@@ -84,9 +87,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + kSmemCtrl);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
+  // Some window tile has rows that no load writes.
+  const bool pads = P.plan.zero_fill;
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(&c.full[i], 1);
+      ptx::mbar_init(&c.full[i], pads ? 2 : 1);
       ptx::mbar_init(&c.empty[i], 1);
     }
     ptx::mbar_init(&c.q_full, 1);
@@ -98,18 +104,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
       ptx::mbar_init(&c.s_full[g], 1);
       ptx::mbar_init(&c.p_full[g], 128);
       ptx::mbar_init(&c.item_full[g], 1);
-      ptx::mbar_init(&c.item_empty[g], kSoftmax + 1);
+      ptx::mbar_init(&c.item_empty[g], kSoftmax + (P.all_full ? 1 : 2));
       ptx::mbar_init(&c.mask_full[g], 1);
     }
     ptx::mbar_init(&c.drain, 1);
     c.abort = 0;
     ptx::fence_mbar_init();
-  }
-  if (P.plan.zero_fill) {
-    // Rows of a tile that no TMA box writes must hold finite values (P is 0 there).
-    uint4 *z = reinterpret_cast<uint4 *>(smem);
-    for (uint32_t i = threadIdx.x; i < kSmemCtrl / 16; i += kThreads) z[i] = make_uint4(0, 0, 0, 0);
-    ptx::fence_proxy_async_smem();
   }
   if (warp == 1) {
     ptx::tmem_alloc(&c.tmem_base, kTmemCols);
@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
               continue;
             }
             ptx::mbar_arrive_expect_tx(&c.full[slot], key_tile_bytes(P, it.keys, key));
+            if (pads && kv < 2) ptx::mbar_arrive(&c.full[slot]);  // V tiles: warp 2
             load_key_tile(P, it.keys, key, kv == 2, kv == 2 ? bh : 2 * bh + kv, smem + kSmemRing + slot * kTileBytes,
                           &c.full[slot]);
           }
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
   } else if (warp == 2) {
     // ------------------------------------------------------------- column masks
     Waiter wt{&c.abort, P.dev_err, P.timeout_ns, BASA_DEVERR_TIMEOUT_SOFTMAX, true};
+    int step = 0;  // key steps before this item
     for (int n = 0; !P.all_full; ++n) {
       // an item is published once the softmax is through with the table of two items before
       if (!__all_sync(0xFFFFFFFFu, wt.wait(&c.item_full[n & 1], (n >> 1) & 1))) break;
@@ -252,6 +254,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&c.mask_full[n & 1]);
+      const int n_kt = it.n_kt;
+      bool ok = true;
+      KeyIter key{0, 0};  // past the table only
+      for (int j = 0; ok && pads && j < n_kt; ++j) {
+        const int ring = 3 * (step + j) + 2, slot = ring % kStages;  // V_j
+        ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.empty[slot], ((ring / kStages) & 1) ^ 1));
+        if (!ok) break;
+        uint32_t mk[4];
+        if (j < kMaskTable) {
+          const uint4 t = reinterpret_cast<const uint4 *>(smem + kSmemMask)[(n & 1) * kMaskTable + j];
+          mk[0] = t.x; mk[1] = t.y; mk[2] = t.z; mk[3] = t.w;
+        } else {
+          if (j == kMaskTable) {
+            key = first_key(P, it.keys);
+            for (int t = 0; t < kMaskTable; ++t) advance(P, it.keys, key);
+          }
+          key_tile_mask(P, it.keys, key, mk);
+          advance(P, it.keys, key);
+        }
+        // pooled and text tiles are written whole; rows past their end read as zero
+        zero_unwritten_rows(smem + kSmemRing + slot * kTileBytes, mk, lane);
+        if (lane == 0) ptx::mbar_arrive(&c.full[slot]);
+      }
+      if (!ok) break;
+      step += n_kt;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&c.item_empty[n & 1]);
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------- the rows' tokens (-1: none)

@@ -139,6 +139,24 @@ __device__ __forceinline__ void store_window_tile(const WindowPlan &plan, const 
   }
 }
 
+// Zeroes the rows of a tile whose mask bit is clear, which no load writes (whole warp; the
+// writes are ordered before the loads and barrier arrivals that lane 0 issues afterwards).
+__device__ __forceinline__ void zero_unwritten_rows(uint8_t *tile, const uint32_t *mask, int lane) {
+  if ((mask[0] & mask[1] & mask[2] & mask[3]) == 0xFFFFFFFFu) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((mask[i] >> lane) & 1u) continue;
+    const uint32_t at = ptx::smem_u32(tile) + uint32_t(32 * i + lane) * 128u;
+#pragma unroll
+    for (uint32_t b = 0; b < 128; b += 16) {
+      ptx::st_shared_v4(at + b, 0, 0, 0, 0);
+      ptx::st_shared_v4(at + kHalfBytes + b, 0, 0, 0, 0);
+    }
+  }
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // Token (original grid coordinates) held by row `row` of a window tile; false for
 // a padding row.
 __device__ __forceinline__ bool tile_row_token(const WindowPlan &plan, const Geo &g, const PlanTile &tile,

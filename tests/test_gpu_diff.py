@@ -313,6 +313,33 @@ def test_nan_stays_in_its_head_and_window():
     assert torch.equal(out[~hit.cuda()], clean[~hit.cuda()])
 
 
+def test_nan_and_infinity_leave_other_heads_alone():
+    """Windows whose tiles have rows that no load writes, more of them than the GPU runs at
+    once: nothing that a bad head leaves behind reaches another one."""
+    c = Case("bad_heads", "bf16", 2, 24, 128, (3, 12, 26), (3, 6, 13), (0, 3, 6), (3, 6, 13), 5, 2)
+    q, k, v, lam, w, dout, _ = c.inputs(9)
+    layer = c.layer()
+    kp, vp, route = _keys(layer, q, k, v, c.shift)
+
+    def step():
+        out, saved = layer.attention_train(q, k, v, lam, c.shift, w, kp=kp, vp=vp, route_idx=route)
+        return (out, *layer.backward(q, k, v, lam, c.shift, saved, dout, w)[:4])
+
+    clean = step()
+    for b, h in ((0, 5), (1, 20)):
+        q[b, 2 * h, ::7], k[b, 2 * h + 1, ::5] = float("nan"), float("inf")
+        v[b, h, ::3], dout[b, h, ::11], vp[b, h] = float("nan"), float("-inf"), float("nan")
+    bad = step()
+    assert layer.device_error() == 0
+    heads = torch.ones(2, 24, dtype=torch.bool, device="cuda")
+    heads[0, 5] = heads[1, 20] = False
+    maps = heads.repeat_interleave(2, 1)
+    for name, x, y, keep in zip(("out", "dq", "dk", "dv"), bad, clean, (heads, maps, maps, heads)):
+        assert torch.equal(x[keep], y[keep]), name
+    keep = heads.all(0)
+    assert torch.equal(bad[4][keep], clean[4][keep]) and bad[4][~keep].isnan().all()
+
+
 def test_out_of_range_route_is_reported():
     c = CASES[4]
     q, k, v, lam, w, dout, _ = c.inputs()
