@@ -70,18 +70,6 @@ struct Ctrl {
 };
 static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block too large");
 
-// 32 columns of a row, rounded to bfloat16: 64 bytes, in whole 32-byte sectors (a warp's rows
-// lie in 32 lines, which is what a store costs: 16 bytes a thread took twice as long).
-__device__ __forceinline__ void store_cols32(__nv_bfloat16 *dst, const float *x) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = ptx::pack_bf16x2(x[16 * i + 2 * e], x[16 * i + 2 * e + 1]);
-    ptx::st_global_v8(dst + 16 * i, w);
-  }
-}
-
 __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __grid_constant__ AttnParams P) {
   extern __shared__ __align__(1024) uint8_t smem[];  // whole swizzle atoms: no room for a manual alignment
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + kSmemCtrl);
@@ -111,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
     c.abort = 0;
     ptx::fence_mbar_init();
   }
+  if (warp >= 4) touch_plan(P.plan, warp - 4, 8);
   if (warp == 1) {
     ptx::tmem_alloc(&c.tmem_base, kTmemCols);
     ptx::tmem_relinquish();
@@ -392,10 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
       ptx::named_barrier(1, kSoftmax);
       const float i0 = sums[row], i1 = sums[kTileRows + row];
       // an item cut short has set abort before: nothing of it is stored
-      const bool write = tok >= 0 && !*reinterpret_cast<volatile int *>(&c.abort);
-      const long long at = ((long long)bh * P.g.N + tok) * 128 + 64 * g;
+      const int row_to = *reinterpret_cast<volatile int *>(&c.abort) ? -1 : tok;
+      const long long at = (long long)bh * P.g.N * 128 + 64 * g;
       ptx::tc_fence_after();
-      float a[64];
+      float a[64], o2[64];
       float ss = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -405,20 +394,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
         ptx::tmem_ld32(tmem + lane_off + 384 + cc * 32, r1);
         ptx::tmem_ld_wait(r0);
         ptx::tmem_ld_wait(r1);
-        float o2[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          o2[i] = __uint_as_float(r1[i]) * i1;
-          a[32 * h + i] = fmaf(-lam, o2[i], __uint_as_float(r0[i]) * i0);
+          o2[32 * h + i] = __uint_as_float(r1[i]) * i1;
+          a[32 * h + i] = fmaf(-lam, o2[32 * h + i], __uint_as_float(r0[i]) * i0);
           ss = fmaf(a[32 * h + i], a[32 * h + i], ss);
         }
-        if (write && P.second != nullptr) store_cols32(P.second + at + 32 * h, o2);
-        if (write && P.pre != nullptr) store_cols32(P.pre + at + 32 * h, a + 32 * h);
       }
       ptx::tc_fence_before();
       ptx::mbar_arrive(&c.o_read);  // the next item's products with V may start
+      if (P.second != nullptr) store_rows64(P.second + at, row_to, o2, lane);
+      if (P.pre != nullptr) store_rows64(P.pre + at, row_to, a, lane);
       // log-sum-exp of this row's map: m and l are in base 2 of the scaled scores
-      if (write && P.lse != nullptr)
+      if (row_to >= 0 && P.lse != nullptr)
         P.lse[(long long)(2 * bh + g) * P.g.N + tok] = (m + log2f(l)) * 0.6931471805599453f;
       if (P.norm_weight != nullptr) {
         ptx::named_barrier(1, kSoftmax);
@@ -438,10 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
         }
       }
       ptx::mbar_arrive(&c.item_empty[n & 1]);  // the item and the sums are read
-      if (write) {
-        store_cols32(P.out + at, a);
-        store_cols32(P.out + at + 32, a + 32);
-      }
+      store_rows64(P.out + at, row_to, a, lane);
     }
   }
 

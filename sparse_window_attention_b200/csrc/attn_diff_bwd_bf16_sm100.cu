@@ -56,17 +56,6 @@ struct Item {
   RouteList keys;  // dq: the key stream's windows; window pass: org[0] of the key tile's window
 };
 
-// 64 columns of a row, rounded to bfloat16: 128 bytes.
-__device__ __forceinline__ void store_row64(__nv_bfloat16 *dst, const float (&x)[64]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = ptx::pack_bf16x2(x[16 * i + 2 * e], x[16 * i + 2 * e + 1]);
-    ptx::st_global_v8(dst + 16 * i, w);
-  }
-}
-
 // ---------------------------------------------------------------------------- dq pass
 constexpr int kDqSlots = 5;
 constexpr uint32_t kDqCtrl = kSmemRing + kDqSlots * kTileBytes;
@@ -104,6 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dq_kernel(const __grid_const
     c.abort = 0;
     ptx::fence_mbar_init();
   }
+  if (warp >= 2 && warp < 10) touch_plan(P.plan, warp - 2, 8);
   if (warp == 1) {
     ptx::tmem_alloc(&c.tmem_base, kTmemCols);
     ptx::tmem_relinquish();
@@ -216,17 +206,20 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dq_kernel(const __grid_const
     // ------------------------------------------------------------- items
     if (lane == 0) {
       const Waiter wt = waiter(BASA_DEVERR_TIMEOUT_PRODUCER, true);
-      for (int n = 0;; ++n) {
+      for (int n = 0, taken = 0;; ++n) {
         int id, tile_idx = 0, w = 0, bh = 0, wtype = 0;
-        for (;;) {
-          id = atomicAdd(P.next_item, 1);
+        for (;; ++taken) {  // the first by the CTA's number, the others from the counter
+          id = taken == 0 ? int(blockIdx.x) : int(gridDim.x) + atomicAdd(P.next_item, 1);
           if (id >= P.n_items) break;
           int ot, oy, ox;
           tile_idx = id % P.max_tiles;
           w = (id / P.max_tiles) % P.g.nWin;
           bh = id / (P.max_tiles * P.g.nWin);
           window_origin(P.g, w, &ot, &oy, &ox, &wtype);
-          if (tile_idx < P.plan.type[wtype].n_tiles) break;
+          if (tile_idx < P.plan.type[wtype].n_tiles) {
+            ++taken;
+            break;
+          }
           for (int i = 0; i < 8; ++i) P.dr[8ll * id + i] = 0.f;  // this window type has fewer query tiles
         }
         if (!wt.wait(&c.item_empty[n & 1], ((n >> 1) & 1) ^ 1)) break;
@@ -390,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dq_kernel(const __grid_const
       const float f = bh & 1 ? -P.scale * __bfloat162float(P.lambda[(bh >> 1) % P.heads]) : P.scale;
 #pragma unroll
       for (int i = 0; i < 64; ++i) x[i] *= f;
-      const bool write = !*reinterpret_cast<volatile int *>(&c.abort);
-      if (write && tok >= 0) store_row64(P.dq + ((long long)bh * P.g.N + tok) * 128 + col64, x);
+      const int row_to = *reinterpret_cast<volatile int *>(&c.abort) ? -1 : tok;
+      store_rows64(P.dq + (long long)bh * P.g.N * 128 + col64, row_to, x, lane);
       float even, odd;
       ptx::f2_unpack(dr2, even, odd);
       float d = tok >= 0 ? (even + odd) * dr_weight : 0.f;
@@ -424,7 +417,7 @@ static_assert(kDkvSmem <= 227u * 1024u, "shared memory above the 227 KB a CTA ma
 struct DkvCtrl {
   uint64_t full[kSlots], empty[kSlots];
   uint64_t k_full, k_free, v_full, v_free, s_full, dp_full, p_full[2], ds_full[2], acc_full, drain;
-  uint64_t item_full[2], item_empty[2];
+  uint64_t item_full[2], item_empty[2], place_full[2];
   uint32_t tmem_base;
   int abort;
   Item item[2];
@@ -447,7 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dkv_kernel(const __grid_cons
       ptx::mbar_init(&c.full[i], pads ? 2 : 1);
       ptx::mbar_init(&c.empty[i], 1);
     }
-    for (uint64_t *b : {&c.k_full, &c.k_free, &c.v_full, &c.v_free, &c.s_full, &c.dp_full, &c.acc_full, &c.drain})
+    for (uint64_t *b : {&c.k_full, &c.k_free, &c.v_full, &c.v_free, &c.s_full, &c.dp_full, &c.acc_full, &c.drain,
+                        &c.place_full[0], &c.place_full[1]})
       ptx::mbar_init(b, 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&c.p_full[i], 128);
@@ -458,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dkv_kernel(const __grid_cons
     c.abort = 0;
     ptx::fence_mbar_init();
   }
+  if (warp >= 2 && warp < 10) touch_plan(P.plan, warp - 2, 8);
   if (warp == 1) {
     ptx::tmem_alloc(&c.tmem_base, kTmemCols);
     ptx::tmem_relinquish();
@@ -666,14 +661,6 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dkv_kernel(const __grid_cons
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) cols += __shfl_xor_sync(0xFFFFFFFFu, cols, o);
-        for (int r = lane; r < kTileRows; r += 32) {
-          int t, y, x;
-          int2 at = make_int2(-1, 0);
-          if (tile_row_token(P.plan, P.g, P.plan.tile[tile], org, r, &t, &y, &x))
-            at = make_int2((t * P.g.H + y) * P.g.W + x,
-                           ((t / P.pt) * (P.g.H / P.ph) + y / P.ph) * (P.g.W / P.pw) + x / P.pw);
-          places[(n & 1) * kTileRows + r] = at;
-        }
       }
       __syncwarp();
       if (lane == 0) {
@@ -688,6 +675,18 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dkv_kernel(const __grid_cons
         ptx::mbar_arrive(&c.item_full[n & 1]);
       }
       if (cols < 0) break;
+      if (!LONG) {
+        for (int r = lane; r < kTileRows; r += 32) {
+          int t, y, x;
+          int2 at = make_int2(-1, 0);
+          if (tile_row_token(P.plan, P.g, P.plan.tile[tile], org, r, &t, &y, &x))
+            at = make_int2((t * P.g.H + y) * P.g.W + x,
+                           ((t / P.pt) * (P.g.H / P.ph) + y / P.ph) * (P.g.W / P.pw) + x / P.pw);
+          places[(n & 1) * kTileRows + r] = at;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&c.place_full[n & 1]);
+      }
       ++n;
     }
     __syncwarp();
@@ -820,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dkv_kernel(const __grid_cons
         }
         t0 += n_cols;
         if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.acc_full, m));  // two maps an item
+        if (ok && !LONG && m == 0) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.place_full[n & 1], (n >> 1) & 1));
         if (!ok) continue;
         if (!LONG && n == 0) ptx::grid_wait();  // the pooled keys' gradients
         ptx::tc_fence_after();
@@ -875,8 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dkv_kernel(const __grid_cons
               }
             }
             const long long rows = P.g.N + P.n_text;
-            if (write && at.x >= 0)
-              store_row64((which ? P.dv + (bh * rows + at.x) * 128 : P.dk + (unit * rows + at.x) * 128) + col, x);
+            store_rows64((which ? P.dv + bh * rows * 128 : P.dk + unit * rows * 128) + col, write ? at.x : -1, x, lane);
           }
         }
       }

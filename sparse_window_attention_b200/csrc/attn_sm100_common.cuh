@@ -7,6 +7,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
@@ -155,6 +156,45 @@ __device__ __forceinline__ void zero_unwritten_rows(uint8_t *tile, const uint32_
   }
   ptx::fence_proxy_async_smem();
   __syncwarp();
+}
+
+// Stores 64 columns of a warp's 32 rows, rounded to bfloat16: lane's row goes to base + 128
+// row (row < 0: nowhere). Eight lanes trade 16-byte chunks first, so that a store writes
+// whole 128-byte lines: a lane writing its own row touches 32 lines a store, which took
+// 2k cycles for 256 rows.
+__device__ __forceinline__ void store_rows64(__nv_bfloat16 *base, int row, const float *x, int lane) {
+  uint32_t w[8][4];
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[c][e] = ptx::pack_bf16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1) {  // 8 x 8 transposition: chunk c of lane l <-> chunk l of lane c
+    const bool up = lane & s;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c & s) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[c][e] : w[c | s][e], s);
+        if (up) w[c][e] = got;
+        else w[c | s][e] = got;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = __shfl_sync(0xFFFFFFFFu, row, (lane & 24) | i);
+    if (r >= 0)
+      *reinterpret_cast<uint4 *>(base + (long long)r * 128 + 8 * (lane & 7)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+  }
+}
+
+// Reads the part of the plan that the launch uses, a few entries a warp, so that its first
+// reads (kernel parameters: a miss each) do not queue up behind one another.
+__device__ __forceinline__ void touch_plan(const WindowPlan &plan, int warp, int warps) {
+  for (int i = 2 * warp; i < plan.n_tiles; i += 2 * warps) asm volatile("" ::"r"(int(plan.tile[i].valid_rows)));
+  for (int i = 8 * warp; i < plan.n_pieces; i += 8 * warps) asm volatile("" ::"r"(int(plan.piece[i].dest)));
 }
 
 // Token (original grid coordinates) held by row `row` of a window tile; false for

@@ -58,19 +58,6 @@ __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t nthreads) {
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// 32 bytes to global memory: one store where the address is a multiple of 32 (the tensors
-// need be aligned to 16 only), else two.
-__device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&v)[8]) {
-  if (reinterpret_cast<uintptr_t>(p) & 16u) {
-    reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 // Named barrier that returns whether any of its threads came with `x` set (the same in all).
 __device__ __forceinline__ bool named_barrier_any(uint32_t id, uint32_t nthreads, bool x) {
   uint32_t r;
