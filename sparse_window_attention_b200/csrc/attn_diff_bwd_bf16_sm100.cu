@@ -1,7 +1,7 @@
 // Backward of the differential attention, bfloat16, head_dim 128, for sm_100a.
 //
 // out = O1 - lambda O2, two softmax maps over one key list that share their values. With g
-// the gradient behind the norm and {-L log2 e, -D, weight, 0} a record of each map's rows
+// the gradient behind the norm and {-L log2 e, -D, weight, token} a record of each map's rows
 // (both taken beforehand):
 //   P_m = exp(q_m K_m^T / sqrt(d) - L_m),  dS_m = P_m (g V^T - D_m),  f_1 = 1, f_2 = -lambda,
 //   dq_m = f_m dS_m K_m / sqrt(d),  dK_m = f_m dS_m^T q_m / sqrt(d),  dV = sum_m f_m P_m^T g.
@@ -49,6 +49,29 @@ constexpr uint32_t kSmemRing = 2 * kTileBytes;  // then a ring of 32 KB tiles
 constexpr uint32_t kCtrlBytes = 1024;
 constexpr uint32_t kTmemCols = 512;
 
+// id -> (tile, window, unit) and the window's origin, by unsigned 32-bit division: these stand
+// at the head of everything a CTA does.
+struct WorkItem {
+  int tile, w, bh, wtype, org[3];
+};
+__device__ __forceinline__ void origin_of(const Geo &g, int w, int *org, int *wtype) {
+  const uint32_t row = uint32_t(w) / uint32_t(g.nWx), jt = row / uint32_t(g.nWy);
+  const int jx = w - int(row) * g.nWx, jy = int(row - jt * uint32_t(g.nWy));
+  org[0] = wrap(int(jt) * g.wt + g.st, g.T);
+  org[1] = wrap(jy * g.wh + g.sy, g.H);
+  org[2] = wrap(jx * g.ww + g.sx, g.W);
+  *wtype = (org[0] + g.wt > g.T ? 1 : 0) | (org[1] + g.wh > g.H ? 2 : 0) | (org[2] + g.ww > g.W ? 4 : 0);
+}
+__device__ __forceinline__ WorkItem work_item(const BwdParams &P, int id) {
+  WorkItem x;
+  const uint32_t rest = uint32_t(id) / uint32_t(P.max_tiles);
+  x.tile = id - int(rest) * P.max_tiles;
+  x.bh = int(rest / uint32_t(P.g.nWin));
+  x.w = int(rest) - x.bh * P.g.nWin;
+  origin_of(P.g, x.w, x.org, &x.wtype);
+  return x;
+}
+
 struct Item {
   int n_cols;  // tiles that are streamed (of one map); < 0: there are no more items
   int bh;      // dq: unit of q; dK/dV: unit of v
@@ -66,7 +89,7 @@ static_assert(kDqSmem <= 227u * 1024u, "shared memory above the 227 KB a CTA may
 struct DqCtrl {
   uint64_t full[kDqSlots], empty[kDqSlots];
   uint64_t row_full, a_ready, s_full, s_free, dp_full, ds_full, acc_full, drain;
-  uint64_t item_full[2], item_empty[2], rec_full, rec_empty;
+  uint64_t item_full[2], item_empty[2];
   uint32_t tmem_base;
   int abort;
   Item item[2];
@@ -76,7 +99,7 @@ static_assert(sizeof(DqCtrl) <= kCtrlBytes, "control block too large");
 __global__ void __launch_bounds__(kThreads, 1) diff_dq_kernel(const __grid_constant__ BwdParams P) {
   extern __shared__ __align__(1024) uint8_t smem[];  // whole swizzle atoms: no room for a manual alignment
   DqCtrl &c = *reinterpret_cast<DqCtrl *>(smem + kDqCtrl);
-  float4 *recs = reinterpret_cast<float4 *>(smem + kDqRec);
+  float4 *recs = reinterpret_cast<float4 *>(smem + kDqRec);  // as loaded; padding rows {0, 0, 0, -1}
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const bool pads = P.plan.zero_fill;  // some window tile has rows that no load writes
   if (threadIdx.x == 0) {
@@ -84,11 +107,12 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dq_kernel(const __grid_const
       ptx::mbar_init(&c.full[i], pads && i < 3 ? 2 : 1);
       ptx::mbar_init(&c.empty[i], 1);
     }
-    for (uint64_t *b : {&c.row_full, &c.s_full, &c.dp_full, &c.acc_full, &c.drain, &c.rec_full}) ptx::mbar_init(b, 1);
-    for (uint64_t *b : {&c.a_ready, &c.s_free, &c.ds_full, &c.rec_empty}) ptx::mbar_init(b, kCompute);
+    for (uint64_t *b : {&c.s_full, &c.dp_full, &c.acc_full, &c.drain}) ptx::mbar_init(b, 1);
+    ptx::mbar_init(&c.row_full, pads ? 2 : 1);
+    for (uint64_t *b : {&c.a_ready, &c.s_free, &c.ds_full}) ptx::mbar_init(b, kCompute);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&c.item_full[i], 1);
-      ptx::mbar_init(&c.item_empty[i], kCompute + 3);  // compute threads, loader, MMA, record warp
+      ptx::mbar_init(&c.item_empty[i], kCompute + (pads ? 3 : 2));  // compute threads, loader, MMA, warp 11
     }
     c.abort = 0;
     ptx::fence_mbar_init();
@@ -120,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dq_kernel(const __grid_const
         // the row tiles are read once the item before has them in TMEM
         if (n > 0 && !wt.wait(&c.a_ready, (n - 1) & 1)) break;
         const PlanTile &qt = P.plan.tile[it.tile];
-        ptx::mbar_arrive_expect_tx(&c.row_full, uint32_t(qt.valid_rows) * 512u);
+        ptx::mbar_arrive_expect_tx(&c.row_full, uint32_t(qt.valid_rows) * (512u + 16u));
+        load_window_records(P.plan, P.g, P.map_rec, qt, it.keys.org[0], bh, smem + kDqRec, &c.row_full);
         load_window_tile(P.plan, P.g, P.map_q, qt, it.keys.org[0], bh, row0, &c.row_full);
         load_window_tile(P.plan, P.g, P.map_do, qt, it.keys.org[0], bh >> 1, row1, &c.row_full);
         ++row_loads;
@@ -207,16 +232,13 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dq_kernel(const __grid_const
     if (lane == 0) {
       const Waiter wt = waiter(BASA_DEVERR_TIMEOUT_PRODUCER, true);
       for (int n = 0, taken = 0;; ++n) {
-        int id, tile_idx = 0, w = 0, bh = 0, wtype = 0;
+        int id;
+        WorkItem x;
         for (;; ++taken) {  // the first by the CTA's number, the others from the counter
           id = taken == 0 ? int(blockIdx.x) : int(gridDim.x) + atomicAdd(P.next_item, 1);
           if (id >= P.n_items) break;
-          int ot, oy, ox;
-          tile_idx = id % P.max_tiles;
-          w = (id / P.max_tiles) % P.g.nWin;
-          bh = id / (P.max_tiles * P.g.nWin);
-          window_origin(P.g, w, &ot, &oy, &ox, &wtype);
-          if (tile_idx < P.plan.type[wtype].n_tiles) {
+          x = work_item(P, id);
+          if (x.tile < P.plan.type[x.wtype].n_tiles) {
             ++taken;
             break;
           }
@@ -226,18 +248,18 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dq_kernel(const __grid_const
         Item &it = c.item[n & 1];
         it.n_cols = -1;
         if (id < P.n_items) {
-          it.bh = bh;
+          it.bh = x.bh;
           it.id = id;
-          it.tile = P.plan.type[wtype].first_tile + tile_idx;
-          window_origin(P.g, w, &it.keys.org[0][0], &it.keys.org[0][1], &it.keys.org[0][2], &it.keys.wtype[0]);
+          it.tile = P.plan.type[x.wtype].first_tile + x.tile;
+          it.keys.wtype[0] = x.wtype;
+          for (int a = 0; a < 3; ++a) it.keys.org[0][a] = x.org[a];
           for (int r = 0; r < P.routed_k; ++r) {
-            int u = P.route[((long long)(bh >> 1) * P.g.nWin + w) * P.routed_k + r];
+            int u = P.route[((long long)(x.bh >> 1) * P.g.nWin + x.w) * P.routed_k + r];
             if (u < 0 || u >= P.g.nWin) {  // reported, and replaced by the own window: accesses stay in bounds
               if (P.dev_err) atomicOr(P.dev_err, BASA_DEVERR_BAD_ROUTE);
-              u = w;
+              u = x.w;
             }
-            window_origin(P.g, u, &it.keys.org[1 + r][0], &it.keys.org[1 + r][1], &it.keys.org[1 + r][2],
-                          &it.keys.wtype[1 + r]);
+            origin_of(P.g, u, it.keys.org[1 + r], &it.keys.wtype[1 + r]);
           }
           int cols = 0;
           for (int s = 0; s <= P.routed_k + 2; ++s) cols += seg_tiles(P, it.keys, s);
@@ -250,31 +272,25 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dq_kernel(const __grid_const
     }
     __syncwarp();
   } else if (warp == 11) {
-    // ----------------------------------- the rows' records, and the key tiles' unwritten rows
-    const Waiter wt = waiter(BASA_DEVERR_TIMEOUT_SOFTMAX, true);
+    // ------------------------------- what no load writes: records of padding rows, rows of key tiles
+    const Waiter wt = waiter(BASA_DEVERR_TIMEOUT_PRODUCER, true);
     int col = 0;
-    for (int n = 0;; ++n) {
+    for (int n = 0; pads; ++n) {
       bool ok = wt.wait(&c.item_full[n & 1], (n >> 1) & 1);
-      if (ok && n > 0) ok = wt.wait(&c.rec_empty, (n - 1) & 1);
+      if (ok && n > 0) ok = wt.wait(&c.a_ready, (n - 1) & 1);  // the records before are read
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       const Item &it = c.item[n & 1];
       if (it.n_cols < 0) break;
-      for (int r = lane; r < kTileRows; r += 32) {
-        int t, y, x;
-        float4 rec = make_float4(0.f, 0.f, 0.f, __int_as_float(-1));  // a padding row
-        if (tile_row_token(P.plan, P.g, P.plan.tile[it.tile], it.keys.org[0], r, &t, &y, &x)) {
-          const int tok = (t * P.g.H + y) * P.g.W + x;
-          rec = P.rec[(long long)it.bh * P.g.N + tok];
-          rec.w = __int_as_float(tok);
-        }
-        recs[r] = rec;
-      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!((P.plan.tile[it.tile].mask[i] >> lane) & 1u))
+          recs[32 * i + lane] = make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&c.rec_full);
+      if (lane == 0) ptx::mbar_arrive(&c.row_full);
       const int n_cols = it.n_cols;
       KeyIter key;
       key_first(P, it.keys, key);
-      for (int j = 0; ok && pads && j < n_cols; ++j, ++col) {
+      for (int j = 0; ok && j < n_cols; ++j, ++col) {
         const int slot = dq_slot(col, false);
         ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.empty[slot], dq_phase(col, false) ^ 1));
         if (!ok) break;
@@ -307,9 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dq_kernel(const __grid_const
       if (!__all_sync(0xFFFFFFFFu, wt.wait(&c.item_full[n & 1], (n >> 1) & 1))) return false;
       n_cols = c.item[n & 1].n_cols;
       if (n_cols < 0) return true;
-      if (!__all_sync(0xFFFFFFFFu, wt.wait(&c.rec_full, n & 1) && wt.wait(&c.row_full, n & 1))) return false;
+      if (!__all_sync(0xFFFFFFFFu, wt.wait(&c.row_full, n & 1))) return false;
       rec = recs[row];
-      ptx::mbar_arrive(&c.rec_empty);
       uint32_t w[32];
       load_row_half(row0, row, g, w);
       ptx::tmem_st32(tmem + lane_off + 384 + 32 * g, w);
@@ -417,7 +432,7 @@ static_assert(kDkvSmem <= 227u * 1024u, "shared memory above the 227 KB a CTA ma
 struct DkvCtrl {
   uint64_t full[kSlots], empty[kSlots];
   uint64_t k_full, k_free, v_full, v_free, s_full, dp_full, p_full[2], ds_full[2], acc_full, drain;
-  uint64_t item_full[2], item_empty[2], place_full[2];
+  uint64_t rows_known[2], item_full[2], item_empty[2], place_full[2];
   uint32_t tmem_base;
   int abort;
   Item item[2];
@@ -441,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dkv_kernel(const __grid_cons
       ptx::mbar_init(&c.empty[i], 1);
     }
     for (uint64_t *b : {&c.k_full, &c.k_free, &c.v_full, &c.v_free, &c.s_full, &c.dp_full, &c.acc_full, &c.drain,
-                        &c.place_full[0], &c.place_full[1]})
+                        &c.place_full[0], &c.place_full[1], &c.rows_known[0], &c.rows_known[1]})
       ptx::mbar_init(b, 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&c.p_full[i], 128);
@@ -473,11 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dkv_kernel(const __grid_cons
       int ring = 0, k_loads = 0, v_loads = 0, tile_no = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
-        if (!wt.wait(&c.item_full[n & 1], (n >> 1) & 1)) break;
+        if (!wt.wait(&c.rows_known[n & 1], (n >> 1) & 1)) break;
         const Item &it = c.item[n & 1];
-        const int n_cols = it.n_cols, bh = it.bh, n_windows = windows_of(it);
+        const int bh = it.bh;
         const int16_t *list = lists + (n & 1) * kMaxList;
-        if (n_cols < 0) break;
+        if (*reinterpret_cast<const volatile int *>(&it.n_cols) < 0) break;
+        int n_cols = 0, n_windows = 0;
         const bool pooled = LONG && it.tile < P.n_pool_tiles;
         // This item's key tile of map (unit) or its value tile.
         auto load_rows = [&](bool is_v, int unit, uint8_t *dst, uint64_t *bar) {
@@ -504,6 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dkv_kernel(const __grid_cons
             if (!ok) break;
             load_rows(true, bh, row1, &c.v_full);
             ++v_loads;
+            if (!(ok = wt.wait(&c.item_full[n & 1], (n >> 1) & 1))) break;
+            n_cols = *reinterpret_cast<const volatile int *>(&it.n_cols);
+            n_windows = windows_of(it);
           }
           QIter q;
           q_first(P, list, kMode, LONG ? it.chunk * P.chunk_tiles : 0, q);
@@ -618,70 +637,73 @@ __global__ void __launch_bounds__(kThreads, 1) diff_dkv_kernel(const __grid_cons
     const Waiter wt = waiter(BASA_DEVERR_TIMEOUT_PRODUCER, true);
     int n = 0;
     for (int id = blockIdx.x;; id += gridDim.x) {
-      int bh = 0, w = 0, tile = 0, chunk = 0, wtype = 0, org[3] = {0, 0, 0}, cols = -1, count = 0;
+      WorkItem x{};
+      int chunk = 0, cols = -1;
       if (id < P.n_items) {
         if (LONG) {
-          chunk = id % P.n_chunks;
-          tile = (id / P.n_chunks) % P.n_long_tiles;
-          bh = id / (P.n_chunks * P.n_long_tiles);
+          const uint32_t rest = uint32_t(id) / uint32_t(P.n_chunks);
+          chunk = id - int(rest) * P.n_chunks;
+          x.bh = int(rest / uint32_t(P.n_long_tiles));
+          x.tile = int(rest) - x.bh * P.n_long_tiles;
           cols = min(P.chunk_tiles, P.q_tiles - chunk * P.chunk_tiles);
         } else {
-          tile = id % P.max_tiles;
-          w = (id / P.max_tiles) % P.g.nWin;
-          bh = id / (P.max_tiles * P.g.nWin);
-          window_origin(P.g, w, &org[0], &org[1], &org[2], &wtype);
-          if (tile >= P.plan.type[wtype].n_tiles) continue;  // this window type has fewer tiles
-          tile += P.plan.type[wtype].first_tile;
+          x = work_item(P, id);
+          if (x.tile >= P.plan.type[x.wtype].n_tiles) continue;  // this window type has fewer tiles
+          x.tile += P.plan.type[x.wtype].first_tile;
+          cols = 1;
         }
       }
       if (!__all_sync(0xFFFFFFFFu, wt.wait(&c.item_empty[n & 1], ((n >> 1) & 1) ^ 1))) break;
-      if (!LONG && id < P.n_items) {
+      if (lane == 0) {  // the key and value tiles can load; how many query tiles there are follows
+        Item &it = c.item[n & 1];
+        it.n_cols = cols;
+        it.bh = x.bh;
+        it.tile = x.tile;
+        it.chunk = chunk;
+        for (int a = 0; a < 3; ++a) it.keys.org[0][a] = x.org[a];
+        ptx::mbar_arrive(&c.rows_known[n & 1]);
+      }
+      if (!LONG && cols > 0) {
         // The query windows that see the key tile: w itself, then every window that routed
         // to w, in ascending id (ordered ballot compaction: a fixed order).
         int16_t *list = lists + (n & 1) * kMaxList;
-        count = 1;
-        if (lane == 0) list[0] = int16_t(w);
+        int count = 1;
+        if (lane == 0) list[0] = int16_t(x.w);
         for (int w0 = 0; P.routed_k > 0 && w0 < P.g.nWin; w0 += 32) {
-          const int x = w0 + lane;
+          const int u = w0 + lane;
           bool hit = false;
-          if (x < P.g.nWin && x != w) {
-            const int32_t *r = P.route + ((long long)bh * P.g.nWin + x) * P.routed_k;
-            for (int i = 0; i < P.routed_k; ++i) hit |= r[i] == w;
+          if (u < P.g.nWin && u != x.w) {
+            const int32_t *r = P.route + ((long long)x.bh * P.g.nWin + u) * P.routed_k;
+            for (int i = 0; i < P.routed_k; ++i) hit |= r[i] == x.w;
           }
           const uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit);
-          if (hit) list[count + __popc(hits & ((1u << lane) - 1u))] = int16_t(x);
+          if (hit) list[count + __popc(hits & ((1u << lane) - 1u))] = int16_t(u);
           count += __popc(hits);
         }
         __syncwarp();
-        cols = 0;
+        int total = 0;
         for (int i = lane; i < count; i += 32) {
-          int a, b, d, t;
-          window_origin(P.g, list[i], &a, &b, &d, &t);
-          cols += P.plan.type[t].n_tiles;
+          int org[3], t;
+          origin_of(P.g, list[i], org, &t);
+          total += P.plan.type[t].n_tiles;
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) cols += __shfl_xor_sync(0xFFFFFFFFu, cols, o);
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+        if (lane == 0) {
+          c.item[n & 1].n_cols = total;
+          c.item[n & 1].n_list = count;
+        }
       }
       __syncwarp();
-      if (lane == 0) {
-        Item &it = c.item[n & 1];
-        it.n_cols = cols;
-        it.bh = bh;
-        it.id = id;
-        it.tile = tile;
-        it.chunk = chunk;
-        it.n_list = count;
-        for (int a = 0; a < 3; ++a) it.keys.org[0][a] = org[a];
-        ptx::mbar_arrive(&c.item_full[n & 1]);
-      }
+      if (lane == 0) ptx::mbar_arrive(&c.item_full[n & 1]);
       if (cols < 0) break;
       if (!LONG) {
         for (int r = lane; r < kTileRows; r += 32) {
-          int t, y, x;
+          int t, y, l;
           int2 at = make_int2(-1, 0);
-          if (tile_row_token(P.plan, P.g, P.plan.tile[tile], org, r, &t, &y, &x))
-            at = make_int2((t * P.g.H + y) * P.g.W + x,
-                           ((t / P.pt) * (P.g.H / P.ph) + y / P.ph) * (P.g.W / P.pw) + x / P.pw);
+          if (tile_row_token(P.plan, P.g, P.plan.tile[x.tile], x.org, r, &t, &y, &l))
+            at = make_int2((t * P.g.H + y) * P.g.W + l,
+                           ((t / P.pt) * (P.g.H / P.ph) + y / P.ph) * (P.g.W / P.pw) + l / P.pw);
           places[(n & 1) * kTileRows + r] = at;
         }
         __syncwarp();

@@ -143,7 +143,8 @@ struct PrepArgs {
   const void *pre, *second, *dout, *lambda, *weight;
   const float *lse;  // [units][2][rows]
   void *g;           // [units][rows][d]; unused without weight (g = dout)
-  float4 *rec;       // nullable: records {-L log2 e, -D, weight of dR in -dlambda, 0} [units][2][rows]
+  float4 *rec;       // nullable: records {-L log2 e, -D, weight of dR in -dlambda, the row itself (an
+                     // int's bits)} [units][2][rows]
   float *drow;       // nullable: D alone, [units][2][rows]
   int *counter;      // nullable: set to 0
   float *part;       // [blocks][1 + d]: sum g . O2, then the weight's gradient
@@ -224,7 +225,8 @@ __global__ void __launch_bounds__(kDiffThreads) diff_prep_kernel(const __grid_co
     if (valid && c < 2) {
       const long long m = (2 * unit + c) * a.rows + r;
       const float d = c == 0 ? fmaf(lam, d2, da) : d2;
-      if (a.rec) a.rec[m] = make_float4(-a.lse[m] * 1.4426950408889634f, -d, c == 0 ? -c2 : fmaf(c2, lam, 1.f), 0.f);
+      if (a.rec) a.rec[m] = make_float4(-a.lse[m] * 1.4426950408889634f, -d, c == 0 ? -c2 : fmaf(c2, lam, 1.f),
+                                       __int_as_float(int(r)));
       if (a.drow) a.drow[m] = d;
     }
   }
