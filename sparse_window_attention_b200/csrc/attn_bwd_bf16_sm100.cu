@@ -28,27 +28,47 @@
 //                MMAs; the epilogue adds the pooled-key gradient of each token's
 //                patch / |patch| and stores dk, dv at the tokens' positions.
 //
+// Differential form (template argument DIFF; out = O1 - lambda O2 of two maps that share
+// their values, the norm's gradient g taken beforehand and D per map in the records): the
+// dq pass runs over the maps, with map 2's sums scaled by -lambda in its epilogue, and adds
+// up each row's dS (what its D was off by), which lambda's gradient takes in. The
+// dK/dV passes run both maps of a (batch, head) in ONE CTA, map 2 first: its dK leaves,
+// the dV accumulator is multiplied by -lambda in TMEM, and map 1 adds to it, so the two
+// maps' dV meet without a buffer or an atomic. (Both maps at once, sharing dout V^T, would
+// take six 128-column accumulators and TMEM holds four.) The passes overlap at their ends by
+// programmatic dependent launch: the long pass runs first, on fewer CTAs than there are SMs
+// as often as not, and the dq pass, which needs nothing of it, fills the rest; the window
+// pass starts under the reduction and waits for it before its epilogue.
+//
 // Warp roles (320 threads): warp 0 TMA loads, warp 1 issues tcgen05 MMAs (one
 // thread), warps 2-9 compute P and dS: two warpgroups, each owning 64 of the 128
 // columns of a row (the backward has no row reductions, so the columns split
 // freely), a thread per (row, column half). Every wait is bounded (globaltimer):
 // on expiry a bit goes to dev_err and the kernel drains and returns.
+#include <cuda_bf16.h>
+
 #include <algorithm>
 #include <cmath>
 #include <cstring>
 
-#include "attn_bwd_sm100.cuh"
+#include "attn_sm100_common.cuh"
+#include "basa_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace basa {
 namespace {
 
 using namespace sm100;
 
+enum Mode { kDq = 0, kDkvWindow = 1, kDkvLong = 2 };
+
 constexpr int kThreads = 320;
 constexpr int kMaxSlots = 5;
 constexpr uint32_t kSmemRow = 0;                            // the two row tiles
 constexpr uint32_t kSmemRing = 2 * kTileBytes;              // then a ring of 32 KB tiles
+constexpr uint32_t kRecBytes = kTileRows * 16;              // 128 records of 16 bytes
 constexpr uint32_t kCtrlBytes = 1024;
+constexpr int kMaxList = 4096;                              // windows whose query tiles one key tile sees
 constexpr uint32_t kTmemCols = 512;
 
 constexpr uint32_t kColRecBytes = 8 * 128 * 4;             // per compute warp: 64 x {-L log2 e}, 64 x {-D}
@@ -66,24 +86,190 @@ struct Smem {
   static constexpr uint32_t col_rec = rec + (MODE == kDq ? 0u : 2 * kRecBytes);
   static constexpr uint32_t ctrl = col_rec + (MODE == kDq ? 0u : kColRecBytes);
   static constexpr uint32_t list = ctrl + kCtrlBytes;
-  static constexpr uint32_t bytes = list + (MODE == kDkvWindow ? kMaxList * 2 : 0) + 1024;  // + alignment slack
+  static constexpr uint32_t place = list + (MODE == kDkvWindow ? kMaxList * 2 : 0);  // differential form
+  static constexpr uint32_t bytes = place + (MODE == kDkvWindow ? 256 * 8 : 0) + 1024;  // + alignment slack
   static_assert(bytes <= 227u * 1024u, "shared memory of a pass above the 227 KB a CTA may hold");
 };
+
+struct alignas(64) BwdParams {
+  CUtensorMap map_q[kMaxShapes], map_k[kMaxShapes], map_v[kMaxShapes], map_do[kMaxShapes];
+  CUtensorMap map_rec[kMaxShapes];                 // per-token records {-L log2 e, -D, 0, 0}
+  CUtensorMap map_dq[kMaxShapes], map_dk[kMaxShapes], map_dv[kMaxShapes];
+  CUtensorMap map_kp, map_vp, map_kt, map_vt;      // pooled and text rows, 128-row boxes
+  WindowPlan plan;
+  const int32_t *route;
+  int32_t *dev_err;
+  const float4 *rec;  // the records, [bh][N] (dq pass: each thread reads its row's)
+  const float *dkvp;  // final pooled-key gradients: dkp [bh][Np][128], then dvp
+  float *part;        // long key tiles: [bh][tile][chunk][dK (of each map) | dV][128][128] partial sums
+  const __nv_bfloat16 *lambda;  // differential form: [heads]
+  __nv_bfloat16 *dk;            // differential form: dk itself, for map 2's rows
+  float *dr;                    // differential form: [map][window][query tile] sums of rec.z (sum dS)
+  int heads;
+  Geo g;
+  int bh_count;  // units of v, dout and the routes (differential form: q, k have two for each)
+  int routed_k, n_pool, n_text, n_pool_tiles, n_text_tiles, n_long_tiles;
+  int pt, ph, pw;
+  float inv_patch;
+  float scale_log2;  // log2(e) / sqrt(d)
+  float scale;       // 1 / sqrt(d)
+  uint32_t flags;    // basa_params.flags (test hook: skip the first ring load)
+  int all_full;      // every tile of the streams is full: no column masks
+  int max_tiles;     // most tiles of a window type
+  int n_chunks, chunk_tiles, q_tiles;  // long mode: query tiles of a head, split in chunks
+  unsigned long long timeout_ns;
+};
+static_assert(sizeof(BwdParams) <= 32764, "window plan too large for the kernel parameter space");
 
 struct Ctrl {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   // dq pass: a_ready, s_full[0], s_free, dp_full[0], ds_full[0]; dK/dV passes: s_full[0],
   // dp_full[0], and per compute group p_full[g], ds_full[g]
-  uint64_t row_full, s_full[2], dp_full[2], s_free, a_ready, p_full[2], ds_full[2], acc_full, drain;
+  uint64_t row_full, row_free, s_full[2], dp_full[2], s_free, a_ready, p_full[2], ds_full[2], acc_full, drain;
   uint32_t tmem_base;
   int abort;
   int n_cols;   // column tiles streamed by this CTA
   int n_list;   // dK/dV window mode: windows in the list
-  RouteList keys;
+  int wtype[1 + kMaxRouted];
+  int org[1 + kMaxRouted][3];
 };
 static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block too large");
 
-template <int MODE>
+// ------------------------------------------------------------- dq pass: the key stream
+// Segments 0..routed_k are windows (own, then routed), then pooled, then text.
+struct KeyIter {
+  int seg, t;
+};
+__device__ __forceinline__ int seg_tiles(const BwdParams &P, const Ctrl &c, int seg) {
+  if (seg <= P.routed_k) return P.plan.type[c.wtype[seg]].n_tiles;
+  return seg == P.routed_k + 1 ? P.n_pool_tiles : P.n_text_tiles;
+}
+__device__ __forceinline__ void key_first(const BwdParams &P, const Ctrl &c, KeyIter &it) {
+  it.seg = 0;
+  it.t = 0;
+  while (it.seg <= P.routed_k + 2 && seg_tiles(P, c, it.seg) == 0) ++it.seg;
+}
+__device__ __forceinline__ void key_next(const BwdParams &P, const Ctrl &c, KeyIter &it) {
+  ++it.t;
+  while (it.seg <= P.routed_k + 2 && it.t >= seg_tiles(P, c, it.seg)) {
+    ++it.seg;
+    it.t = 0;
+  }
+}
+__device__ __forceinline__ uint32_t load_key(const BwdParams &P, const Ctrl &c, const KeyIter &it, bool is_v, int bh,
+                                             uint8_t *dst, uint64_t *bar) {  // bh: unit of the tensor read
+  if (it.seg <= P.routed_k) {
+    const PlanTile &tile = P.plan.tile[P.plan.type[c.wtype[it.seg]].first_tile + it.t];
+    load_window_tile(P.plan, P.g, is_v ? P.map_v : P.map_k, tile, c.org[it.seg], bh, dst, bar);
+    return uint32_t(tile.valid_rows) * 256u;
+  }
+  const bool pooled = it.seg == P.routed_k + 1;
+  const CUtensorMap *map = pooled ? (is_v ? &P.map_vp : &P.map_kp) : (is_v ? &P.map_vt : &P.map_kt);
+  const int row = pooled ? it.t * kTileRows : P.g.N + it.t * kTileRows;
+  ptx::tma_load_3d(dst, map, bar, 0, row, bh);
+  ptx::tma_load_3d(dst + kHalfBytes, map, bar, 64, row, bh);
+  return kTileBytes;
+}
+__device__ __forceinline__ void key_mask(const BwdParams &P, const Ctrl &c, const KeyIter &it, uint32_t *m) {
+  if (it.seg <= P.routed_k) {
+    const PlanTile &tile = P.plan.tile[P.plan.type[c.wtype[it.seg]].first_tile + it.t];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = tile.mask[i];
+    return;
+  }
+  const bool pooled = it.seg == P.routed_k + 1;
+  prefix_mask(min(kTileRows, (pooled ? P.n_pool : P.n_text) - it.t * kTileRows), m);
+}
+
+// ------------------------------------------------------------- dK/dV passes: the query stream
+// Window list entry li (window mode: the smem list; long mode: window li itself) and
+// tile t of it.
+struct QIter {
+  int li, t, ntiles, type, org[3];
+};
+__device__ __forceinline__ void q_load(const BwdParams &P, const int16_t *list, int mode, QIter &it) {
+  const int w = mode == kDkvLong ? it.li : int(list[it.li]);
+  window_origin(P.g, w, &it.org[0], &it.org[1], &it.org[2], &it.type);
+  it.ntiles = P.plan.type[it.type].n_tiles;
+}
+// Positions the iterator at global query tile `skip` of the window sequence.
+__device__ __forceinline__ void q_first(const BwdParams &P, const int16_t *list, int mode, int skip, QIter &it) {
+  it.li = 0;
+  it.t = 0;
+  q_load(P, list, mode, it);
+  while (skip >= it.ntiles) {
+    skip -= it.ntiles;
+    ++it.li;
+    q_load(P, list, mode, it);
+  }
+  it.t = skip;
+}
+__device__ __forceinline__ void q_next(const BwdParams &P, const int16_t *list, int mode, int n_windows, QIter &it) {
+  if (++it.t < it.ntiles) return;
+  it.t = 0;
+  if (++it.li < n_windows) q_load(P, list, mode, it);
+}
+__device__ __forceinline__ const PlanTile &q_tile(const BwdParams &P, const QIter &it) {
+  return P.plan.tile[P.plan.type[it.type].first_tile + it.t];
+}
+
+// dq pass ring: key tile j in slot j % 3 (read by S(j) and, much later, dq(j)),
+// value tile j in slot 3 + j % 2 (read by dP(j) only), so the next key tiles load
+// while earlier ones still wait for their dq product, and value tile j + 1 loads
+// while dP(j) is computed and read.
+__device__ __forceinline__ int dq_slot(int j, bool is_v) { return is_v ? 3 + (j & 1) : j % 3; }
+__device__ __forceinline__ uint32_t dq_phase(int j, bool is_v) { return is_v ? ((j >> 1) & 1) : ((j / 3) & 1); }
+
+// Sets the columns whose mask bit is clear to 0 (m0: columns 0-31, m1: 32-63).
+__device__ __forceinline__ void zero_masked(float (&x)[64], uint32_t m0, uint32_t m1) {
+#pragma unroll
+  for (int i = 0; i < 64; ++i)
+    if (!(((i < 32 ? m0 : m1) >> (i & 31)) & 1u)) x[i] = 0.f;
+}
+
+// Packs 64 fp32 values (pairs 2i, 2i+1) into 32 bf16x2 words.
+__device__ __forceinline__ void pack64(const float (&x)[64], uint32_t (&w)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) w[i] = ptx::pack_bf16x2(x[2 * i], x[2 * i + 1]);
+}
+
+// 64 consecutive TMEM columns of this thread's lane, as floats.
+__device__ __forceinline__ void tmem_ld64f(uint32_t taddr, float (&x)[64]) {
+  uint32_t r[64];
+  ptx::tmem_ld64(taddr, r);
+  ptx::tmem_ld_wait(r);
+#pragma unroll
+  for (int i = 0; i < 64; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+// Writes 64 bf16 values (columns [64 half, 64 half + 64) of row `row`) into a
+// swizzled 128-row staging tile.
+__device__ __forceinline__ void stage_row_half(uint8_t *tile, int row, int half, const float (&x)[64]) {
+  const uint32_t base = ptx::smem_u32(tile) + uint32_t(half) * kHalfBytes + uint32_t(row) * 128u;
+  const uint32_t swz = row & 7;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    ptx::st_shared_v4(base + ((uint32_t(c) ^ swz) << 4), ptx::pack_bf16x2(x[8 * c], x[8 * c + 1]),
+                      ptx::pack_bf16x2(x[8 * c + 2], x[8 * c + 3]), ptx::pack_bf16x2(x[8 * c + 4], x[8 * c + 5]),
+                      ptx::pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
+}
+
+// Reads 64 bf16 values (columns [64 half, 64 half + 64) of row `row`) from a swizzled
+// 128-row tile as 32 bf16x2 words, the layout of an MMA A operand in TMEM.
+__device__ __forceinline__ void load_row_half(const uint8_t *tile, int row, int half, uint32_t (&w)[32]) {
+  const uint8_t *base = tile + uint32_t(half) * kHalfBytes + uint32_t(row) * 128u;
+  const uint32_t swz = row & 7;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(base + ((uint32_t(c) ^ swz) << 4));
+    w[4 * c] = v.x;
+    w[4 * c + 1] = v.y;
+    w[4 * c + 2] = v.z;
+    w[4 * c + 3] = v.w;
+  }
+}
+
+template <int MODE, bool DIFF>
 __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid_constant__ BwdParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -92,6 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + L::ctrl);
   int16_t *list = reinterpret_cast<int16_t *>(smem + L::list);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (DIFF && MODE == kDkvLong) ptx::grid_launch_dependents();
+  // What follows the dq pass needs the long pass's sums: one CTA of it ends after them.
+  const bool last_to_end = DIFF && MODE == kDq && blockIdx.x == gridDim.x - 1 && threadIdx.x == 0;
 
   // ----------------------------------------------------------- unit of this CTA
   int bh, w = 0, tile_idx = 0, kt = 0, chunk = 0, ot = 0, oy = 0, ox = 0, wtype = 0;
@@ -104,8 +293,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     w = (blockIdx.x / P.max_tiles) % P.g.nWin;
     bh = blockIdx.x / (P.max_tiles * P.g.nWin);
     window_origin(P.g, w, &ot, &oy, &ox, &wtype);
-    if (tile_idx >= P.plan.type[wtype].n_tiles) return;  // whole CTA: this window type has fewer tiles
+    if (tile_idx >= P.plan.type[wtype].n_tiles) {  // whole CTA: this window type has fewer tiles
+      if (DIFF && MODE == kDq && threadIdx.x == 0) P.dr[blockIdx.x] = 0.f;
+      if (last_to_end) ptx::grid_wait();
+      return;
+    }
   }
+  // Units: bh counts maps in the dq pass and values (two maps each) in the dK/dV passes.
+  const int bh_v = DIFF && MODE == kDq ? bh >> 1 : bh;       // unit of v, dout and the routes
+  constexpr int kMaps = DIFF && MODE != kDq ? 2 : 1;         // maps this CTA goes through
+  auto map_unit = [&](int m) { return kMaps == 2 ? 2 * bh + 1 - m : bh; };  // unit of q, k of its m-th map
+  const float neg_lambda = DIFF ? -__bfloat162float(P.lambda[bh_v % P.heads]) : 1.f;
   const int row_org[3] = {ot, oy, ox};
   const PlanTile &row_tile = P.plan.tile[P.plan.type[wtype].first_tile + tile_idx];  // window modes
 
@@ -115,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
       ptx::mbar_init(&c.empty[i], 1);
     }
     ptx::mbar_init(&c.row_full, 1);
+    ptx::mbar_init(&c.row_free, 1);
     const uint32_t per_group = MODE == kDq ? 256 : 128;  // compute threads that arrive
     for (int g = 0; g < 2; ++g) {
       ptx::mbar_init(&c.s_full[g], 1);
@@ -128,21 +327,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     ptx::mbar_init(&c.drain, 1);
     c.abort = 0;
     if (MODE == kDq) {
-      c.keys.wtype[0] = wtype;
-      c.keys.org[0][0] = ot; c.keys.org[0][1] = oy; c.keys.org[0][2] = ox;
+      c.wtype[0] = wtype;
+      c.org[0][0] = ot; c.org[0][1] = oy; c.org[0][2] = ox;
       for (int r = 0; r < P.routed_k; ++r) {
-        int u = P.route[((long long)bh * P.g.nWin + w) * P.routed_k + r];
+        int u = P.route[((long long)bh_v * P.g.nWin + w) * P.routed_k + r];
         if (u < 0 || u >= P.g.nWin) {  // reported, and replaced by the own window: accesses stay in bounds
           if (P.dev_err) atomicOr(P.dev_err, BASA_DEVERR_BAD_ROUTE);
           u = w;
         }
         int a, b, d, t;
         window_origin(P.g, u, &a, &b, &d, &t);
-        c.keys.wtype[1 + r] = t;
-        c.keys.org[1 + r][0] = a; c.keys.org[1 + r][1] = b; c.keys.org[1 + r][2] = d;
+        c.wtype[1 + r] = t;
+        c.org[1 + r][0] = a; c.org[1 + r][1] = b; c.org[1 + r][2] = d;
       }
       int n = 0;
-      for (int s = 0; s <= P.routed_k + 2; ++s) n += seg_tiles(P, c.keys, s);
+      for (int s = 0; s <= P.routed_k + 2; ++s) n += seg_tiles(P, c, s);
       c.n_cols = n;
     } else if (MODE == kDkvLong) {
       c.n_cols = max(0, min(P.chunk_tiles, P.q_tiles - chunk * P.chunk_tiles));
@@ -210,26 +409,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
       if (MODE == kDq) {
         ptx::mbar_arrive_expect_tx(&c.row_full, uint32_t(row_tile.valid_rows) * 512u);
         load_window_tile(P.plan, P.g, P.map_q, row_tile, row_org, bh, row0, &c.row_full);
-        load_window_tile(P.plan, P.g, P.map_do, row_tile, row_org, bh, row1, &c.row_full);
+        load_window_tile(P.plan, P.g, P.map_do, row_tile, row_org, bh_v, row1, &c.row_full);
       } else if (MODE == kDkvWindow) {
         ptx::mbar_arrive_expect_tx(&c.row_full, uint32_t(row_tile.valid_rows) * 512u);
-        load_window_tile(P.plan, P.g, P.map_k, row_tile, row_org, bh, row0, &c.row_full);
+        load_window_tile(P.plan, P.g, P.map_k, row_tile, row_org, map_unit(0), row0, &c.row_full);
         load_window_tile(P.plan, P.g, P.map_v, row_tile, row_org, bh, row1, &c.row_full);
       } else {
         const bool pooled = kt < P.n_pool_tiles;
         const CUtensorMap *mk = pooled ? &P.map_kp : &P.map_kt, *mv = pooled ? &P.map_vp : &P.map_vt;
         const int row = pooled ? kt * kTileRows : P.g.N + (kt - P.n_pool_tiles) * kTileRows;
         ptx::mbar_arrive_expect_tx(&c.row_full, 2 * kTileBytes);
-        ptx::tma_load_3d(row0, mk, &c.row_full, 0, row, bh);
-        ptx::tma_load_3d(row0 + kHalfBytes, mk, &c.row_full, 64, row, bh);
+        ptx::tma_load_3d(row0, mk, &c.row_full, 0, row, map_unit(0));
+        ptx::tma_load_3d(row0 + kHalfBytes, mk, &c.row_full, 64, row, map_unit(0));
         ptx::tma_load_3d(row1, mv, &c.row_full, 0, row, bh);
         ptx::tma_load_3d(row1 + kHalfBytes, mv, &c.row_full, 64, row, bh);
       }
-      int last = -1, last_k = -1, last_v = -1;
+      int last = -1, last_k = -1, last_v = -1, row_loads = 1;
       bool skipped0 = false;  // test hook: the first ring item was never loaded
       if (MODE == kDq) {
         KeyIter it;
-        key_first(P, c.keys, it);
+        key_first(P, c, it);
         for (int j = 0; j < n_cols; ++j) {
           bool ok = true;
           for (int kv = 0; kv < 2; ++kv) {
@@ -241,48 +440,66 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
               continue;
             }
             const uint32_t bytes = it.seg <= P.routed_k
-                                       ? uint32_t(P.plan.tile[P.plan.type[c.keys.wtype[it.seg]].first_tile + it.t].valid_rows) * 256u
+                                       ? uint32_t(P.plan.tile[P.plan.type[c.wtype[it.seg]].first_tile + it.t].valid_rows) * 256u
                                        : kTileBytes;
             ptx::mbar_arrive_expect_tx(&c.full[slot], bytes);
-            load_key(P, c.keys, it, kv == 1, bh, smem + kSmemRing + slot * kTileBytes, &c.full[slot]);
+            load_key(P, c, it, kv == 1, kv == 1 ? bh_v : bh, smem + kSmemRing + slot * kTileBytes, &c.full[slot]);
             (kv ? last_v : last_k) = j;
           }
           if (!ok) break;
-          key_next(P, c.keys, it);
+          key_next(P, c, it);
         }
       } else if (n_cols > 0) {
-        QIter it;
-        q_first(P, list, MODE, MODE == kDkvLong ? chunk * P.chunk_tiles : 0, it);
-        for (int j = 0; j < n_cols; ++j) {
-          bool ok = true;
-          const PlanTile &tile = q_tile(P, it);
-          for (int kv = 0; kv < 2; ++kv) {
-            const int item = 2 * j + kv, slot = item % kSlots;
-            if (!wt.wait(&c.empty[slot], ((item / kSlots) & 1) ^ 1)) { ok = false; break; }
-            if (item == 0 && (P.flags & BASA_FLAG_TEST_SKIP_FIRST_KEY_LOAD)) {
-              skipped0 = true;
-              last = 0;
-              continue;
-            }
-            uint8_t *dst = smem + kSmemRing + slot * kTileBytes;
-            if (kv == 0) {  // q tile and its records (record buffer j & 1, freed with the q slot)
-              ptx::mbar_arrive_expect_tx(&c.full[slot], uint32_t(tile.valid_rows) * (256u + 16u));
-              load_window_tile(P.plan, P.g, P.map_q, tile, it.org, bh, dst, &c.full[slot]);
-              load_window_records(P.plan, P.g, P.map_rec, tile, it.org, bh, smem + L::rec + (j & 1) * kRecBytes,
-                                  &c.full[slot]);
+        bool ok = true;
+        for (int m = 0; ok && m < kMaps; ++m) {
+          const int unit = map_unit(m);
+          if (m == 1) {  // the key tile of map 1, once the last product with map 2's has read it
+            if (!wt.wait(&c.row_free, 0)) break;
+            const bool pooled = MODE == kDkvLong && kt < P.n_pool_tiles;
+            if (MODE == kDkvWindow) {
+              ptx::mbar_arrive_expect_tx(&c.row_full, uint32_t(row_tile.valid_rows) * 256u);
+              load_window_tile(P.plan, P.g, P.map_k, row_tile, row_org, unit, row0, &c.row_full);
             } else {
-              ptx::mbar_arrive_expect_tx(&c.full[slot], uint32_t(tile.valid_rows) * 256u);
-              load_window_tile(P.plan, P.g, P.map_do, tile, it.org, bh, dst, &c.full[slot]);
+              const CUtensorMap *mk = pooled ? &P.map_kp : &P.map_kt;
+              const int row = pooled ? kt * kTileRows : P.g.N + (kt - P.n_pool_tiles) * kTileRows;
+              ptx::mbar_arrive_expect_tx(&c.row_full, kTileBytes);
+              ptx::tma_load_3d(row0, mk, &c.row_full, 0, row, unit);
+              ptx::tma_load_3d(row0 + kHalfBytes, mk, &c.row_full, 64, row, unit);
             }
-            last = item;
+            row_loads = 2;
           }
-          if (!ok) break;
-          q_next(P, list, MODE, n_windows, it);
+          QIter it;
+          q_first(P, list, MODE, MODE == kDkvLong ? chunk * P.chunk_tiles : 0, it);
+          for (int j = m * n_cols; j < (m + 1) * n_cols; ++j) {
+            const PlanTile &tile = q_tile(P, it);
+            for (int kv = 0; kv < 2; ++kv) {
+              const int item = 2 * j + kv, slot = item % kSlots;
+              if (!wt.wait(&c.empty[slot], ((item / kSlots) & 1) ^ 1)) { ok = false; break; }
+              if (item == 0 && (P.flags & BASA_FLAG_TEST_SKIP_FIRST_KEY_LOAD)) {
+                skipped0 = true;
+                last = 0;
+                continue;
+              }
+              uint8_t *dst = smem + kSmemRing + slot * kTileBytes;
+              if (kv == 0) {  // q tile and its records (record buffer j & 1, freed with the q slot)
+                ptx::mbar_arrive_expect_tx(&c.full[slot], uint32_t(tile.valid_rows) * (256u + 16u));
+                load_window_tile(P.plan, P.g, P.map_q, tile, it.org, unit, dst, &c.full[slot]);
+                load_window_records(P.plan, P.g, P.map_rec, tile, it.org, unit, smem + L::rec + (j & 1) * kRecBytes,
+                                    &c.full[slot]);
+              } else {
+                ptx::mbar_arrive_expect_tx(&c.full[slot], uint32_t(tile.valid_rows) * 256u);
+                load_window_tile(P.plan, P.g, P.map_do, tile, it.org, bh, dst, &c.full[slot]);
+              }
+              last = item;
+            }
+            if (!ok) break;
+            q_next(P, list, MODE, n_windows, it);
+          }
         }
       }
       // Drain: wait for the copies still in flight (immediate when all were consumed).
       // A slot's earlier copies completed before the slot was granted again.
-      drain.wait(&c.row_full, 0);
+      drain.wait(&c.row_full, (row_loads - 1) & 1);
       if (MODE == kDq) {
         for (int j = max(0, last_k - 2); j <= last_k; ++j)
           if (j > 0 || !skipped0) drain.wait(&c.full[dq_slot(j, false)], dq_phase(j, false));
@@ -354,11 +571,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
         // is in TMEM. S^T and dP^T stay whole N = 128 products (an N = 64 half reads
         // the same A operand from shared memory for half the work).
         const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
+        // Differential form: tiles [0, n_cols) are map 2's, [n_cols, 2 n_cols) map 1's.
+        const int total = kMaps * n_cols;
         ok = wt.wait(&c.full[0], 0);
         if (ok) {
           ptx::tc_fence_after();
           issue_ss(tS, r0, ringK + slot_of(0));  // S^T(0) = K q0^T
           ptx::mma_commit(&c.s_full[0]);
+          if (kMaps == 2 && n_cols == 1) ptx::mma_commit(&c.row_free);
           ok = wt.wait(&c.full[1], 0);
         }
         if (ok) {
@@ -366,9 +586,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           issue_ss(tDP, r1, ringK + slot_of(1));  // dP^T(0) = V dout0^T
           ptx::mma_commit(&c.dp_full[0]);
         }
-        for (int j = 0; ok && j < n_cols; ++j) {
+        for (int j = 0; ok && j < total; ++j) {
           const int qi = 2 * j, di = 2 * j + 1, qn = qi + 2, dn = di + 2;
-          const bool more = j + 1 < n_cols;
+          const bool more = j + 1 < total;
+          const bool map_start = j == 0 || (kMaps == 2 && j == n_cols);
+          if (kMaps == 2 && j == n_cols) {
+            // both groups have read map 2's dK and rescaled dV before their first P^T
+            ok = wt.wait(&c.p_full[0], j & 1) && wt.wait(&c.p_full[1], j & 1);
+            if (!ok) break;
+          }
           for (int g = 0; ok && g < 2; ++g) {
             ok = wt.wait(&c.p_full[g], j & 1);
             if (!ok) break;
@@ -377,20 +603,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           }
           if (!ok) break;
           ptx::mma_commit(&c.empty[di % kSlots]);
-          if (more) {
-            if (!wt.wait(&c.full[qn % kSlots], (qn / kSlots) & 1)) break;
+          // Map 2's last tile: its dK first, which does not wait for map 1's key tile.
+          const bool boundary = kMaps == 2 && j + 1 == n_cols;
+          auto next_scores = [&] {
+            if (!wt.wait(&c.full[qn % kSlots], (qn / kSlots) & 1)) return false;
+            if (boundary && !wt.wait(&c.row_full, 1)) return false;
             ptx::tc_fence_after();
             issue_ss(tS, r0, ringK + slot_of(qn));  // S^T(j+1): P^T(j) has been read by dV
             ptx::mma_commit(&c.s_full[0]);
-          }
+            if (kMaps == 2 && j + 2 == n_cols) ptx::mma_commit(&c.row_free);
+            return true;
+          };
+          if (more && !boundary && !next_scores()) break;
           for (int g = 0; ok && g < 2; ++g) {
             ok = wt.wait(&c.ds_full[g], j & 1);
             if (!ok) break;
             ptx::tc_fence_after();
-            issue_ts_group(tDK, tDP, ringMn + slot_of(qi), g, j > 0 || g > 0);  // dK += dS^T(j) q_j
+            issue_ts_group(tDK, tDP, ringMn + slot_of(qi), g, !map_start || g > 0);  // dK += dS^T(j) q_j
           }
           if (!ok) break;
           ptx::mma_commit(&c.empty[qi % kSlots]);
+          if (boundary) {
+            ptx::mma_commit(&c.acc_full);  // map 2 is complete
+            if (!next_scores()) break;
+          }
           if (more) {
             if (!wt.wait(&c.full[dn % kSlots], (dn / kSlots) & 1)) break;
             ptx::tc_fence_after();
@@ -417,12 +653,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     bool ok = true;
     if (MODE == kDq) {
       const uint32_t tS = tmem + lane_off + col, tDP = tmem + lane_off + 128 + col;
+      float dr_weight = 0.f;
+      uint64_t dr2 = 0;            // sums of this row's dS (even and odd columns)
       uint64_t nl2 = 0, nd2 = 0;  // this row's -L log2 e and -D, paired for packed arithmetic
       int t, y, x;                // (a padding row keeps 0, 0: its dS is 0 as its dout row is 0)
       if (n_cols > 0 && tile_row_token(P.plan, P.g, row_tile, row_org, row, &t, &y, &x)) {
         const float4 rec = P.rec[(long long)bh * P.g.N + ((long long)t * P.g.H + y) * P.g.W + x];
         nl2 = ptx::f2_pack(rec.x, rec.x);
         nd2 = ptx::f2_pack(rec.y, rec.y);
+        dr_weight = rec.z;
       }
       if (n_cols > 0) {
         // This row's q and dout (this group's 64 of the head dims) into TMEM, where the
@@ -441,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
       }
       const uint64_t sl2x2 = ptx::f2_pack(sl2, sl2);
       KeyIter it;
-      key_first(P, c.keys, it);
+      key_first(P, c, it);
       for (int j = 0; ok && j < n_cols; ++j) {
         ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.s_full[0], j & 1));
         if (!ok) break;
@@ -451,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
         ptx::tc_fence_before();
         ptx::mbar_arrive(&c.s_free);  // S(j) is in registers: the MMA may overwrite it
         uint32_t m[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (!P.all_full) key_mask(P, c.keys, it, m);
+        if (!P.all_full) key_mask(P, c, it, m);
         const uint32_t m0 = m[2 * g], m1 = m[2 * g + 1];
 #pragma unroll
         for (int i = 0; i < 64; i += 2) {
@@ -473,13 +712,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           s[i + 1] = d1;
         }
         if ((m0 & m1) != 0xFFFFFFFFu) zero_masked(s, m0, m1);  // warp-uniform: a partial key tile
+        if (DIFF) {
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) dr2 = ptx::fadd2(dr2, ptx::f2_pack(s[i], s[i + 1]));
+        }
         uint32_t pk[32];
         pack64(s, pk);
         ptx::tmem_st32(tDP, pk);  // dS (bf16) over the first half of this thread's dP columns
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&c.ds_full[0]);
-        key_next(P, c.keys, it);
+        key_next(P, c, it);
       }
       if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.acc_full, 0));
       if (ok) {
@@ -487,11 +730,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
         float x[64];
         tmem_ld64f(tmem + lane_off + 256 + col, x);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) x[i] *= P.scale;
+        for (int i = 0; i < 64; ++i) x[i] *= DIFF && (bh & 1) ? P.scale * neg_lambda : P.scale;
         stage_row_half(row0, row, g, x);  // the q tile is no longer read
         ptx::fence_proxy_async_smem();
+        if (DIFF) {  // the 256 half rows' weighted sums, in a fixed order (the dout tile is no longer read)
+          float even, odd;
+          ptx::f2_unpack(dr2, even, odd);
+          float d = (even + odd) * dr_weight;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+          if (lane == 0) reinterpret_cast<float *>(row1)[warp - 2] = d;
+        }
       }
       ptx::named_barrier(1, 256);
+      if (DIFF && threadIdx.x == 64) {
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d += reinterpret_cast<const float *>(row1)[i];
+        P.dr[blockIdx.x] = d;  // [map][window][query tile]
+      }
       if (threadIdx.x == 64 && ok && !*reinterpret_cast<volatile int *>(&c.abort)) {
         store_window_tile(P.plan, P.g, P.map_dq, row_tile, row_org, bh, row0);
         ptx::tma_store_commit();
@@ -501,129 +758,172 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
       const uint32_t tS = tmem + lane_off + col, tDP = tmem + lane_off + 128 + col;
       float *wrec = reinterpret_cast<float *>(smem + L::col_rec) + (warp - 2) * 128;  // [-L log2 e x 64 | -D x 64]
       const float4 *nl4 = reinterpret_cast<const float4 *>(wrec), *nd4 = reinterpret_cast<const float4 *>(wrec + 64);
-      QIter it;
-      if (n_cols > 0) q_first(P, list, MODE, MODE == kDkvLong ? chunk * P.chunk_tiles : 0, it);
-      for (int j = 0; ok && j < n_cols; ++j) {
-        ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.s_full[0], j & 1));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        float p[64];
-        tmem_ld64f(tS, p);
-        {
-          // This warp's 64 query records {-L log2 e, -D, 0, 0}, one load per lane
-          // for two columns, rewritten as two arrays that the loops below read four
-          // values at a time.
-          const float4 *r = reinterpret_cast<const float4 *>(smem + L::rec + (j & 1) * kRecBytes) + col;
-          const float4 a = r[lane], b = r[32 + lane];
-          __syncwarp();  // every lane has read the previous tile's arrays
-          wrec[lane] = a.x;
-          wrec[32 + lane] = b.x;
-          wrec[64 + lane] = a.y;
-          wrec[96 + lane] = b.y;
-          __syncwarp();
-        }
-        uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
-        if (!P.all_full) {
-          const PlanTile &qt = q_tile(P, it);
-          m0 = qt.mask[2 * g];
-          m1 = qt.mask[2 * g + 1];
-        }
-        const uint64_t sl2x2 = ptx::f2_pack(sl2, sl2);
+      // Differential form: this row's token (-1: none) and its patch, kept for the two
+      // epilogues in shared memory (registers are full) while the first scores are on their way.
+      int2 *place = reinterpret_cast<int2 *>(smem + L::place) + (threadIdx.x - 64);
+      auto row_place = [&] {
+        int t, y, x;
+        if (!tile_row_token(P.plan, P.g, row_tile, row_org, row, &t, &y, &x)) return make_int2(-1, 0);
+        return make_int2((t * P.g.H + y) * P.g.W + x,
+                         ((t / P.pt) * (P.g.H / P.ph) + y / P.ph) * (P.g.W / P.pw) + x / P.pw);
+      };
+      if (DIFF && MODE == kDkvWindow) *place = row_place();
+      // unrolled: the two maps' epilogues differ (a rolled loop spills over 800 bytes a thread)
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 nl = nl4[i / 4];
-          float x0, x1, x2, x3;
-          ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(p[i], p[i + 1]), sl2x2, ptx::f2_pack(nl.x, nl.y)), x0, x1);
-          ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(p[i + 2], p[i + 3]), sl2x2, ptx::f2_pack(nl.z, nl.w)), x2, x3);
-          p[i] = ptx::ex2(x0);
-          p[i + 1] = ptx::ex2(x1);
-          p[i + 2] = ptx::ex2(x2);
-          p[i + 3] = ptx::ex2(x3);
-        }
-        const bool partial = (m0 & m1) != 0xFFFFFFFFu;  // warp-uniform: a partial query tile
-        if (partial) zero_masked(p, m0, m1);
-        uint32_t pk[32];
-        pack64(p, pk);
-        ptx::tmem_st32(tS, pk);  // P^T (bf16) over the first half of this thread's S^T columns
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&c.p_full[g]);
-        ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.dp_full[0], j & 1));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        float dp[64];
-        tmem_ld64f(tDP, dp);
+      for (int m = 0; m < kMaps; ++m) {
+        QIter it;
+        if (n_cols > 0) q_first(P, list, MODE, MODE == kDkvLong ? chunk * P.chunk_tiles : 0, it);
+        for (int j = m * n_cols; ok && j < (m + 1) * n_cols; ++j) {
+          ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.s_full[0], j & 1));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          float p[64];
+          tmem_ld64f(tS, p);
+          {
+            // This warp's 64 query records {-L log2 e, -D, 0, 0}, one load per lane
+            // for two columns, rewritten as two arrays that the loops below read four
+            // values at a time.
+            const float4 *r = reinterpret_cast<const float4 *>(smem + L::rec + (j & 1) * kRecBytes) + col;
+            const float4 a = r[lane], b = r[32 + lane];
+            __syncwarp();  // every lane has read the previous tile's arrays
+            wrec[lane] = a.x;
+            wrec[32 + lane] = b.x;
+            wrec[64 + lane] = a.y;
+            wrec[96 + lane] = b.y;
+            __syncwarp();
+          }
+          uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
+          if (!P.all_full) {
+            const PlanTile &qt = q_tile(P, it);
+            m0 = qt.mask[2 * g];
+            m1 = qt.mask[2 * g + 1];
+          }
+          const uint64_t sl2x2 = ptx::f2_pack(sl2, sl2);
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 nd = nd4[i / 4];
-          float d0, d1, d2, d3;
-          ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(p[i], p[i + 1]),
-                                    ptx::fadd2(ptx::f2_pack(dp[i], dp[i + 1]), ptx::f2_pack(nd.x, nd.y))),
-                         d0, d1);
-          ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(p[i + 2], p[i + 3]),
-                                    ptx::fadd2(ptx::f2_pack(dp[i + 2], dp[i + 3]), ptx::f2_pack(nd.z, nd.w))),
-                         d2, d3);
-          dp[i] = d0;
-          dp[i + 1] = d1;
-          dp[i + 2] = d2;
-          dp[i + 3] = d3;
+          for (int i = 0; i < 64; i += 4) {
+            const float4 nl = nl4[i / 4];
+            float x0, x1, x2, x3;
+            ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(p[i], p[i + 1]), sl2x2, ptx::f2_pack(nl.x, nl.y)), x0, x1);
+            ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(p[i + 2], p[i + 3]), sl2x2, ptx::f2_pack(nl.z, nl.w)), x2, x3);
+            p[i] = ptx::ex2(x0);
+            p[i + 1] = ptx::ex2(x1);
+            p[i + 2] = ptx::ex2(x2);
+            p[i + 3] = ptx::ex2(x3);
+          }
+          const bool partial = (m0 & m1) != 0xFFFFFFFFu;  // warp-uniform: a partial query tile
+          if (partial) zero_masked(p, m0, m1);
+          uint32_t pk[32];
+          pack64(p, pk);
+          ptx::tmem_st32(tS, pk);  // P^T (bf16) over the first half of this thread's S^T columns
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&c.p_full[g]);
+          ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.dp_full[0], j & 1));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          float dp[64];
+          tmem_ld64f(tDP, dp);
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const float4 nd = nd4[i / 4];
+            float d0, d1, d2, d3;
+            ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(p[i], p[i + 1]),
+                                      ptx::fadd2(ptx::f2_pack(dp[i], dp[i + 1]), ptx::f2_pack(nd.x, nd.y))),
+                           d0, d1);
+            ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(p[i + 2], p[i + 3]),
+                                      ptx::fadd2(ptx::f2_pack(dp[i + 2], dp[i + 3]), ptx::f2_pack(nd.z, nd.w))),
+                           d2, d3);
+            dp[i] = d0;
+            dp[i + 1] = d1;
+            dp[i + 2] = d2;
+            dp[i + 3] = d3;
+          }
+          if (partial) zero_masked(dp, m0, m1);  // dS = 0 there whatever dP holds
+          pack64(dp, pk);
+          ptx::tmem_st32(tDP, pk);  // dS^T (bf16) over the first half of this thread's dP^T columns
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&c.ds_full[g]);
+          q_next(P, list, MODE, n_windows, it);
         }
-        if (partial) zero_masked(dp, m0, m1);  // dS = 0 there whatever dP holds
-        pack64(dp, pk);
-        ptx::tmem_st32(tDP, pk);  // dS^T (bf16) over the first half of this thread's dP^T columns
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&c.ds_full[g]);
-        q_next(P, list, MODE, n_windows, it);
-      }
-      if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.acc_full, 0));
-      if (ok) {
+        if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.acc_full, n_cols > 0 ? m : 0));
+        if (!ok) continue;
+        if (DIFF && MODE == kDkvWindow) ptx::grid_wait();  // the pooled keys' gradients
         ptx::tc_fence_after();
+        const bool last_map = m + 1 == kMaps;
+        const int unit = map_unit(m);  // of k and dk
+        if (!last_map) {  // map 2's part of dV, before map 1 adds to it
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            ptx::tmem_ld32(tmem + lane_off + 256 + col + 32 * h, r);
+            ptx::tmem_ld_wait(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * neg_lambda);
+            ptx::tmem_st32(tmem + lane_off + 256 + col + 32 * h, r);
+          }
+        }
         float dv[64], dk[64];
         if (n_cols > 0) {
-          tmem_ld64f(tmem + lane_off + 256 + col, dv);
           tmem_ld64f(tmem + lane_off + 384 + col, dk);
+          if (last_map) tmem_ld64f(tmem + lane_off + 256 + col, dv);
         } else {
 #pragma unroll
           for (int i = 0; i < 64; ++i) dv[i] = dk[i] = 0.f;
         }
+        const float dk_scale = last_map ? P.scale : P.scale * neg_lambda;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) dk[i] *= P.scale;
+        for (int i = 0; i < 64; ++i) dk[i] *= dk_scale;
+        if (!last_map) {
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+        }
         if (MODE == kDkvLong) {
-          // partial sums of this chunk, float32 [dK | dV][row][128]
-          float *dst = P.part + ((((long long)bh * P.n_long_tiles + kt) * P.n_chunks + chunk) * 2) * (kTileRows * 128);
-          float4 *pk4 = reinterpret_cast<float4 *>(dst + row * 128 + col);
-          float4 *pv4 = reinterpret_cast<float4 *>(dst + kTileRows * 128 + row * 128 + col);
+          // partial sums of this chunk, float32 [dK of each map | dV][row][128]
+          float *dst = P.part + ((((long long)bh * P.n_long_tiles + kt) * P.n_chunks + chunk) * (kMaps + 1)) * (kTileRows * 128) +
+                       row * 128 + col;
+          float4 *pk4 = reinterpret_cast<float4 *>(dst + (kMaps - 1 - m) * (kTileRows * 128));
+          float4 *pv4 = reinterpret_cast<float4 *>(dst + kMaps * (kTileRows * 128));
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             pk4[i] = make_float4(dk[4 * i], dk[4 * i + 1], dk[4 * i + 2], dk[4 * i + 3]);
-            pv4[i] = make_float4(dv[4 * i], dv[4 * i + 1], dv[4 * i + 2], dv[4 * i + 3]);
+            if (last_map) pv4[i] = make_float4(dv[4 * i], dv[4 * i + 1], dv[4 * i + 2], dv[4 * i + 3]);
           }
         } else {
-          int t, y, x;
-          if (P.n_pool > 0 && tile_row_token(P.plan, P.g, row_tile, row_org, row, &t, &y, &x)) {
+          int2 at = make_int2(-1, 0);
+          if (DIFF) at = *place;
+          else if (P.n_pool > 0) at = row_place();
+          if (P.n_pool > 0 && at.x >= 0) {
             // the pooled keys' gradient of this token's patch, spread evenly
-            const int pidx = ((t / P.pt) * (P.g.H / P.ph) + y / P.ph) * (P.g.W / P.pw) + x / P.pw;
-            const float4 *gk = reinterpret_cast<const float4 *>(P.dkvp + ((long long)bh * P.n_pool + pidx) * 128 + col);
+            const float4 *gk = reinterpret_cast<const float4 *>(P.dkvp + ((long long)unit * P.n_pool + at.y) * 128 + col);
             const float4 *gv = reinterpret_cast<const float4 *>(
-                P.dkvp + ((long long)(P.bh_count + bh) * P.n_pool + pidx) * 128 + col);
+                P.dkvp + (((long long)kMaps * P.bh_count + bh) * P.n_pool + at.y) * 128 + col);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float4 a = gk[i], b = gv[i];
+              const float4 a = gk[i];
               dk[4 * i] += a.x * P.inv_patch; dk[4 * i + 1] += a.y * P.inv_patch;
               dk[4 * i + 2] += a.z * P.inv_patch; dk[4 * i + 3] += a.w * P.inv_patch;
-              dv[4 * i] += b.x * P.inv_patch; dv[4 * i + 1] += b.y * P.inv_patch;
-              dv[4 * i + 2] += b.z * P.inv_patch; dv[4 * i + 3] += b.w * P.inv_patch;
+              if (last_map) {
+                const float4 b = gv[i];
+                dv[4 * i] += b.x * P.inv_patch; dv[4 * i + 1] += b.y * P.inv_patch;
+                dv[4 * i + 2] += b.z * P.inv_patch; dv[4 * i + 3] += b.w * P.inv_patch;
+              }
             }
           }
-          stage_row_half(row0, row, g, dk);  // the k and v tiles are no longer read
-          stage_row_half(row1, row, g, dv);
-          ptx::fence_proxy_async_smem();
+          if (last_map) {
+            stage_row_half(row0, row, g, dk);  // the k and v tiles are no longer read
+            stage_row_half(row1, row, g, dv);
+            ptx::fence_proxy_async_smem();
+          } else {
+            // the key tile's place in shared memory is map 1's already
+            store_rows64(P.dk + (long long)unit * (P.g.N + P.n_text) * 128 + col,
+                         *reinterpret_cast<volatile int *>(&c.abort) ? -1 : at.x, dk, lane);
+          }
         }
       }
       ptx::named_barrier(1, 256);
       if (MODE == kDkvWindow && threadIdx.x == 64 && ok && !*reinterpret_cast<volatile int *>(&c.abort)) {
-        store_window_tile(P.plan, P.g, P.map_dk, row_tile, row_org, bh, row0);
+        store_window_tile(P.plan, P.g, P.map_dk, row_tile, row_org, map_unit(kMaps - 1), row0);
         store_window_tile(P.plan, P.g, P.map_dv, row_tile, row_org, bh, row1);
         ptx::tma_store_commit();
         ptx::tma_store_wait_read_all();
@@ -637,6 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
+  if (last_to_end) ptx::grid_wait();
 }
 
 // Per query token: {-L log2(e), -(dout . out), 0, 0}, two tokens per warp (16 lanes x
@@ -699,6 +1000,11 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(const float *part, floa
 }
 
 // ----------------------------------------------------------------- host side
+struct BwdLayout {
+  size_t rec, part, dkvp, total;  // of `maps` maps for each unit of v
+  int n_long, n_chunks, chunk_tiles, q_tiles;
+};
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Query tiles per head: the sum over windows of their type's tile count.
@@ -720,8 +1026,6 @@ int head_query_tiles(const basa_params &p, const WindowPlan &plan) {
 // the chunk sums (hence the bits of the results) are the same on every device.
 constexpr long long kLongSms = 148;
 constexpr double kLongCtaCostTiles = 3.5;
-}  // namespace
-
 BwdLayout bwd_layout(const basa_params &p, const WindowPlan &plan, int maps) {
   BwdLayout L{};
   const long long bh = (long long)p.B * p.heads;
@@ -752,19 +1056,28 @@ BwdLayout bwd_layout(const basa_params &p, const WindowPlan &plan, int maps) {
   return L;
 }
 
-namespace {
-template <int MODE>
-basa_status run_bwd(const BwdParams &P, long long blocks, cudaStream_t s) {
+template <int MODE, bool DIFF>
+basa_status run_bwd(const BwdParams &P, long long blocks, cudaStream_t s, bool early = false) {
   if (blocks <= 0) return BASA_OK;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(attn_bwd_bf16_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<MODE>::bytes) !=
-      cudaSuccess)
+  if (cudaFuncSetAttribute(attn_bwd_bf16_kernel<MODE, DIFF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Smem<MODE>::bytes) != cudaSuccess)
     return BASA_ERR_CUDA;
-  attn_bwd_bf16_kernel<MODE><<<unsigned(blocks), kThreads, Smem<MODE>::bytes, s>>>(P);
-  return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<MODE>::bytes;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_bwd_bf16_kernel<MODE, DIFF>, P) == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
 }
-}  // namespace
 
+// Parameters of a backward over p.heads units of v with `maps` maps each; the
+// workspace starts with a BwdLayout (records, partial sums, pooled gradients).
 basa_status bwd_params(BwdParams &P, BwdLayout &L, const void *q, const void *k, const void *v, const void *kp,
                        const void *vp, const int32_t *route_idx, const void *dout, void *dq, void *dk, void *dv,
                        void *workspace, const basa_params &p, int maps) {
@@ -821,14 +1134,27 @@ basa_status bwd_params(BwdParams &P, BwdLayout &L, const void *q, const void *k,
   return BASA_OK;
 }
 
-basa_status launch_bwd_reduce(const BwdParams &P, const BwdLayout &L, void *dk, void *dv, const basa_params &p, int maps,
-                              cudaStream_t s) {
-  const long long threads = (long long)P.bh_count * L.n_long * kTileRows * 32;
-  bwd_reduce_kernel<<<dim3(unsigned((threads + 255) / 256), unsigned(maps + 1)), 256, 0, s>>>(
-      P.part, const_cast<float *>(P.dkvp), static_cast<__nv_bfloat16 *>(dk), static_cast<__nv_bfloat16 *>(dv), P.bh_count,
-      maps, L.n_long, L.n_chunks, P.n_pool, P.n_pool_tiles, p.n_text, P.g.N);
-  return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
+// The passes after the records: dq, pooled and text dK/dV, their chunks' sums, window dK/dV.
+// In the differential form `early` launches start under the one before them, see above.
+template <bool DIFF>
+basa_status run_passes(const BwdParams &P, const BwdLayout &L, void *dk, void *dv, const basa_params &p, cudaStream_t s) {
+  constexpr int maps = DIFF ? 2 : 1;
+  const long long bh = P.bh_count, window_blocks = bh * P.g.nWin * P.max_tiles;
+  basa_status st = DIFF ? BASA_OK : run_bwd<kDq, DIFF>(P, window_blocks, s);
+  if (st != BASA_OK) return st;
+  if (L.n_long > 0 && (st = run_bwd<kDkvLong, DIFF>(P, bh * L.n_long * L.n_chunks, s)) != BASA_OK) return st;
+  if (DIFF && (st = run_bwd<kDq, DIFF>(P, maps * window_blocks, s, L.n_long > 0)) != BASA_OK) return st;
+  if (L.n_long > 0) {
+    const long long threads = bh * L.n_long * kTileRows * 32;
+    bwd_reduce_kernel<<<dim3(unsigned((threads + 255) / 256), maps + 1), 256, 0, s>>>(
+        P.part, const_cast<float *>(P.dkvp), static_cast<__nv_bfloat16 *>(dk), static_cast<__nv_bfloat16 *>(dv), int(bh),
+        maps, L.n_long, L.n_chunks, P.n_pool, P.n_pool_tiles, p.n_text, P.g.N);
+    if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
+  }
+  return run_bwd<kDkvWindow, DIFF>(P, window_blocks, s, DIFF && L.n_long > 0);
 }
+
+}  // namespace
 
 size_t attn_bwd_bf16_workspace(const basa_params &p) {
   static thread_local WindowPlan plan;  // large: kept off the stack
@@ -843,18 +1169,51 @@ basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, co
   BwdLayout L;
   basa_status st = bwd_params(P, L, q, k, v, kp, vp, route_idx, dout, dq, dk, dv, workspace, p, 1);
   if (st != BASA_OK) return st;
-  const long long bh = P.bh_count, rows = bh * P.g.N;
+  const long long rows = (long long)P.bh_count * P.g.N;
   bwd_records_kernel<<<unsigned((rows + 15) / 16), 256, 0, s>>>(
       static_cast<const __nv_bfloat16 *>(out), static_cast<const __nv_bfloat16 *>(dout), lse,
       static_cast<float4 *>(workspace), rows);
   if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
-  const long long window_blocks = bh * P.g.nWin * P.max_tiles;
-  if ((st = run_bwd<kDq>(P, window_blocks, s)) != BASA_OK) return st;
-  if (L.n_long > 0) {
-    if ((st = run_bwd<kDkvLong>(P, bh * L.n_long * L.n_chunks, s)) != BASA_OK) return st;
-    if ((st = launch_bwd_reduce(P, L, dk, dv, p, 1, s)) != BASA_OK) return st;
-  }
-  return run_bwd<kDkvWindow>(P, window_blocks, s);
+  return run_passes<false>(P, L, dk, dv, p, s);
+}
+
+// Differential form: the layout of two maps, then g (with a norm), then the partial sums
+// of dlambda and dweight, then the dq pass's.
+size_t dr_count(const basa_params &p, const WindowPlan &plan) {
+  int tiles = 0;
+  for (int t = 0; t < 8; ++t) tiles = std::max<int>(tiles, plan.type[t].n_tiles);
+  return 2 * size_t(p.B) * p.heads * make_geo(p).nWin * tiles;
+}
+
+size_t diff_attn_bwd_bf16_workspace(bool norm, const basa_params &p) {
+  static thread_local WindowPlan plan;
+  if (build_window_plan(p, &plan) != BASA_OK) return 0;
+  const size_t g = norm ? align256(size_t(p.B) * p.heads * p.T * p.H * p.W * p.head_dim * 2) : 0;
+  return bwd_layout(p, plan, 2).total + g + align256(diff_prep_workspace(p)) + align256(dr_count(p, plan) * sizeof(float));
+}
+
+basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
+                                      const int32_t *route_idx, const basa_diff_params &dp, const void *pre,
+                                      const void *second, const float *lse, const void *dout, void *dq, void *dk,
+                                      void *dv, void *dlambda, void *dweight, void *workspace, const basa_params &p,
+                                      cudaStream_t s) {
+  static thread_local BwdParams P;
+  static thread_local WindowPlan plan;
+  basa_status st = build_window_plan(p, &plan);
+  if (st != BASA_OK) return st;
+  uint8_t *ws = static_cast<uint8_t *>(workspace), *g = ws + bwd_layout(p, plan, 2).total, *part = g;
+  if (dp.weight) part += align256(size_t(p.B) * p.heads * p.T * p.H * p.W * p.head_dim * 2);
+  const void *grad = dp.weight ? g : dout;
+  BwdLayout L;
+  if ((st = bwd_params(P, L, q, k, v, kp, vp, route_idx, grad, dq, dk, dv, ws, p, 2)) != BASA_OK) return st;
+  P.lambda = static_cast<const __nv_bfloat16 *>(dp.lambda);
+  P.heads = p.heads;
+  P.dk = static_cast<__nv_bfloat16 *>(dk);
+  P.dr = reinterpret_cast<float *>(part + align256(diff_prep_workspace(p)));
+  float *sums = reinterpret_cast<float *>(part);
+  st = launch_diff_prep(pre, second, lse, dout, dp, g, reinterpret_cast<float4 *>(ws), nullptr, sums, p, s);
+  if (st != BASA_OK || (st = run_passes<true>(P, L, dk, dv, p, s)) != BASA_OK) return st;
+  return launch_diff_sums(sums, P.dr, 2 * P.g.nWin * P.max_tiles, dp, dlambda, dweight, p, s);
 }
 
 }  // namespace basa

@@ -26,7 +26,7 @@
 //               of plan lookups that the softmax warps, which bound a step, are spared);
 //               warp 2 also zeroes the rows of the V tiles that no load writes: P is 0 there,
 //               but what an earlier item left may be infinite or NaN. (The loader doing it
-//               cost 20%: it is within two steps of being late.)
+//               cost 20%, doing it for every tile 4%.)
 //   warps 4-11  softmax group g for map g, a thread per query row; then group g finishes
 //               columns [64 g, 64 g + 64) of the output rows
 #include <cudaTypedefs.h>
@@ -99,7 +99,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
     c.abort = 0;
     ptx::fence_mbar_init();
   }
-  if (warp >= 4) touch_plan(P.plan, warp - 4, 8);
+  if (pads) {
+    uint4 *z = reinterpret_cast<uint4 *>(smem + kSmemRing);
+    for (uint32_t i = threadIdx.x; i < kStages * kTileBytes / 16; i += kThreads) z[i] = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async_smem();
+  }
   if (warp == 1) {
     ptx::tmem_alloc(&c.tmem_base, kTmemCols);
     ptx::tmem_relinquish();
@@ -139,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
           load_window_tile(P.plan, P.g, P.map_q, qt, it.keys.org[0], 2 * bh + g, smem + kSmemQ + g * kTileBytes,
                            &c.q_full);
         ++n;
+        const int item_no = n - 1;
         KeyIter key = first_key(P, it.keys);
         for (int j = 0; ok && j < n_kt; ++j) {
           for (int kv = 0; kv < 3; ++kv, ++ring) {
@@ -149,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
               continue;
             }
             ptx::mbar_arrive_expect_tx(&c.full[slot], key_tile_bytes(P, it.keys, key));
-            if (pads && kv < 2) ptx::mbar_arrive(&c.full[slot]);  // V tiles: warp 2
+            // the second arrival: warp 2's where it zeroes rows, see there
+            if (pads && !(kv == 2 && item_no > 0 && j < kStages)) ptx::mbar_arrive(&c.full[slot]);
             load_key_tile(P, it.keys, key, kv == 2, kv == 2 ? bh : 2 * bh + kv, smem + kSmemRing + slot * kTileBytes,
                           &c.full[slot]);
           }
@@ -245,23 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
       if (lane == 0) ptx::mbar_arrive(&c.mask_full[n & 1]);
       const int n_kt = it.n_kt;
       bool ok = true;
-      KeyIter key{0, 0};  // past the table only
-      for (int j = 0; ok && pads && j < n_kt; ++j) {
-        const int ring = 3 * (step + j) + 2, slot = ring % kStages;  // V_j
+      // V_0 .. V_4 take each ring slot once: after them a slot's unwritten rows hold zeros or
+      // rows of this item. (The first item finds the ring zeroed.)
+      for (int j = 0; ok && pads && n > 0 && j < min(n_kt, kStages); ++j) {
+        const int ring = 3 * (step + j) + 2, slot = ring % kStages;
         ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.empty[slot], ((ring / kStages) & 1) ^ 1));
         if (!ok) break;
-        uint32_t mk[4];
-        if (j < kMaskTable) {
-          const uint4 t = reinterpret_cast<const uint4 *>(smem + kSmemMask)[(n & 1) * kMaskTable + j];
-          mk[0] = t.x; mk[1] = t.y; mk[2] = t.z; mk[3] = t.w;
-        } else {
-          if (j == kMaskTable) {
-            key = first_key(P, it.keys);
-            for (int t = 0; t < kMaskTable; ++t) advance(P, it.keys, key);
-          }
-          key_tile_mask(P, it.keys, key, mk);
-          advance(P, it.keys, key);
-        }
+        const uint4 t = reinterpret_cast<const uint4 *>(smem + kSmemMask)[(n & 1) * kMaskTable + j];
+        const uint32_t mk[4] = {t.x, t.y, t.z, t.w};
         // pooled and text tiles are written whole; rows past their end read as zero
         zero_unwritten_rows(smem + kSmemRing + slot * kTileBytes, mk, lane);
         if (lane == 0) ptx::mbar_arrive(&c.full[slot]);

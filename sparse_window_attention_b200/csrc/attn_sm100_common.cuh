@@ -190,13 +190,6 @@ __device__ __forceinline__ void store_rows64(__nv_bfloat16 *base, int row, const
   }
 }
 
-// Reads the part of the plan that the launch uses, a few entries a warp, so that its first
-// reads (kernel parameters: a miss each) do not queue up behind one another.
-__device__ __forceinline__ void touch_plan(const WindowPlan &plan, int warp, int warps) {
-  for (int i = 2 * warp; i < plan.n_tiles; i += 2 * warps) asm volatile("" ::"r"(int(plan.tile[i].valid_rows)));
-  for (int i = 8 * warp; i < plan.n_pieces; i += 8 * warps) asm volatile("" ::"r"(int(plan.piece[i].dest)));
-}
-
 // Token (original grid coordinates) held by row `row` of a window tile; false for
 // a padding row.
 __device__ __forceinline__ bool tile_row_token(const WindowPlan &plan, const Geo &g, const PlanTile &tile,

@@ -183,7 +183,7 @@ basa_status launch_diff_combine(int n_splits, const float *part, const float *pa
 size_t diff_prep_workspace(const basa_params &p);
 basa_status launch_diff_prep(const void *pre, const void *second, const float *lse, const void *dout,
                              const basa_diff_params &dp, void *g, float4 *rec, float *drow, float *part,
-                             int *counter, const basa_params &p, cudaStream_t s);
+                             const basa_params &p, cudaStream_t s);
 basa_status launch_diff_sums(const float *part, const float *dr, int dr_per_unit, const basa_diff_params &dp,
                              void *dlambda, void *dweight, const basa_params &p, cudaStream_t s);
 size_t diff_attn_bwd_bf16_workspace(bool norm, const basa_params &p);

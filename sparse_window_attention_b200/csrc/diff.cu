@@ -143,10 +143,8 @@ struct PrepArgs {
   const void *pre, *second, *dout, *lambda, *weight;
   const float *lse;  // [units][2][rows]
   void *g;           // [units][rows][d]; unused without weight (g = dout)
-  float4 *rec;       // nullable: records {-L log2 e, -D, weight of dR in -dlambda, the row itself (an
-                     // int's bits)} [units][2][rows]
+  float4 *rec;       // nullable: records {-L log2 e, -D, weight of dR in -dlambda, 0} [units][2][rows]
   float *drow;       // nullable: D alone, [units][2][rows]
-  int *counter;      // nullable: set to 0
   float *part;       // [blocks][1 + d]: sum g . O2, then the weight's gradient
   int heads, blocks_per_unit;
   long long rows;
@@ -157,7 +155,6 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kDiffThreads) diff_prep_kernel(const __grid_constant__ PrepArgs a) {
   constexpr int LPR = D / 8, ROWS = kDiffThreads / LPR;
   __shared__ float red[kDiffThreads / 32][D + 1];
-  if (a.counter != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
   const long long unit = blockIdx.x / a.blocks_per_unit;
   const long long r0 = (long long)(blockIdx.x % a.blocks_per_unit) * kPrepRows;
   const long long r1 = min(a.rows, r0 + kPrepRows);
@@ -225,8 +222,7 @@ __global__ void __launch_bounds__(kDiffThreads) diff_prep_kernel(const __grid_co
     if (valid && c < 2) {
       const long long m = (2 * unit + c) * a.rows + r;
       const float d = c == 0 ? fmaf(lam, d2, da) : d2;
-      if (a.rec) a.rec[m] = make_float4(-a.lse[m] * 1.4426950408889634f, -d, c == 0 ? -c2 : fmaf(c2, lam, 1.f),
-                                       __int_as_float(int(r)));
+      if (a.rec) a.rec[m] = make_float4(-a.lse[m] * 1.4426950408889634f, -d, c == 0 ? -c2 : fmaf(c2, lam, 1.f), 0.f);
       if (a.drow) a.drow[m] = d;
     }
   }
@@ -333,7 +329,7 @@ size_t diff_prep_workspace(const basa_params &p) {
 
 basa_status launch_diff_prep(const void *pre, const void *second, const float *lse, const void *dout,
                              const basa_diff_params &dp, void *g, float4 *rec, float *drow, float *part,
-                             int *counter, const basa_params &p, cudaStream_t s) {
+                             const basa_params &p, cudaStream_t s) {
   PrepArgs a{};
   a.pre = pre;
   a.second = second;
@@ -345,7 +341,6 @@ basa_status launch_diff_prep(const void *pre, const void *second, const float *l
   a.rec = rec;
   a.drow = drow;
   a.part = part;
-  a.counter = counter;
   a.heads = p.heads;
   a.rows = (long long)p.T * p.H * p.W;
   a.gain = dp.gain;
