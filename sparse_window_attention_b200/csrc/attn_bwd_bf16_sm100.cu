@@ -1135,9 +1135,11 @@ basa_status bwd_params(BwdParams &P, BwdLayout &L, const void *q, const void *k,
 }
 
 // The passes after the records: dq, pooled and text dK/dV, their chunks' sums, window dK/dV.
-// In the differential form `early` launches start under the one before them, see above.
-template <bool DIFF>
-basa_status run_passes(const BwdParams &P, const BwdLayout &L, void *dk, void *dv, const basa_params &p, cudaStream_t s) {
+// In the differential form `early` launches start under the one before them, see above;
+// `sums` is launched before the window pass, which waits for it and for what it waits for.
+template <bool DIFF, typename F>
+basa_status run_passes(const BwdParams &P, const BwdLayout &L, void *dk, void *dv, const basa_params &p, cudaStream_t s,
+                       F &&sums) {
   constexpr int maps = DIFF ? 2 : 1;
   const long long bh = P.bh_count, window_blocks = bh * P.g.nWin * P.max_tiles;
   basa_status st = DIFF ? BASA_OK : run_bwd<kDq, DIFF>(P, window_blocks, s);
@@ -1151,7 +1153,8 @@ basa_status run_passes(const BwdParams &P, const BwdLayout &L, void *dk, void *d
         maps, L.n_long, L.n_chunks, P.n_pool, P.n_pool_tiles, p.n_text, P.g.N);
     if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
   }
-  return run_bwd<kDkvWindow, DIFF>(P, window_blocks, s, DIFF && L.n_long > 0);
+  if ((st = sums()) != BASA_OK) return st;
+  return run_bwd<kDkvWindow, DIFF>(P, window_blocks, s, DIFF);
 }
 
 }  // namespace
@@ -1174,7 +1177,7 @@ basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, co
       static_cast<const __nv_bfloat16 *>(out), static_cast<const __nv_bfloat16 *>(dout), lse,
       static_cast<float4 *>(workspace), rows);
   if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
-  return run_passes<false>(P, L, dk, dv, p, s);
+  return run_passes<false>(P, L, dk, dv, p, s, [] { return BASA_OK; });
 }
 
 // Differential form: the layout of two maps, then g (with a norm), then the partial sums
@@ -1212,8 +1215,10 @@ basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *
   P.dr = reinterpret_cast<float *>(part + align256(diff_prep_workspace(p)));
   float *sums = reinterpret_cast<float *>(part);
   st = launch_diff_prep(pre, second, lse, dout, dp, g, reinterpret_cast<float4 *>(ws), nullptr, sums, p, s);
-  if (st != BASA_OK || (st = run_passes<true>(P, L, dk, dv, p, s)) != BASA_OK) return st;
-  return launch_diff_sums(sums, P.dr, 2 * P.g.nWin * P.max_tiles, dp, dlambda, dweight, p, s);
+  if (st != BASA_OK) return st;
+  return run_passes<true>(P, L, dk, dv, p, s, [&] {
+    return launch_diff_sums(sums, P.dr, 2 * P.g.nWin * P.max_tiles, dp, dlambda, dweight, L.n_long > 0, p, s);
+  });
 }
 
 }  // namespace basa
