@@ -25,8 +25,9 @@
 // the window, pooled or text segments from the key stream, and an optional
 // epilogue writes each query row's log-sum-exp; and the text-query rows, where the
 // queries are 128-row boxes of the text rows and the key stream is every k/v row,
-// split over CTA groups whose partial results are merged by log-sum-exp. With PART the
-// text rows' (partial) outputs leave in float32, for a difference of maps taken afterwards.
+// split over CTA groups whose partial results are merged by log-sum-exp. With PART two
+// maps share their values and the text rows' (partial) outputs leave in float32, for a
+// difference of the maps taken afterwards.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -108,13 +109,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
     }
     ptx::mbar_init(&c.drain, 1);
     c.abort = 0;
-    if (P.dense) {
-      c.keys.tile0 = split * P.split_tiles;
-      c.keys.ntile = min(P.split_tiles, (P.dense_rows + kTileRows - 1) / kTileRows - c.keys.tile0);
-      c.keys.wtype[0] = 0;
-    } else {
-      fill_windows(P, c.keys, bh, w);
-    }
+    c.keys.tile0 = P.dense ? split * P.split_tiles : 0;
+    c.keys.ntile = P.dense ? min(P.split_tiles, (P.dense_rows + kTileRows - 1) / kTileRows - c.keys.tile0) : 0;
+    c.keys.wtype[0] = wtype;
+    c.keys.org[0][0] = ot; c.keys.org[0][1] = oy; c.keys.org[0][2] = ox;
+    fill_routes(P, c.keys, bh, w);
     ptx::fence_mbar_init();
   }
   if (P.plan.zero_fill) {
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bf16_kernel(const __grid_con
           // Arm the barrier with the byte count before issuing the copies.
           const uint32_t bytes = key_tile_bytes(P, c.keys, it);
           ptx::mbar_arrive_expect_tx(&c.full[slot], bytes);
-          load_key_tile(P, c.keys, it, kv == 1, kv == 1 ? bh >> P.v_shift : bh, dst, &c.full[slot]);
+          load_key_tile(P, c.keys, it, kv == 1, PART && kv == 1 ? bh >> 1 : bh, dst, &c.full[slot]);
           last = item;
         }
         if (!ok) break;
@@ -618,10 +617,10 @@ size_t text_attn_workspace(const basa_params &p, int sms) {
 }
 
 namespace {
-// Parameters of a text-query launch over p.heads maps, whose values v_shift maps share
-// in groups of 2^v_shift. The caller sets where the outputs go.
+// Parameters of a text-query launch over p.heads maps, of which `maps` share their values.
+// The caller sets where the outputs go.
 basa_status text_params(AttnParams &P, const void *q_text, const void *k, const void *v, const basa_params &p, int splits,
-                        int v_shift) {
+                        int maps) {
   if (!tensor_map_encoder()) return BASA_ERR_CUDA;
   std::memset(&P, 0, sizeof(P));
   P.g = make_geo(p);
@@ -629,8 +628,7 @@ basa_status text_params(AttnParams &P, const void *q_text, const void *k, const 
   const long long kv_rows = N + p.n_text;
   const int bh = p.B * p.heads;
   basa_params pv = p;
-  pv.heads = p.heads >> v_shift;
-  P.v_shift = v_shift;
+  pv.heads = p.heads / maps;
   if (!encode_rows_map(&P.map_kt, k, p, kv_rows) || !encode_rows_map(&P.map_vt, v, pv, kv_rows) ||
       !encode_rows_map(&P.map_qd, q_text, p, p.n_text))
     return BASA_ERR_CUDA;
@@ -661,7 +659,7 @@ basa_status launch_attn_text_bf16(const void *q_text, const void *k, const void 
   AttnParams P;
   const int bh = p.B * p.heads;
   const int splits = text_splits(p, sms);
-  basa_status st = text_params(P, q_text, k, v, p, splits, 0);
+  basa_status st = text_params(P, q_text, k, v, p, splits, 1);
   if (st != BASA_OK) return st;
   uint8_t *part = static_cast<uint8_t *>(workspace);
   float *part_lse = reinterpret_cast<float *>(part + size_t(splits) * bh * p.n_text * p.head_dim * 2);
@@ -701,7 +699,7 @@ basa_status launch_diff_text_bf16(const void *q_text, const void *k, const void 
   basa_params pm = p;
   pm.heads = 2 * p.heads;
   const int splits = text_splits(pm, sms);
-  basa_status st = text_params(P, q_text, k, v, pm, splits, 1);
+  basa_status st = text_params(P, q_text, k, v, pm, splits, 2);
   if (st != BASA_OK) return st;
   const size_t rows = size_t(splits) * pm.B * pm.heads * p.n_text;
   P.part = static_cast<float *>(workspace);

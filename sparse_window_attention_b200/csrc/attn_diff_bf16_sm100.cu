@@ -129,7 +129,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_diff_bf16_kernel(const __gri
         Item &it = c.item[n & 1];
         it.bh = bh;
         it.tile = P.plan.type[wtype].first_tile + tile;
-        fill_windows(P, it.keys, bh, w);
+        it.keys.tile0 = it.keys.ntile = 0;
+        it.keys.wtype[0] = wtype;
+        it.keys.org[0][0] = ot; it.keys.org[0][1] = oy; it.keys.org[0][2] = ox;
+        fill_routes(P, it.keys, bh, w);
         int n_kt = 0;
         for (int s = 0; s <= P.routed_k + 2; ++s) n_kt += seg_tiles(P, it.keys, s);
         it.n_kt = n_kt;

@@ -42,15 +42,14 @@ struct alignas(64) AttnParams {
   int text_row0;  // first k/v row of the text segment: N (window mode) or 0
   float *lse;       // nullable: log-sum-exp of each query row's scaled scores [B*heads][N]
   int all_full;  // every key tile of the launch is full: no column masks
-  int v_shift;   // v and vp belong to unit bh >> v_shift (two maps that share their values)
+  uint32_t flags;
+  unsigned long long timeout_ns;
   // differential form: a CTA's unit is a (batch, differential head); map g's q, k, kp are unit 2 * unit + g
   const __nv_bfloat16 *lambda, *norm_weight;  // [heads]; nullable [128]
   __nv_bfloat16 *out, *pre, *second;          // [B*heads][N][128]; pre and second nullable
   int heads, q_tiles, n_items;                // query tiles of a window (at most); work items
   float gain, eps;
   float *part;  // text rows that leave in float32: outputs [split][b*head][n_text][128]
-  uint32_t flags;
-  unsigned long long timeout_ns;
 };
 
 // __grid_constant__ kernel parameters are limited to 32764 bytes.
@@ -63,17 +62,18 @@ struct KeyList {
   int org[1 + kMaxRouted][3];
 };
 
-// Window w of the shifted grid and the windows routed to it (unit `bh` of the routes).
-__device__ __forceinline__ void fill_windows(const AttnParams &P, KeyList &c, int bh, int w) {
-  c.tile0 = c.ntile = 0;
-  window_origin(P.g, w, &c.org[0][0], &c.org[0][1], &c.org[0][2], &c.wtype[0]);
+// The windows routed to window w (unit `bh` of the routes).
+__device__ __forceinline__ void fill_routes(const AttnParams &P, KeyList &c, int bh, int w) {
   for (int r = 0; r < P.routed_k; ++r) {
     int u = P.route[((long long)bh * P.g.nWin + w) * P.routed_k + r];
     if (u < 0 || u >= P.g.nWin) {  // reported, and replaced by the own window: accesses stay in bounds
       if (P.dev_err) atomicOr(P.dev_err, BASA_DEVERR_BAD_ROUTE);
       u = w;
     }
-    window_origin(P.g, u, &c.org[1 + r][0], &c.org[1 + r][1], &c.org[1 + r][2], &c.wtype[1 + r]);
+    int a, b, d, t;
+    window_origin(P.g, u, &a, &b, &d, &t);
+    c.wtype[1 + r] = t;
+    c.org[1 + r][0] = a; c.org[1 + r][1] = b; c.org[1 + r][2] = d;
   }
 }
 
