@@ -963,17 +963,16 @@ __global__ void __launch_bounds__(256) bwd_records_kernel(const __nv_bfloat16 *o
 }
 
 // Sums the chunks of the long key tiles in order: pooled rows -> dkvp (float32),
-// text rows -> dk, dv (bf16, rows N.. of each b*head). `maps` dK arrays and one dV for
-// each unit of v; a thread sums one of them.
+// text rows -> dk, dv (bf16, rows N.. of each b*head). MAPS dK arrays and one dV for each
+// unit of v, all by one thread.
+template <int MAPS>
 __global__ void __launch_bounds__(256) bwd_reduce_kernel(const float *part, float *dkvp, __nv_bfloat16 *dk,
-                                                         __nv_bfloat16 *dv, int bh_count, int maps, int n_long,
-                                                         int n_chunks, int n_pool, int n_pool_tiles, int n_text,
-                                                         long long N) {
-  if (maps == 2) ptx::grid_launch_dependents();
+                                                         __nv_bfloat16 *dv, int bh_count, int n_long, int n_chunks,
+                                                         int n_pool, int n_pool_tiles, int n_text, long long N) {
+  if (MAPS == 2) ptx::grid_launch_dependents();
   const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;  // (bh, tile, row, 4-column group)
   const long long total = (long long)bh_count * n_long * kTileRows * 32;
   if (idx >= total) return;
-  const int which = blockIdx.y;  // dK of map `which`, or dV
   const int c4 = int(idx % 32);
   const int row = int((idx / 32) % kTileRows);
   const int tile = int((idx / (32 * kTileRows)) % n_long);
@@ -981,21 +980,29 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(const float *part, floa
   const bool pooled = tile < n_pool_tiles;
   const int r = (pooled ? tile : tile - n_pool_tiles) * kTileRows + row;
   if (r >= (pooled ? n_pool : n_text)) return;
-  const long long step = (long long)(maps + 1) * (kTileRows * 128);
-  const float *p = part + (((long long)bh * n_long + tile) * n_chunks) * step + which * (kTileRows * 128) + row * 128 + c4 * 4;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int ch = 0; ch < n_chunks; ++ch, p += step) {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+  float4 s[MAPS + 1];  // dK of each map, dV
+#pragma unroll
+  for (int a = 0; a <= MAPS; ++a) s[a] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float *base = part + (((long long)bh * n_long + tile) * n_chunks) * (MAPS + 1) * (kTileRows * 128);
+  for (int ch = 0; ch < n_chunks; ++ch) {
+    const float *p = base + (long long)ch * (MAPS + 1) * (kTileRows * 128) + row * 128 + c4 * 4;
+#pragma unroll
+    for (int a = 0; a <= MAPS; ++a) {
+      const float4 x = *reinterpret_cast<const float4 *>(p + a * kTileRows * 128);
+      s[a].x += x.x; s[a].y += x.y; s[a].z += x.z; s[a].w += x.w;
+    }
   }
-  const bool is_v = which == maps;
-  const long long unit = is_v ? bh : (long long)maps * bh + which;
-  if (pooled) {
-    const long long at = (is_v ? (long long)maps * bh_count : 0) + unit;
-    *reinterpret_cast<float4 *>(dkvp + (at * n_pool + r) * 128 + c4 * 4) = s;
-  } else {
-    const long long o = (unit * (N + n_text) + N + r) * 128 + c4 * 4;
-    reinterpret_cast<uint2 *>((is_v ? dv : dk) + o)[0] = make_uint2(ptx::pack_bf16x2(s.x, s.y), ptx::pack_bf16x2(s.z, s.w));
+#pragma unroll
+  for (int a = 0; a <= MAPS; ++a) {
+    const long long unit = a < MAPS ? (long long)MAPS * bh + a : bh;
+    if (pooled) {
+      const long long at = (a < MAPS ? 0 : (long long)MAPS * bh_count) + unit;
+      *reinterpret_cast<float4 *>(dkvp + (at * n_pool + r) * 128 + c4 * 4) = s[a];
+    } else {
+      const long long o = (unit * (N + n_text) + N + r) * 128 + c4 * 4;
+      reinterpret_cast<uint2 *>((a < MAPS ? dk : dv) + o)[0] =
+          make_uint2(ptx::pack_bf16x2(s[a].x, s[a].y), ptx::pack_bf16x2(s[a].z, s[a].w));
+    }
   }
 }
 
@@ -1148,9 +1155,9 @@ basa_status run_passes(const BwdParams &P, const BwdLayout &L, void *dk, void *d
   if (DIFF && (st = run_bwd<kDq, DIFF>(P, maps * window_blocks, s, L.n_long > 0)) != BASA_OK) return st;
   if (L.n_long > 0) {
     const long long threads = bh * L.n_long * kTileRows * 32;
-    bwd_reduce_kernel<<<dim3(unsigned((threads + 255) / 256), maps + 1), 256, 0, s>>>(
+    bwd_reduce_kernel<maps><<<unsigned((threads + 255) / 256), 256, 0, s>>>(
         P.part, const_cast<float *>(P.dkvp), static_cast<__nv_bfloat16 *>(dk), static_cast<__nv_bfloat16 *>(dv), int(bh),
-        maps, L.n_long, L.n_chunks, P.n_pool, P.n_pool_tiles, p.n_text, P.g.N);
+        L.n_long, L.n_chunks, P.n_pool, P.n_pool_tiles, p.n_text, P.g.N);
     if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
   }
   if ((st = sums()) != BASA_OK) return st;
