@@ -202,8 +202,10 @@ def _stream(stream):
     if stream is None:
         import torch
 
-        if torch.cuda.is_initialized():
-            return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
+        if torch.cuda.is_initialized():  # the handle alone: a Stream object costs more than a small launch's checks
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            device = torch.cuda.current_device()
+            return raw(device) if raw else torch.cuda.current_stream(device).cuda_stream
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     return stream if isinstance(stream, int) else stream.cuda_stream
 

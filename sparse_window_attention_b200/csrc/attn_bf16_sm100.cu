@@ -566,7 +566,7 @@ basa_status window_params(AttnParams &P, const void *q, const void *k, const voi
     if (!encode_grid_map(&P.map_q[i], q, pm, N, P.plan.shape[i]) ||
         !encode_grid_map(&P.map_k[i], k, pm, kv_rows, P.plan.shape[i]) ||
         !encode_grid_map(&P.map_v[i], v, p, kv_rows, P.plan.shape[i]) ||
-        !encode_grid_map(&P.map_o[i], out, p, N, P.plan.shape[i]))
+        (out && !encode_grid_map(&P.map_o[i], out, p, N, P.plan.shape[i])))
       return BASA_ERR_CUDA;
   }
   P.n_pool = p.pt > 0 ? (p.T / p.pt) * (p.H / p.ph) * (p.W / p.pw) : 0;

@@ -444,7 +444,7 @@ basa_status launch_diff_attn_bf16(const void *q, const void *k, const void *v, c
                                   const int32_t *route_idx, const basa_diff_params &dp, void *out, void *pre,
                                   void *second, float *lse, const basa_params &p, cudaStream_t s) {
   static thread_local AttnParams P;  // large: kept off the stack
-  basa_status st = window_params(P, q, k, v, kp, vp, route_idx, out, lse, BASA_KEYS_ALL, p, 2);
+  basa_status st = window_params(P, q, k, v, kp, vp, route_idx, nullptr, lse, BASA_KEYS_ALL, p, 2);
   if (st != BASA_OK) return st;
   P.lambda = static_cast<const __nv_bfloat16 *>(dp.lambda);
   P.norm_weight = static_cast<const __nv_bfloat16 *>(dp.weight);

@@ -222,7 +222,7 @@ __device__ __forceinline__ void apply_mask(uint32_t (&s)[N], const uint32_t *mas
 }  // namespace sm100
 
 // Parameters of a window-mode launch. `maps` softmax maps share a head's values: q, k, kp
-// have maps * heads heads, v, vp and out have heads.
+// have maps * heads heads, v, vp and out have heads. `out` may be null: no map of it.
 basa_status window_params(sm100::AttnParams &P, const void *q, const void *k, const void *v, const void *kp,
                           const void *vp, const int32_t *route_idx, void *out, float *lse, uint32_t keys,
                           const basa_params &p, int maps);
