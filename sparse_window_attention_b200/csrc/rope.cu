@@ -193,13 +193,15 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const _
   const bool norm = t.weight != nullptr;
   const int u0 = group * t.group_units, n_units = min(t.group_units, a.B * t.heads - u0);
   const T *kind = nullptr;
-  // A row past the end reads row 0 (shuffles want every lane) and writes nothing.
+  // A row past the end works on zeros (shuffles want every lane) and writes nothing.
   const long long row = valid ? r : 0;
   const T *x0 = static_cast<const T *>(t.x) + row * t.xs[2] + c * VEC;
   T *y0 = static_cast<T *>(t.y) + row * t.ys[2] + c * VEC;
   const T *d0 = static_cast<const T *>(t.dy) + row * t.ds[2] + c * VEC;
   UnitWalk yw(t.ys, u0, t.heads);
-  const auto load = [](const T *p, uint4 &u, uint4 &v) {
+  const auto load = [valid](const T *p, uint4 &u, uint4 &v) {
+    u = v = make_uint4(0, 0, 0, 0);
+    if (!valid) return;
     u = __ldcs(reinterpret_cast<const uint4 *>(p));
     v = __ldcs(reinterpret_cast<const uint4 *>(p + D / 2));
   };
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const _
 #pragma unroll
           for (int i = 0; i < H2; ++i) ss = ptx::ffma2(xb[i], xb[i], ptx::ffma2(xa[i], xa[i], ss));
           const float rms = rsqrtf(row_sum<LPR>(f2_sum(ss)) * (1.f / D) + a.eps);
-          const uint64_t rms2 = f2_both(valid ? rms : 0.f);  // a row past the end adds nothing to dweight
+          const uint64_t rms2 = f2_both(rms);
 #pragma unroll
           for (int i = 0; i < H2; ++i) {
             const uint64_t pa = ptx::fmul2(ga[i], xa[i]), pb = ptx::fmul2(gb[i], xb[i]);

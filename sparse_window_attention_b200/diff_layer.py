@@ -19,7 +19,7 @@ class BasaDiffLayer:
     q [batch, 2 heads, N, head_dim]; k [batch, 2 heads, N + n_text, head_dim];
     v [batch, heads, N + n_text, head_dim]; ``lam`` [heads] the second maps' weights;
     ``weight`` [head_dim] (None: no norm) of the RMS norm of each head's rows, times
-    ``gain``. Pooled keys and values and routed windows are taken from ``kp``, ``vp``,
+    ``gain``. All tensors are contiguous. Pooled keys and values and routed windows are taken from ``kp``, ``vp``,
     ``route_idx`` where given and computed otherwise (``pool_kv``, ``route``).
     """
 
@@ -27,6 +27,8 @@ class BasaDiffLayer:
                  device="cuda", route_radius=0, gain=1.0, eps=1e-6):
         if dtype not in ("bf16", "f32"):
             raise ValueError("dtype: bf16 or f32")
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("BasaDiffLayer clears its error word when it is made: make it before a capture")
         self.batch, self.heads, self.head_dim = batch, heads, head_dim
         self.grid, self.window, self.pool = tuple(grid), tuple(window), tuple(pool)
         self.n_text, self.routed_k, self.route_radius = n_text, routed_k, route_radius

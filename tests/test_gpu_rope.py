@@ -209,6 +209,22 @@ def test_zero_rows_infinities_and_nan_stay_in_their_rows():
     assert torch.equal(y[keep], clean[keep])
 
 
+def test_overflowing_rows_in_place_stay_out_of_other_gradients():
+    """Rows in blocks that the sequence does not fill: a first row that overflows (and is
+    overwritten in place) leaves the weight's gradient of a range without it as it was."""
+    from sparse_window_attention_b200.rope import GridRope, RopePart
+
+    g = _rng(9)
+    rope = GridRope(128, (1, 5, 9), (16, 56, 56))
+    x, w, dy = _randn(g, 1, 2, 45, 128, dtype="bf16"), _randn(g, 128, dtype="bf16"), _randn(g, 1, 2, 45, 128, dtype="bf16")
+    sub = lambda t: t[:, :, 1:]  # noqa: E731
+    want_dx = torch.empty_like(x)
+    want, = rope.backward([RopePart(sub(x), sub(x), w, 1)], [sub(dy)], [sub(want_dx)])
+    x[:, :, 0], dy[:, :, 0] = float("inf"), float("nan")
+    got, = rope.backward([RopePart(sub(x), sub(x), w, 1)], [sub(dy)], [sub(dy)])
+    assert torch.equal(got, want) and torch.equal(sub(dy), sub(want_dx))
+
+
 def test_offsets_past_32_bits():
     """Rows more than 2^31 elements apart, read and written."""
     from sparse_window_attention_b200.rope import GridRope, RopePart
