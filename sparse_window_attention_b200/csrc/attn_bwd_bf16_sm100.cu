@@ -37,8 +37,12 @@
 // maps' dV meet without a buffer or an atomic. (Both maps at once, sharing dout V^T, would
 // take six 128-column accumulators and TMEM holds four.) The passes overlap at their ends by
 // programmatic dependent launch: the long pass runs first, on fewer CTAs than there are SMs
-// as often as not, and the dq pass, which needs nothing of it, fills the rest; the window
-// pass starts under the reduction and waits for it before its epilogue.
+// as often as not, and the dq pass, which needs nothing of it, fills the rest. With few chunks
+// the last CTA of a long key tile to finish sums them itself (in their order), so the window
+// pass starts as the dq pass drains and waits for both before its epilogue; lambda's and the
+// weight's sums run under its end. With many chunks one CTA would sum them for longer than
+// the dq pass hides, and the reduction is a launch of its own, under which the window pass
+// starts.
 //
 // Warp roles (320 threads): warp 0 TMA loads, warp 1 issues tcgen05 MMAs (one
 // thread), warps 2-9 compute P and dS: two warpgroups, each owning 64 of the 128
@@ -105,6 +109,8 @@ struct alignas(64) BwdParams {
   const __nv_bfloat16 *lambda;  // differential form: [heads]
   __nv_bfloat16 *dk;            // differential form: dk itself, for map 2's rows
   float *dr;                    // differential form: [map][window][query tile] sums of rec.z (sum dS)
+  int *long_done;               // differential form, nullable: [unit of v][long tile] chunks that are finished
+  __nv_bfloat16 *dv;            // (with long_done) for the text rows
   int heads;
   Geo g;
   int bh_count;  // units of v, dout and the routes (differential form: q, k have two for each)
@@ -227,6 +233,22 @@ __device__ __forceinline__ void zero_masked(float (&x)[64], uint32_t m0, uint32_
     if (!(((i < 32 ? m0 : m1) >> (i & 31)) & 1u)) x[i] = 0.f;
 }
 
+// Stores the sum of four columns of a long key row's gradient: dK of map `which` of unit bh, or
+// (which == maps) dV. Pooled rows to dkvp (float32), text rows to dk, dv.
+__device__ __forceinline__ void store_long_sum(const float4 &s, float *dkvp, __nv_bfloat16 *dk, __nv_bfloat16 *dv, int which,
+                                               int maps, int bh, int bh_count, bool pooled, int r, int c4, int n_pool,
+                                               int n_text, long long N) {
+  const bool is_v = which == maps;
+  const long long unit = is_v ? bh : (long long)maps * bh + which;
+  if (pooled) {
+    const long long at = (is_v ? (long long)maps * bh_count : 0) + unit;
+    *reinterpret_cast<float4 *>(dkvp + (at * n_pool + r) * 128 + c4 * 4) = s;
+  } else {
+    const long long o = (unit * (N + n_text) + N + r) * 128 + c4 * 4;
+    reinterpret_cast<uint2 *>((is_v ? dv : dk) + o)[0] = make_uint2(ptx::pack_bf16x2(s.x, s.y), ptx::pack_bf16x2(s.z, s.w));
+  }
+}
+
 // Packs 64 fp32 values (pairs 2i, 2i+1) into 32 bf16x2 words.
 __device__ __forceinline__ void pack64(const float (&x)[64], uint32_t (&w)[32]) {
 #pragma unroll
@@ -278,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + L::ctrl);
   int16_t *list = reinterpret_cast<int16_t *>(smem + L::list);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (DIFF && MODE == kDkvLong) ptx::grid_launch_dependents();
+  if (DIFF && MODE != kDkvWindow) ptx::grid_launch_dependents();
   // What follows the dq pass needs the long pass's sums: one CTA of it ends after them.
   const bool last_to_end = DIFF && MODE == kDq && blockIdx.x == gridDim.x - 1 && threadIdx.x == 0;
 
@@ -848,7 +870,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
         }
         if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.acc_full, n_cols > 0 ? m : 0));
         if (!ok) continue;
-        if (DIFF && MODE == kDkvWindow) ptx::grid_wait();  // the pooled keys' gradients
+        if (DIFF && MODE == kDkvWindow) {
+          ptx::grid_wait();  // the pooled keys' gradients
+          ptx::grid_launch_dependents();
+        }
         ptx::tc_fence_after();
         const bool last_map = m + 1 == kMaps;
         const int unit = map_unit(m);  // of k and dk
@@ -921,7 +946,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           }
         }
       }
+      if (DIFF && MODE == kDkvLong) __threadfence();  // this chunk's sums, before it counts as finished
       ptx::named_barrier(1, 256);
+      if (DIFF && MODE == kDkvLong && P.long_done != nullptr) {
+        if (threadIdx.x == 64)
+          c.n_list = *reinterpret_cast<volatile int *>(&c.abort) ? -1 : atomicAdd(P.long_done + bh * P.n_long_tiles + kt, 1);
+        ptx::named_barrier(1, 256);
+        if (c.n_list == P.n_chunks - 1) {  // the last chunk of this key tile: their sums, in order
+          __threadfence();
+          const bool pooled = kt < P.n_pool_tiles;
+          const int tile = pooled ? kt : kt - P.n_pool_tiles, rows = pooled ? P.n_pool : P.n_text;
+          const float *base = P.part + (((long long)bh * P.n_long_tiles + kt) * P.n_chunks) * 3 * (kTileRows * 128);
+          for (int i = 0; i < 6; ++i) {  // 3 arrays of 128 x 32 groups of four columns, eight a thread at a time
+            float4 sum[8];
+            const int first = (i & 1) * 2048 + (threadIdx.x - 64);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int ch = 0; ch < P.n_chunks; ++ch) {
+              const float4 *p = reinterpret_cast<const float4 *>(base + ((long long)ch * 3 + (i >> 1)) * (kTileRows * 128)) + first;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 x = __ldcg(p + 256 * e);
+                sum[e].x += x.x; sum[e].y += x.y; sum[e].z += x.z; sum[e].w += x.w;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int at = first + 256 * e, r = tile * kTileRows + at / 32;
+              if (r < rows)
+                store_long_sum(sum[e], const_cast<float *>(P.dkvp), P.dk, P.dv, i >> 1, 2, bh, P.bh_count, pooled, r, at % 32,
+                               P.n_pool, P.n_text, P.g.N);
+            }
+          }
+        }
+      }
       if (MODE == kDkvWindow && threadIdx.x == 64 && ok && !*reinterpret_cast<volatile int *>(&c.abort)) {
         store_window_tile(P.plan, P.g, P.map_dk, row_tile, row_org, map_unit(kMaps - 1), row0);
         store_window_tile(P.plan, P.g, P.map_dv, row_tile, row_org, bh, row1);
@@ -993,17 +1051,8 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(const float *part, floa
     }
   }
 #pragma unroll
-  for (int a = 0; a <= MAPS; ++a) {
-    const long long unit = a < MAPS ? (long long)MAPS * bh + a : bh;
-    if (pooled) {
-      const long long at = (a < MAPS ? 0 : (long long)MAPS * bh_count) + unit;
-      *reinterpret_cast<float4 *>(dkvp + (at * n_pool + r) * 128 + c4 * 4) = s[a];
-    } else {
-      const long long o = (unit * (N + n_text) + N + r) * 128 + c4 * 4;
-      reinterpret_cast<uint2 *>((a < MAPS ? dk : dv) + o)[0] =
-          make_uint2(ptx::pack_bf16x2(s[a].x, s[a].y), ptx::pack_bf16x2(s[a].z, s[a].w));
-    }
-  }
+  for (int a = 0; a <= MAPS; ++a)
+    store_long_sum(s[a], dkvp, dk, dv, a, MAPS, bh, bh_count, pooled, r, c4, n_pool, n_text, N);
 }
 
 // ----------------------------------------------------------------- host side
@@ -1141,27 +1190,14 @@ basa_status bwd_params(BwdParams &P, BwdLayout &L, const void *q, const void *k,
   return BASA_OK;
 }
 
-// The passes after the records: dq, pooled and text dK/dV, their chunks' sums, window dK/dV.
-// In the differential form `early` launches start under the one before them, see above;
-// `sums` is launched before the window pass, which waits for it and for what it waits for.
-template <bool DIFF, typename F>
-basa_status run_passes(const BwdParams &P, const BwdLayout &L, void *dk, void *dv, const basa_params &p, cudaStream_t s,
-                       F &&sums) {
-  constexpr int maps = DIFF ? 2 : 1;
-  const long long bh = P.bh_count, window_blocks = bh * P.g.nWin * P.max_tiles;
-  basa_status st = DIFF ? BASA_OK : run_bwd<kDq, DIFF>(P, window_blocks, s);
-  if (st != BASA_OK) return st;
-  if (L.n_long > 0 && (st = run_bwd<kDkvLong, DIFF>(P, bh * L.n_long * L.n_chunks, s)) != BASA_OK) return st;
-  if (DIFF && (st = run_bwd<kDq, DIFF>(P, maps * window_blocks, s, L.n_long > 0)) != BASA_OK) return st;
-  if (L.n_long > 0) {
-    const long long threads = bh * L.n_long * kTileRows * 32;
-    bwd_reduce_kernel<maps><<<unsigned((threads + 255) / 256), 256, 0, s>>>(
-        P.part, const_cast<float *>(P.dkvp), static_cast<__nv_bfloat16 *>(dk), static_cast<__nv_bfloat16 *>(dv), int(bh),
-        L.n_long, L.n_chunks, P.n_pool, P.n_pool_tiles, p.n_text, P.g.N);
-    if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
-  }
-  if ((st = sums()) != BASA_OK) return st;
-  return run_bwd<kDkvWindow, DIFF>(P, window_blocks, s, DIFF);
+basa_status run_reduce(int maps, const BwdParams &P, const BwdLayout &L, void *dk, void *dv, const basa_params &p,
+                       cudaStream_t s) {
+  const long long threads = (long long)P.bh_count * L.n_long * kTileRows * 32;
+  const auto kernel = maps == 2 ? bwd_reduce_kernel<2> : bwd_reduce_kernel<1>;
+  kernel<<<unsigned((threads + 255) / 256), 256, 0, s>>>(
+      P.part, const_cast<float *>(P.dkvp), static_cast<__nv_bfloat16 *>(dk), static_cast<__nv_bfloat16 *>(dv), P.bh_count,
+      L.n_long, L.n_chunks, P.n_pool, P.n_pool_tiles, p.n_text, P.g.N);
+  return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1184,22 +1220,43 @@ basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, co
       static_cast<const __nv_bfloat16 *>(out), static_cast<const __nv_bfloat16 *>(dout), lse,
       static_cast<float4 *>(workspace), rows);
   if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
-  return run_passes<false>(P, L, dk, dv, p, s, [] { return BASA_OK; });
+  const long long bh = P.bh_count, window_blocks = bh * P.g.nWin * P.max_tiles;
+  if ((st = run_bwd<kDq, false>(P, window_blocks, s)) != BASA_OK) return st;
+  if (L.n_long > 0) {
+    if ((st = run_bwd<kDkvLong, false>(P, bh * L.n_long * L.n_chunks, s)) != BASA_OK) return st;
+    if ((st = run_reduce(1, P, L, dk, dv, p, s)) != BASA_OK) return st;
+  }
+  return run_bwd<kDkvWindow, false>(P, window_blocks, s);
 }
 
-// Differential form: the layout of two maps, then g (with a norm), then the partial sums
-// of dlambda and dweight, then the dq pass's.
-size_t dr_count(const basa_params &p, const WindowPlan &plan) {
+namespace {
+// Differential form. A long key tile's chunks are summed by its last CTA up to this many.
+constexpr int kLastSums = 8;
+
+// Workspace: the layout of two maps, g (with a norm), the partial sums of dlambda and
+// dweight, the dq pass's, the counts of finished chunks.
+struct DiffLayout {
+  size_t g, sums, dr, done, total;
+};
+DiffLayout diff_layout(bool norm, const basa_params &p, const WindowPlan &plan) {
   int tiles = 0;
   for (int t = 0; t < 8; ++t) tiles = std::max<int>(tiles, plan.type[t].n_tiles);
-  return 2 * size_t(p.B) * p.heads * make_geo(p).nWin * tiles;
+  const size_t units = size_t(p.B) * p.heads;
+  const BwdLayout L = bwd_layout(p, plan, 2);
+  DiffLayout D{};
+  D.g = L.total;
+  D.sums = D.g + (norm ? align256(units * p.T * p.H * p.W * p.head_dim * 2) : 0);
+  D.dr = D.sums + align256(diff_prep_workspace(p));
+  D.done = D.dr + align256(2 * units * make_geo(p).nWin * tiles * sizeof(float));
+  D.total = D.done + align256(units * L.n_long * sizeof(int));
+  return D;
 }
+}  // namespace
 
 size_t diff_attn_bwd_bf16_workspace(bool norm, const basa_params &p) {
   static thread_local WindowPlan plan;
   if (build_window_plan(p, &plan) != BASA_OK) return 0;
-  const size_t g = norm ? align256(size_t(p.B) * p.heads * p.T * p.H * p.W * p.head_dim * 2) : 0;
-  return bwd_layout(p, plan, 2).total + g + align256(diff_prep_workspace(p)) + align256(dr_count(p, plan) * sizeof(float));
+  return diff_layout(norm, p, plan).total;
 }
 
 basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *v, const void *kp, const void *vp,
@@ -1211,21 +1268,34 @@ basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *
   static thread_local WindowPlan plan;
   basa_status st = build_window_plan(p, &plan);
   if (st != BASA_OK) return st;
-  uint8_t *ws = static_cast<uint8_t *>(workspace), *g = ws + bwd_layout(p, plan, 2).total, *part = g;
-  if (dp.weight) part += align256(size_t(p.B) * p.heads * p.T * p.H * p.W * p.head_dim * 2);
-  const void *grad = dp.weight ? g : dout;
+  const DiffLayout D = diff_layout(dp.weight != nullptr, p, plan);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
   BwdLayout L;
-  if ((st = bwd_params(P, L, q, k, v, kp, vp, route_idx, grad, dq, dk, dv, ws, p, 2)) != BASA_OK) return st;
+  st = bwd_params(P, L, q, k, v, kp, vp, route_idx, dp.weight ? ws + D.g : dout, dq, dk, dv, ws, p, 2);
+  if (st != BASA_OK) return st;
+  const bool any_long = L.n_long > 0, last_sums = any_long && L.n_chunks <= kLastSums;
   P.lambda = static_cast<const __nv_bfloat16 *>(dp.lambda);
   P.heads = p.heads;
   P.dk = static_cast<__nv_bfloat16 *>(dk);
-  P.dr = reinterpret_cast<float *>(part + align256(diff_prep_workspace(p)));
-  float *sums = reinterpret_cast<float *>(part);
-  st = launch_diff_prep(pre, second, lse, dout, dp, g, reinterpret_cast<float4 *>(ws), nullptr, sums, p, s);
+  P.dv = static_cast<__nv_bfloat16 *>(dv);
+  P.dr = reinterpret_cast<float *>(ws + D.dr);
+  P.long_done = last_sums ? reinterpret_cast<int *>(ws + D.done) : nullptr;
+  float *sums = reinterpret_cast<float *>(ws + D.sums);
+  st = launch_diff_prep(pre, second, lse, dout, dp, ws + D.g, reinterpret_cast<float4 *>(ws), nullptr, sums, P.long_done,
+                        L.n_long, p, s);
   if (st != BASA_OK) return st;
-  return run_passes<true>(P, L, dk, dv, p, s, [&] {
-    return launch_diff_sums(sums, P.dr, 2 * P.g.nWin * P.max_tiles, dp, dlambda, dweight, L.n_long > 0, p, s);
-  });
+  const long long bh = P.bh_count, window_blocks = bh * P.g.nWin * P.max_tiles;
+  const auto run_sums = [&] {
+    return launch_diff_sums(sums, P.dr, 2 * P.g.nWin * P.max_tiles, dp, dlambda, dweight, true, p, s);
+  };
+  if (any_long && (st = run_bwd<kDkvLong, true>(P, bh * L.n_long * L.n_chunks, s)) != BASA_OK) return st;
+  if ((st = run_bwd<kDq, true>(P, 2 * window_blocks, s, any_long)) != BASA_OK) return st;
+  if (any_long && !last_sums) {
+    if ((st = run_reduce(2, P, L, dk, dv, p, s)) != BASA_OK || (st = run_sums()) != BASA_OK) return st;
+    return run_bwd<kDkvWindow, true>(P, window_blocks, s, true);
+  }
+  if ((st = run_bwd<kDkvWindow, true>(P, window_blocks, s, true)) != BASA_OK) return st;
+  return run_sums();
 }
 
 }  // namespace basa

@@ -431,7 +431,7 @@ basa_status launch_diff_attn_bwd_f32(const void *q, const void *k, const void *v
   float *g = reinterpret_cast<float *>(ws);
   if (dp.weight) ws += align256(rows * p.head_dim * sizeof(float));
   float *part = reinterpret_cast<float *>(ws);
-  basa_status st = launch_diff_prep(pre, second, lse, dout, dp, g, nullptr, drow, part, p, s);
+  basa_status st = launch_diff_prep(pre, second, lse, dout, dp, g, nullptr, drow, part, nullptr, 0, p, s);
   if (st != BASA_OK || (st = launch_diff_sums(part, nullptr, 0, dp, dlambda, dweight, false, p, s)) != BASA_OK) return st;
   BwdArgs b{};
   b.lse = lse;

@@ -179,12 +179,12 @@ basa_status launch_diff_text_bf16(const void *q_text, const void *k, const void 
 basa_status launch_diff_combine(int n_splits, const float *part, const float *part_lse, long long rows,
                                 const basa_diff_params &dp, void *out, const basa_params &p, cudaStream_t s);
 // Start of the backward: g, the rows' records (or D alone), partial sums of dlambda and
-// dweight; and their end, with the dq pass's sums (`dr`, nullable: dr_per_unit for each unit).
+// dweight (and n_zeros counters of each unit are cleared, where given); and their end, with the dq pass's sums (`dr`, nullable: dr_per_unit for each unit).
 // An `early` end may run under the launch before it, whose results it does not need.
 size_t diff_prep_workspace(const basa_params &p);
 basa_status launch_diff_prep(const void *pre, const void *second, const float *lse, const void *dout,
                              const basa_diff_params &dp, void *g, float4 *rec, float *drow, float *part,
-                             const basa_params &p, cudaStream_t s);
+                             int *zeros, int n_zeros, const basa_params &p, cudaStream_t s);
 basa_status launch_diff_sums(const float *part, const float *dr, int dr_per_unit, const basa_diff_params &dp,
                              void *dlambda, void *dweight, bool early, const basa_params &p, cudaStream_t s);
 size_t diff_attn_bwd_bf16_workspace(bool norm, const basa_params &p);

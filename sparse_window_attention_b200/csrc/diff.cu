@@ -166,8 +166,9 @@ struct PrepArgs {
   void *g;           // [units][rows][d]; unused without weight (g = dout)
   float4 *rec;       // nullable: records {-L log2 e, -D, weight of dR in -dlambda, 0} [units][2][rows]
   float *drow;       // nullable: D alone, [units][2][rows]
+  int *zeros;        // nullable: [units][n_zeros], set to 0
   float *part;       // [blocks][1 + d]: sum g . O2, then the weight's gradient
-  int heads, blocks_per_unit;
+  int heads, blocks_per_unit, n_zeros;
   long long rows;
   float gain, eps;
 };
@@ -179,6 +180,8 @@ __global__ void __launch_bounds__(kDiffThreads) diff_prep_kernel(const __grid_co
   const long long unit = blockIdx.x / a.blocks_per_unit;
   const long long r0 = (long long)(blockIdx.x % a.blocks_per_unit) * kPrepRows;
   const long long r1 = min(a.rows, r0 + kPrepRows);
+  if (a.zeros != nullptr && r0 == 0)
+    for (int i = threadIdx.x; i < a.n_zeros; i += kDiffThreads) a.zeros[unit * a.n_zeros + i] = 0;
   const int c = threadIdx.x % LPR;
   const float lam = to_float(static_cast<const T *>(a.lambda)[unit % a.heads]);
   float w[8], dw[8], dl = 0.f;
@@ -296,11 +299,11 @@ __global__ void __launch_bounds__(1024) diff_sum_kernel(const __grid_constant__ 
     const int n = a.B * a.blocks_per_unit;
     for (int i = threadIdx.x; i < n; i += 1024) {
       const long long unit = (long long)(i / a.blocks_per_unit) * a.heads + blockIdx.x;
-      s += a.part[(unit * a.blocks_per_unit + i % a.blocks_per_unit) * stride];
+      s += __ldcg(a.part + (unit * a.blocks_per_unit + i % a.blocks_per_unit) * stride);
     }
     for (int b = 0; a.dr != nullptr && b < a.B; ++b) {
       const float *p = a.dr + ((long long)b * a.heads + blockIdx.x) * a.dr_per_unit;
-      for (int i = threadIdx.x; i < a.dr_per_unit; i += 1024) s += p[i];
+      for (int i = threadIdx.x; i < a.dr_per_unit; i += 1024) s += __ldcg(p + i);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(1024) diff_sum_kernel(const __grid_constant__ 
     const int col = (blockIdx.x - a.heads) * 32 + lane;
     const long long n = (long long)a.B * a.heads * a.blocks_per_unit;
 #pragma unroll 4
-    for (long long i = slice; i < n; i += 32) s += a.part[i * stride + 1 + col];
+    for (long long i = slice; i < n; i += 32) s += __ldcg(a.part + i * stride + 1 + col);
     red[slice][lane] = s;
     __syncthreads();
     if (slice == 0) {
@@ -363,7 +366,7 @@ size_t diff_prep_workspace(const basa_params &p) {
 
 basa_status launch_diff_prep(const void *pre, const void *second, const float *lse, const void *dout,
                              const basa_diff_params &dp, void *g, float4 *rec, float *drow, float *part,
-                             const basa_params &p, cudaStream_t s) {
+                             int *zeros, int n_zeros, const basa_params &p, cudaStream_t s) {
   PrepArgs a{};
   a.pre = pre;
   a.second = second;
@@ -375,6 +378,8 @@ basa_status launch_diff_prep(const void *pre, const void *second, const float *l
   a.rec = rec;
   a.drow = drow;
   a.part = part;
+  a.zeros = zeros;
+  a.n_zeros = n_zeros;
   a.heads = p.heads;
   a.rows = (long long)p.T * p.H * p.W;
   a.gain = dp.gain;
