@@ -1230,8 +1230,13 @@ basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, co
 }
 
 namespace {
-// Differential form. A long key tile's chunks are summed by its last CTA up to this many.
-constexpr int kLastSums = 8;
+// Differential form: whether a long key tile's chunks are summed by its last CTA. That takes
+// it 1 to 2 us a chunk, which hides behind the dq pass's waves and costs where those are few:
+// a training step of 6 chunks and 2 waves took 211 us so and 218 us with kernels of their own,
+// one of 5 chunks and 1 wave 98 us so and 89 us with kernels of their own.
+bool last_cta_sums(const BwdLayout &L, long long dq_ctas) {
+  return L.n_long > 0 && L.n_chunks <= 2 + 2 * ((dq_ctas + kLongSms - 1) / kLongSms);
+}
 
 // Workspace: the layout of two maps, g (with a norm), the partial sums of dlambda and
 // dweight, the dq pass's, the counts of finished chunks.
@@ -1273,7 +1278,8 @@ basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *
   BwdLayout L;
   st = bwd_params(P, L, q, k, v, kp, vp, route_idx, dp.weight ? ws + D.g : dout, dq, dk, dv, ws, p, 2);
   if (st != BASA_OK) return st;
-  const bool any_long = L.n_long > 0, last_sums = any_long && L.n_chunks <= kLastSums;
+  const long long bh = P.bh_count, window_blocks = bh * P.g.nWin * P.max_tiles;
+  const bool any_long = L.n_long > 0, last_sums = last_cta_sums(L, 2 * window_blocks);
   P.lambda = static_cast<const __nv_bfloat16 *>(dp.lambda);
   P.heads = p.heads;
   P.dk = static_cast<__nv_bfloat16 *>(dk);
@@ -1284,7 +1290,6 @@ basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *
   st = launch_diff_prep(pre, second, lse, dout, dp, ws + D.g, reinterpret_cast<float4 *>(ws), nullptr, sums, P.long_done,
                         L.n_long, p, s);
   if (st != BASA_OK) return st;
-  const long long bh = P.bh_count, window_blocks = bh * P.g.nWin * P.max_tiles;
   const auto run_sums = [&] {
     return launch_diff_sums(sums, P.dr, 2 * P.g.nWin * P.max_tiles, dp, dlambda, dweight, true, p, s);
   };
