@@ -10,7 +10,8 @@
 // no shuffles but the row maximum's) and a group of channels for the product with V (the
 // probabilities read back as broadcasts). Few queries a CTA because the layers that run in
 // float32 are small and bound by latency: with a thread a query and a launch a map, 2 heads
-// of 16 windows of 64 tokens (128 keys each) took 57 us.
+// of 16 windows of 64 tokens (128 keys each) took 57 us, so 19 us (1, 2 and 8 queries a warp 26,
+// 20 and 29).
 #include "attn_f32.cuh"
 
 namespace basa {

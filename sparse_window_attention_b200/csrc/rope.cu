@@ -14,7 +14,9 @@
 // is in packed float32 pairs, two channel pairs an instruction, with the norm's weight
 // multiplied into the cos and sin beforehand: element by element, and with the unit's
 // index divided out for every load, the kernel was bound by its instructions (half of
-// all issue slots, 4.6 TB/s).
+// all issue slots, 4.6 TB/s). Measured: q, k, v of 24 heads and 16384 + 512 rows (623 MB in
+// and out) 107 us, 5.8 of the 6.55 TB/s that a copy reaches; forward and backward of 12
+// heads and 32760 rows (1.41 GB) 247 us, 5.7 TB/s; one row 3.4 us, a launch's latency.
 #include <cuda_bf16.h>
 
 #include <algorithm>
