@@ -50,8 +50,8 @@
 // keys 340 us (18 products of 2 d FLOP a query and key where 12 would do, as the scores and
 // dout V^T are taken again in the dK/dV passes, the latter per map); 2 x 3 heads,
 // 6 x 18 x 26, 234-token windows, 2 routed 202 us. What bounds them: in the dq and long passes
-// the chain score, P, dS of each tile (40% of tensor cycles each), in the window pass a CTA's
-// start and end around its few query tiles (18%).
+// the chain score, P, dS of each tile (tensor cores active 30% of the time), in the window pass
+// a CTA's start and end around its few query tiles (15%).
 //
 // Warp roles (320 threads): warp 0 TMA loads, warp 1 issues tcgen05 MMAs (one
 // thread), warps 2-9 compute P and dS: two warpgroups, each owning 64 of the 128
