@@ -139,8 +139,8 @@ static_assert(sizeof(BwdParams) <= 32764, "window plan too large for the kernel 
 struct Ctrl {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   // dq pass: a_ready, s_full[0], s_free, dp_full[0], ds_full[0]; dK/dV passes: s_full[0],
-  // dp_full[0], and per compute group p_full[g], ds_full[g]
-  uint64_t row_full, row_free, s_full[2], dp_full[2], s_free, a_ready, p_full[2], ds_full[2], acc_full, drain;
+  // s_free, dp_full[0], and per compute group ds_full[g]
+  uint64_t row_full, row_free, s_full[2], dp_full[2], s_free, a_ready, ds_full[2], acc_full, drain;
   uint32_t tmem_base;
   int abort;
   int n_cols;   // column tiles streamed by this CTA
@@ -349,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     for (int g = 0; g < 2; ++g) {
       ptx::mbar_init(&c.s_full[g], 1);
       ptx::mbar_init(&c.dp_full[g], 1);
-      ptx::mbar_init(&c.p_full[g], 128);
       ptx::mbar_init(&c.ds_full[g], per_group);
     }
     ptx::mbar_init(&c.s_free, 256);
@@ -597,10 +596,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
         }
       } else if (MODE != kDq && ok && n_cols > 0) {
         // TMEM: S^T at 0, dP^T at 128, dV at 256, dK at 384. Compute group g owns query
-        // columns [64 g, 64 g + 64) of S^T and dP^T; the dV and dK products are issued
-        // per group (the K-steps over its queries) as soon as that group's P^T or dS^T
-        // is in TMEM. S^T and dP^T stay whole N = 128 products (an N = 64 half reads
-        // the same A operand from shared memory for half the work).
+        // columns [64 g, 64 g + 64) of S^T and dP^T, and writes dS^T and P^T (bf16, 32
+        // columns each) over its dP^T: S^T is free once it is in registers, so S^T(j+1) is
+        // there before the next tile's P is begun (with P^T over S^T it had to wait for dV
+        // to read that: 24 heads of 16896 keys 1.38 against 1.36 ms). The dK products are issued per group (the K-steps over its
+        // queries) as soon as that group's dS^T is in TMEM, and before those of dV, since
+        // the next tile but one's queries, wanted first, take their slot. S^T and dP^T stay
+        // whole N = 128 products (an N = 64 half reads the same A operand from shared
+        // memory for half the work).
         const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
         // Differential form: tiles [0, n_cols) are map 2's, [n_cols, 2 n_cols) map 1's.
         const int total = kMaps * n_cols;
@@ -621,31 +624,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           const int qi = 2 * j, di = 2 * j + 1, qn = qi + 2, dn = di + 2;
           const bool more = j + 1 < total;
           const bool map_start = j == 0 || (kMaps == 2 && j == n_cols);
-          if (kMaps == 2 && j == n_cols) {
-            // both groups have read map 2's dK and rescaled dV before their first P^T
-            ok = wt.wait(&c.p_full[0], j & 1) && wt.wait(&c.p_full[1], j & 1);
-            if (!ok) break;
-          }
-          for (int g = 0; ok && g < 2; ++g) {
-            ok = wt.wait(&c.p_full[g], j & 1);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            issue_ts_group(tDV, tS, ringMn + slot_of(di), g, j > 0 || g > 0);  // dV += P^T(j) dout_j
-          }
-          if (!ok) break;
-          ptx::mma_commit(&c.empty[di % kSlots]);
-          // Map 2's last tile: its dK first, which does not wait for map 1's key tile.
+          // Map 2's last tile: its sums first, which do not wait for map 1's key tile.
           const bool boundary = kMaps == 2 && j + 1 == n_cols;
           auto next_scores = [&] {
-            if (!wt.wait(&c.full[qn % kSlots], (qn / kSlots) & 1)) return false;
+            if (!wt.wait(&c.s_free, j & 1) || !wt.wait(&c.full[qn % kSlots], (qn / kSlots) & 1)) return false;
             if (boundary && !wt.wait(&c.row_full, 1)) return false;
             ptx::tc_fence_after();
-            issue_ss(tS, r0, ringK + slot_of(qn));  // S^T(j+1): P^T(j) has been read by dV
+            issue_ss(tS, r0, ringK + slot_of(qn));  // S^T(j+1), while P(j) is computed
             ptx::mma_commit(&c.s_full[0]);
             if (kMaps == 2 && j + 2 == n_cols) ptx::mma_commit(&c.row_free);
             return true;
           };
           if (more && !boundary && !next_scores()) break;
+          if (kMaps == 2 && j == n_cols) {
+            // both groups have read map 2's dK and rescaled dV before their first P^T
+            ok = wt.wait(&c.ds_full[0], j & 1) && wt.wait(&c.ds_full[1], j & 1);
+            if (!ok) break;
+          }
           for (int g = 0; ok && g < 2; ++g) {
             ok = wt.wait(&c.ds_full[g], j & 1);
             if (!ok) break;
@@ -654,6 +649,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           }
           if (!ok) break;
           ptx::mma_commit(&c.empty[qi % kSlots]);
+          for (int g = 0; g < 2; ++g)
+            issue_ts_group(tDV, tDP + 32, ringMn + slot_of(di), g, j > 0 || g > 0);  // dV += P^T(j) dout_j
+          ptx::mma_commit(&c.empty[di % kSlots]);
           if (boundary) {
             ptx::mma_commit(&c.acc_full);  // map 2 is complete
             if (!next_scores()) break;
@@ -661,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           if (more) {
             if (!wt.wait(&c.full[dn % kSlots], (dn / kSlots) & 1)) break;
             ptx::tc_fence_after();
-            issue_ss(tDP, r1, ringK + slot_of(dn));  // dP^T(j+1)
+            issue_ss(tDP, r1, ringK + slot_of(dn));  // dP^T(j+1), after the sums have read P^T(j) and dS^T(j)
             ptx::mma_commit(&c.dp_full[0]);
           }
         }
@@ -810,6 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           ptx::tc_fence_after();
           float p[64];
           tmem_ld64f(tS, p);
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&c.s_free);  // S^T(j) is in registers: the MMA may overwrite it
           {
             // This warp's 64 query records {-L log2 e, -D, 0, 0}, one load per lane
             // for two columns, rewritten as two arrays that the loops below read four
@@ -843,12 +843,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           }
           const bool partial = (m0 & m1) != 0xFFFFFFFFu;  // warp-uniform: a partial query tile
           if (partial) zero_masked(p, m0, m1);
-          uint32_t pk[32];
-          pack64(p, pk);
-          ptx::tmem_st32(tS, pk);  // P^T (bf16) over the first half of this thread's S^T columns
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(&c.p_full[g]);
           ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.dp_full[0], j & 1));
           if (!ok) break;
           ptx::tc_fence_after();
@@ -870,8 +864,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
             dp[i + 3] = d3;
           }
           if (partial) zero_masked(dp, m0, m1);  // dS = 0 there whatever dP holds
+          uint32_t pk[32];
           pack64(dp, pk);
-          ptx::tmem_st32(tDP, pk);  // dS^T (bf16) over the first half of this thread's dP^T columns
+          ptx::tmem_st32(tDP, pk);  // dS^T (bf16) over the first half of this thread's dP^T columns,
+          pack64(p, pk);
+          ptx::tmem_st32(tDP + 32, pk);  // P^T over the second
           ptx::tmem_st_wait();
           ptx::tc_fence_before();
           ptx::mbar_arrive(&c.ds_full[g]);
