@@ -875,11 +875,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
           q_next(P, list, MODE, n_windows, it);
         }
         if (ok) ok = __all_sync(0xFFFFFFFFu, wt.wait(&c.acc_full, n_cols > 0 ? m : 0));
-        if (!ok) continue;
         if (DIFF && MODE == kDkvWindow) {
-          ptx::grid_wait();  // the pooled keys' gradients
+          ptx::grid_wait();  // the pooled keys' gradients; after an expired wait too: this launch ends after the others
           ptx::grid_launch_dependents();
         }
+        if (!ok) continue;
         ptx::tc_fence_after();
         const bool last_map = m + 1 == kMaps;
         const int unit = map_unit(m);  // of k and dk
