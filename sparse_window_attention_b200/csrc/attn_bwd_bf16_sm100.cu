@@ -47,9 +47,9 @@
 // Roundings, as in the other form: P and dS to bfloat16 for the products that sum them (2^-9
 // of each element at most), so dq, dk and dv are off 0.003 of their size where their own
 // rounding is 0.0017. Measured, forward and backward: 12 heads, 64 x 64, 16 x 16 windows, 832
-// keys 340 us (18 products of 2 d FLOP a query and key where 12 would do, as the scores and
+// keys 336 us (18 products of 2 d FLOP a query and key where 12 would do, as the scores and
 // dout V^T are taken again in the dK/dV passes, the latter per map); 2 x 3 heads,
-// 6 x 18 x 26, 234-token windows, 2 routed 202 us. What bounds them: in the dq and long passes
+// 6 x 18 x 26, 234-token windows, 2 routed 200 us. What bounds them: in the dq and long passes
 // the chain score, P, dS of each tile (tensor cores active 30% of the time), in the window pass
 // a CTA's start and end around its few query tiles (15%).
 //
