@@ -37,7 +37,7 @@ struct PlanShape {
 };
 
 struct PlanPiece {
-  int16_t lt, ly, lx;  // offset of the piece inside the window (window-local coordinates)
+  uint16_t lt, ly, lx;  // offset of the piece inside the window (below kMaxTiles * kTileRows = 65536 along any axis)
   uint8_t shape;       // index into WindowPlan::shape
   uint8_t dest;        // first row of the piece inside its tile (multiple of 8)
 };

@@ -238,9 +238,9 @@ basa_status search_window_plan(const basa_params &p, WindowPlan *plan) {
           plan->shape[shape] = {int16_t(rp.ct), int16_t(rp.cy), int16_t(rp.cx), int16_t(rp.rows())};
         }
         PlanPiece &pc = plan->piece[plan->n_pieces++];
-        pc.lt = int16_t(rp.lt);
-        pc.ly = int16_t(rp.ly);
-        pc.lx = int16_t(rp.lx);
+        pc.lt = uint16_t(rp.lt);
+        pc.ly = uint16_t(rp.ly);
+        pc.lx = uint16_t(rp.lx);
         pc.shape = uint8_t(shape);
         pc.dest = uint8_t(tp.dest[id]);
         for (int r = tp.dest[id]; r < tp.dest[id] + rp.rows(); ++r) t.mask[r >> 5] |= 1u << (r & 31);

@@ -75,3 +75,19 @@ def test_random_geometries(checker):
         assert r.startswith("ok") or r == "unsupported", (g, r)
         supported += r.startswith("ok")
     assert supported >= 290  # the plan's limits are only reached by unusual shapes
+
+
+def test_windows_past_32767_along_an_axis(checker):
+    """A window may have 512 tiles of 128 tokens, along one axis too: every piece's offset
+    in it, up to 65535, counts in full."""
+    geos = [
+        (1, 1, 40000, 1, 1, 40000, 0, 0, 0),
+        (1, 1, 65536, 1, 1, 65536, 0, 0, 0),
+        (1, 65280, 1, 1, 32640, 1, 0, 77, 0),
+        (40960, 1, 1, 40960, 1, 1, 640, 0, 0),
+        (1, 1, 40000, 1, 1, 40000, 0, 0, 129),  # wraps: one type of window
+    ]
+    for g, r in zip(geos, run(checker, geos)):
+        assert r.startswith("ok"), (g, r)
+    # one tile more than a plan holds
+    assert run(checker, [(1, 1, 65537, 1, 1, 65537, 0, 0, 0)]) == ["unsupported"]
