@@ -81,7 +81,7 @@ constexpr uint32_t kSmemRow = 0;                            // the two row tiles
 constexpr uint32_t kSmemRing = 2 * kTileBytes;              // then a ring of 32 KB tiles
 constexpr uint32_t kRecBytes = kTileRows * 16;              // 128 records of 16 bytes
 constexpr uint32_t kCtrlBytes = 1024;
-constexpr int kMaxList = 4096;                              // windows whose query tiles one key tile sees
+constexpr int kMaxList = 4096;                              // windows whose query tiles one key tile sees (with routing)
 constexpr uint32_t kTmemCols = 512;
 
 constexpr uint32_t kColRecBytes = 8 * 128 * 4;             // per compute warp: 64 x {-L log2 e}, 64 x {-D}
@@ -99,7 +99,7 @@ struct Smem {
   static constexpr uint32_t col_rec = rec + (MODE == kDq ? 0u : 2 * kRecBytes);
   static constexpr uint32_t ctrl = col_rec + (MODE == kDq ? 0u : kColRecBytes);
   static constexpr uint32_t list = ctrl + kCtrlBytes;
-  static constexpr uint32_t place = list + (MODE == kDkvWindow ? kMaxList * 2 : 0);  // differential form
+  static constexpr uint32_t place = list + (MODE == kDkvWindow ? kMaxList * 4 : 0);  // differential form
   static constexpr uint32_t bytes = place + (MODE == kDkvWindow ? 256 * 8 : 0) + 1024;  // + alignment slack
   static_assert(bytes <= 227u * 1024u, "shared memory of a pass above the 227 KB a CTA may hold");
 };
@@ -202,13 +202,13 @@ __device__ __forceinline__ void key_mask(const BwdParams &P, const Ctrl &c, cons
 struct QIter {
   int li, t, ntiles, type, org[3];
 };
-__device__ __forceinline__ void q_load(const BwdParams &P, const int16_t *list, int mode, QIter &it) {
-  const int w = mode == kDkvLong ? it.li : int(list[it.li]);
+__device__ __forceinline__ void q_load(const BwdParams &P, const int *list, int mode, QIter &it) {
+  const int w = mode == kDkvLong ? it.li : list[it.li];
   window_origin(P.g, w, &it.org[0], &it.org[1], &it.org[2], &it.type);
   it.ntiles = P.plan.type[it.type].n_tiles;
 }
 // Positions the iterator at global query tile `skip` of the window sequence.
-__device__ __forceinline__ void q_first(const BwdParams &P, const int16_t *list, int mode, int skip, QIter &it) {
+__device__ __forceinline__ void q_first(const BwdParams &P, const int *list, int mode, int skip, QIter &it) {
   it.li = 0;
   it.t = 0;
   q_load(P, list, mode, it);
@@ -219,7 +219,7 @@ __device__ __forceinline__ void q_first(const BwdParams &P, const int16_t *list,
   }
   it.t = skip;
 }
-__device__ __forceinline__ void q_next(const BwdParams &P, const int16_t *list, int mode, int n_windows, QIter &it) {
+__device__ __forceinline__ void q_next(const BwdParams &P, const int *list, int mode, int n_windows, QIter &it) {
   if (++it.t < it.ntiles) return;
   it.t = 0;
   if (++it.li < n_windows) q_load(P, list, mode, it);
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
   using L = Smem<MODE>;
   constexpr int kSlots = L::slots;
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + L::ctrl);
-  int16_t *list = reinterpret_cast<int16_t *>(smem + L::list);
+  int *list = reinterpret_cast<int *>(smem + L::list);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (DIFF && MODE != kDkvWindow) ptx::grid_launch_dependents();
   // What follows the dq pass needs the long pass's sums: one CTA of it ends after them.
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
     // The query windows that see key tile (w, tile_idx): w itself, then every window
     // that routed to w, in ascending id (ordered ballot compaction: a fixed order).
     int n = 1;
-    if (lane == 0) list[0] = int16_t(w);
+    if (lane == 0) list[0] = w;
     for (int w0 = 0; P.routed_k > 0 && w0 < P.g.nWin; w0 += 32) {
       const int x = w0 + lane;
       bool hit = false;
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
         for (int i = 0; i < P.routed_k; ++i) hit |= r[i] == w;
       }
       const uint32_t m = __ballot_sync(0xFFFFFFFFu, hit);
-      if (hit) list[n + __popc(m & ((1u << lane) - 1u))] = int16_t(x);
+      if (hit) list[n + __popc(m & ((1u << lane) - 1u))] = x;
       n += __popc(m);
     }
     __syncwarp();
