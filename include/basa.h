@@ -210,7 +210,9 @@ basa_status basa_pool_route(const void *q, const void *k, const void *v,
  * cores in bfloat16 and the output is rounded once to bfloat16.
  * kp, vp must be NULL iff the pool patch is all zero; route_idx must be NULL
  * iff routed_k == 0. Route ids must lie in [0, nWin); the kernel checks them and
- * reports one outside (BASA_DEVERR_BAD_ROUTE in *dev_err, see there).
+ * reports one outside (BASA_DEVERR_BAD_ROUTE in *dev_err, see there). An id may be
+ * repeated and may be the query's own window: its tokens are then keys as often as they
+ * are listed, here and in the gradients.
  * bfloat16 requires head_dim == 128; float32 supports 64 and 128.
  */
 basa_status basa_window_attn_fwd(const void *q, const void *k, const void *v,
@@ -278,7 +280,7 @@ basa_status basa_text_attn_fwd(const void *q_text, const void *k, const void *v,
  *    gradients of the pooled and text keys and the pooled keys' gradients. Every
  *    sum has a fixed order and nothing is accumulated atomically: the results are
  *    identical run to run. P and dS are rounded to bfloat16 before the tensor-core
- *    products, each output once at the end. With routing, nWin <= 4096.
+ *    products, each output once at the end. nWin <= 4096 with routing, 2^27 without.
  *    BASA_ERR_UNSUPPORTED when the window tiling exceeds the kernel's limits.
  *  - BASA_F32: CUDA cores, 16-byte aligned workspace for the pooled keys'
  *    gradients (NULL when that is 0); dk, dv are accumulated with atomic adds, so

@@ -54,6 +54,12 @@ basa_status check_common(const basa_params *p) {
 
 bool has_pool(const basa_params *p) { return p->pt > 0; }
 
+// More windows than the bfloat16 backward's lists of them take.
+bool too_many_windows(const basa_params *p) {
+  const int64_t n = int64_t(p->T / p->wt) * (p->H / p->wh) * (p->W / p->ww);
+  return p->dtype == BASA_BF16 && n > (p->routed_k > 0 ? basa::kMaxBwdRouted : basa::kMaxBwdWindows);
+}
+
 bool aligned_element(const void *x, const basa_params *p) {
   return (reinterpret_cast<uintptr_t>(x) & (p->dtype == BASA_BF16 ? 1u : 3u)) == 0;
 }
@@ -327,8 +333,7 @@ basa_status basa_window_attn_bwd(const void *q, const void *k, const void *v, co
   basa_status st = check_common(p);
   if (st != BASA_OK) return st;
   if (p->head_dim != 128) return BASA_ERR_UNSUPPORTED;
-  if (p->dtype == BASA_BF16 && p->routed_k > 0 && int64_t(p->T / p->wt) * (p->H / p->wh) * (p->W / p->ww) > 4096)
-    return BASA_ERR_UNSUPPORTED;
+  if (too_many_windows(p)) return BASA_ERR_UNSUPPORTED;
   if (empty_batch(p)) return BASA_OK;
   if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv) return BASA_ERR_INVALID_ARG;
   if (has_pool(p) != (kp != nullptr) || has_pool(p) != (vp != nullptr)) return BASA_ERR_INVALID_ARG;
@@ -424,8 +429,7 @@ basa_status basa_diff_attn_bwd(const void *q, const void *k, const void *v, cons
                                void *dweight, void *workspace, const basa_params *p, basa_stream_t stream) {
   basa_status st = check_diff(dp, p);
   if (st != BASA_OK) return st;
-  if (p->dtype == BASA_BF16 && p->routed_k > 0 && int64_t(p->T / p->wt) * (p->H / p->wh) * (p->W / p->ww) > 4096)
-    return BASA_ERR_UNSUPPORTED;
+  if (too_many_windows(p)) return BASA_ERR_UNSUPPORTED;
   if (empty_batch(p)) return p->heads > 0 || dp->weight ? BASA_ERR_INVALID_ARG : BASA_OK;
   if ((st = check_diff_inputs(q, k, v, kp, vp, route_idx, dp, p)) != BASA_OK) return st;
   for (const void *x : {pre, second, static_cast<const void *>(lse), dout, static_cast<const void *>(dq),

@@ -24,9 +24,10 @@
 //   reduce       chunks summed in order: pooled-key gradients (float32, for the
 //                spread) and the text rows of dk, dv.
 //   dK/dV window one CTA per (b*head, window u, key tile of u): the query tiles of
-//                u and of every window that routed to u (ascending window id), same
-//                MMAs; the epilogue adds the pooled-key gradient of each token's
-//                patch / |patch| and stores dk, dv at the tokens' positions.
+//                u and of every window that routed to u (ascending window id; as often
+//                as its key list holds u), same MMAs; the epilogue adds the pooled-key
+//                gradient of each token's patch / |patch| and stores dk, dv at the
+//                tokens' positions.
 //
 // Differential form (template argument DIFF; out = O1 - lambda O2 of two maps that share
 // their values, the norm's gradient g taken beforehand and D per map in the records): the
@@ -81,7 +82,9 @@ constexpr uint32_t kSmemRow = 0;                            // the two row tiles
 constexpr uint32_t kSmemRing = 2 * kTileBytes;              // then a ring of 32 KB tiles
 constexpr uint32_t kRecBytes = kTileRows * 16;              // 128 records of 16 bytes
 constexpr uint32_t kCtrlBytes = 1024;
-constexpr int kMaxList = 4096;                              // windows whose query tiles one key tile sees (with routing)
+constexpr int kMaxList = kMaxBwdRouted;                     // windows whose query tiles one key tile sees (with routing)
+constexpr int kIdBits = 27;                                 // of a list entry
+static_assert(kMaxBwdWindows == 1 << kIdBits, "window ids in a list entry");
 constexpr uint32_t kTmemCols = 512;
 
 constexpr uint32_t kColRecBytes = 8 * 128 * 4;             // per compute warp: 64 x {-L log2 e}, 64 x {-D}
@@ -198,17 +201,27 @@ __device__ __forceinline__ void key_mask(const BwdParams &P, const Ctrl &c, cons
 
 // ------------------------------------------------------------- dK/dV passes: the query stream
 // Window list entry li (window mode: the smem list; long mode: window li itself) and
-// tile t of it.
+// tile t of it. An entry is a window's id and, above it, how many times more than once its
+// key list holds the key tile's window (a route may be repeated, and name its own window):
+// its tiles are streamed as often.
 struct QIter {
-  int li, t, ntiles, type, org[3];
+  int li, t, ntiles, type, org[3], more;
 };
-__device__ __forceinline__ void q_load(const BwdParams &P, const int *list, int mode, QIter &it) {
-  const int w = mode == kDkvLong ? it.li : list[it.li];
+static_assert(kMaxRouted < 1 << (32 - kIdBits), "a window may list itself kMaxRouted times more");
+__device__ __forceinline__ int entry_window(uint32_t e) { return int(e & ((1u << kIdBits) - 1u)); }
+__device__ __forceinline__ int entry_more(uint32_t e) { return int(e >> kIdBits); }
+__device__ __forceinline__ void q_load(const BwdParams &P, const uint32_t *list, int mode, QIter &it) {
+  int w = it.li;
+  if (mode == kDkvWindow) {
+    const uint32_t e = list[it.li];
+    it.more = entry_more(e);
+    w = entry_window(e);
+  }
   window_origin(P.g, w, &it.org[0], &it.org[1], &it.org[2], &it.type);
   it.ntiles = P.plan.type[it.type].n_tiles;
 }
 // Positions the iterator at global query tile `skip` of the window sequence.
-__device__ __forceinline__ void q_first(const BwdParams &P, const int *list, int mode, int skip, QIter &it) {
+__device__ __forceinline__ void q_first(const BwdParams &P, const uint32_t *list, int mode, int skip, QIter &it) {
   it.li = 0;
   it.t = 0;
   q_load(P, list, mode, it);
@@ -219,9 +232,10 @@ __device__ __forceinline__ void q_first(const BwdParams &P, const int *list, int
   }
   it.t = skip;
 }
-__device__ __forceinline__ void q_next(const BwdParams &P, const int *list, int mode, int n_windows, QIter &it) {
+__device__ __forceinline__ void q_next(const BwdParams &P, const uint32_t *list, int mode, int n_windows, QIter &it) {
   if (++it.t < it.ntiles) return;
   it.t = 0;
+  if (mode == kDkvWindow && --it.more >= 0) return;
   if (++it.li < n_windows) q_load(P, list, mode, it);
 }
 __device__ __forceinline__ const PlanTile &q_tile(const BwdParams &P, const QIter &it) {
@@ -307,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
   using L = Smem<MODE>;
   constexpr int kSlots = L::slots;
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + L::ctrl);
-  int *list = reinterpret_cast<int *>(smem + L::list);
+  uint32_t *list = reinterpret_cast<uint32_t *>(smem + L::list);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (DIFF && MODE != kDkvWindow) ptx::grid_launch_dependents();
   // What follows the dq pass needs the long pass's sums: one CTA of it ends after them.
@@ -380,26 +394,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_bf16_kernel(const __grid
   }
   if (MODE == kDkvWindow && warp == 0) {
     // The query windows that see key tile (w, tile_idx): w itself, then every window
-    // that routed to w, in ascending id (ordered ballot compaction: a fixed order).
+    // that routed to w, in ascending id (ordered ballot compaction: a fixed order). A
+    // route out of range stands for its window itself, as in the forward.
     int n = 1;
-    if (lane == 0) list[0] = w;
+    if (lane == 0 && P.routed_k == 0) list[0] = uint32_t(w);
     for (int w0 = 0; P.routed_k > 0 && w0 < P.g.nWin; w0 += 32) {
       const int x = w0 + lane;
-      bool hit = false;
-      if (x < P.g.nWin && x != w) {
+      int hits = 0;
+      if (x < P.g.nWin) {
         const int32_t *r = P.route + ((long long)bh * P.g.nWin + x) * P.routed_k;
-        for (int i = 0; i < P.routed_k; ++i) hit |= r[i] == w;
+        for (int i = 0; i < P.routed_k; ++i) hits += r[i] == w || (x == w && uint32_t(r[i]) >= uint32_t(P.g.nWin));
+        if (x == w) {
+          list[0] = uint32_t(w) | uint32_t(hits) << kIdBits;
+          hits = 0;
+        }
       }
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, hit);
-      if (hit) list[n + __popc(m & ((1u << lane) - 1u))] = x;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, hits > 0);
+      if (hits > 0) list[n + __popc(m & ((1u << lane) - 1u))] = uint32_t(x) | uint32_t(hits - 1) << kIdBits;
       n += __popc(m);
     }
     __syncwarp();
     int cols = 0;
     for (int i = lane; i < n; i += 32) {
       int a, b, d, t;
-      window_origin(P.g, list[i], &a, &b, &d, &t);
-      cols += P.plan.type[t].n_tiles;
+      window_origin(P.g, entry_window(list[i]), &a, &b, &d, &t);
+      cols += P.plan.type[t].n_tiles * (1 + entry_more(list[i]));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) cols += __shfl_xor_sync(0xFFFFFFFFu, cols, o);
@@ -1149,7 +1168,7 @@ basa_status bwd_params(BwdParams &P, BwdLayout &L, const void *q, const void *k,
   if (st != BASA_OK) return st;
   L = bwd_layout(p, P.plan, maps);
   P.g = make_geo(p);
-  if (p.routed_k > 0 && P.g.nWin > kMaxList) return BASA_ERR_UNSUPPORTED;
+  if (P.g.nWin > (p.routed_k > 0 ? kMaxBwdRouted : kMaxBwdWindows)) return BASA_ERR_UNSUPPORTED;
   const long long N = P.g.N, kv_rows = N + p.n_text, bh = (long long)p.B * p.heads;
   basa_params pm = p;
   pm.heads = p.heads * maps;

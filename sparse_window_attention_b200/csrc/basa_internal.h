@@ -31,6 +31,8 @@ constexpr int kMaxShapes = 8;
 constexpr int kMaxPieces = 1024;
 constexpr int kMaxTiles = 512;
 constexpr int kMaxRouted = 16;
+// Most windows of the bfloat16 backward, with routes and without.
+constexpr int kMaxBwdRouted = 4096, kMaxBwdWindows = 1 << 27;
 
 struct PlanShape {
   int16_t ct, cy, cx, rows;  // box extents in t, y, x and their product

@@ -401,3 +401,13 @@ def test_diff_text_checks():
     assert call(_p(B=0), q=None) == 0
     assert B.basa_diff_text_attn_workspace_bytes(_p(n_text=0)) == 0
     assert B.basa_diff_text_attn_workspace_bytes(_p(dtype="f32")) == 0
+
+
+def test_backward_window_limits():
+    """The bfloat16 backward names windows in 27 bits, and lists 4096 of them with routes."""
+    plain = [FAKE] * 3 + [None] * 3 + [FAKE] * 7
+    diff = [FAKE] * 3 + [None] * 3 + [_diff()] + [FAKE] * 10
+    for grid, kw in (((1, 8192, 16385), {}), ((1, 64, 65), dict(routed_k=1))):
+        p = _p(grid=grid, window=(1, 1, 1), shift=(0, 0, 0), pool=(0, 0, 0), **kw)
+        assert B.basa_window_attn_bwd(*plain, p, stream=0, check=False) == 3
+        assert B.basa_diff_attn_bwd(*diff, p, stream=0, check=False) == 3
