@@ -9,12 +9,15 @@
 //             D2 = g . O2,  D1 = g . O1 = g . a + lambda D2,  dlambda = -sum g . O2;
 //           the maps' outputs are rounded here, so D is a little off the rows' true sum
 //           R = sum_j P dP. The dq pass, which has P in float32, finds by how much: sum_j dS
-//           = R - D. And where a stands in for the true one, g is orthogonal to a up to eps
-//           (g . a = mean(G w xh) d eps r^2) but not to the true one, R1 - lambda R2, so with
-//           c = O2 . a / a . a what is summed is
+//           = R - D. And where a stands in for the true one, g . a is known (mean(G w xh) d
+//           eps r^2), but with the true one, R1 - lambda R2, it is something else, so with
+//           c = O2 . a / (a . a + d eps) what is summed is
 //             g . O2 - c (g . a) + c mean(G w xh) d eps r^2  +  (1 + c lambda) dR2 - c dR1
-//           (dR of the dq pass, weighted by the records). Maps that are nearly alike would
-//           otherwise leave dlambda 5% off, and a sum over rows that cancels 2%;
+//           (dR of the dq pass, weighted by the records). This c takes out what a's error e
+//           does to g . O2 through mean(G w e): r^3 / d (a . O2) (G w . e), as r^2 = d / (a . a
+//           + d eps). Maps that are nearly alike would otherwise leave dlambda 5% off, and a sum
+//           over rows that cancels 2%. (Without d eps, c grows without bound where a is small
+//           against sqrt(eps), where g hardly depends on a, and dlambda is up to half off.)
 //           g goes on as the output gradient of both maps (map 2's factor -lambda is put
 //           on its dq, dK and dV sums), D1 and D2 as their rows' softmax corrections.
 // reduce    the blocks' partial sums of dlambda and dweight, in a fixed order.
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kDiffThreads) diff_prep_kernel(const __grid_co
       }
       ss = row_sum<LPR>(ss);
       so = row_sum<LPR>(so);
-      c2 = ss > 0.f ? so / ss : 0.f;
+      c2 = so / fmaf(float(D), a.eps, ss);
       const float rms = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
