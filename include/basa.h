@@ -370,7 +370,11 @@ typedef struct {
  * and written head-major. Row r is row first_row + r of the key sequence: a grid token
  * in raster order below N = T*H*W, text row (first_row + r - N) from there on.
  * Strides are >= 0 and multiples of 16 bytes; those of x and dy may be 0 (broadcast), y
- * must not overlap itself. heads may differ between the tensors of a call. */
+ * must not overlap itself. heads may differ between the tensors of a call. What a call
+ * writes (y, dweight) must not overlap anything else that it reads or writes, except y on
+ * its own x or dy as said below. The tensors, weights and their gradients are checked: slices
+ * of one buffer that interleave without meeting are accepted, but where the strides of two
+ * tensors are so unlike that a few thousand steps do not decide, the call is refused. */
 typedef struct {
   const void *x;       /* forward: input. backward: the forward's input (unused without weight) */
   int64_t x_stride[3];

@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbasa.so")
 SOURCES = ["api.cpp", "plan.cpp", "pool_route.cu", "pool_route_fused.cu", "merge.cu", "rope.cu", "diff.cu", "attn_f32.cu", "attn_diff_f32.cu", "attn_bf16_sm100.cu", "attn_diff_bf16_sm100.cu", "attn_bwd_bf16_sm100.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("basa_internal.h", "sm100_ptx.cuh", "attn_sm100_common.cuh", "attn_fwd_sm100.cuh", "attn_f32.cuh")] + [os.path.join(ROOT, "include", "basa.h")]
+HEADERS = [os.path.join(CSRC, h) for h in ("basa_internal.h", "sm100_ptx.cuh", "attn_sm100_common.cuh", "attn_fwd_sm100.cuh", "attn_f32.cuh", "byte_views.h")] + [os.path.join(ROOT, "include", "basa.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

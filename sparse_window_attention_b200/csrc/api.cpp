@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "basa_internal.h"
+#include "byte_views.h"
 
 namespace {
 
@@ -133,6 +134,58 @@ bool rope_strides_ok(const int64_t *stride, const basa_rope_tensor &t, const bas
 
 bool same_strides(const int64_t *a, const int64_t *b) { return a[0] == b[0] && a[1] == b[1] && a[2] == b[2]; }
 
+using basa::ByteView;
+using basa::views_meet;
+
+ByteView rope_view(const void *base, const int64_t *stride, const basa_rope_tensor &t, const basa_params *p) {
+  const int64_t size = p->dtype == BASA_BF16 ? 2 : 4, ext[3] = {p->B, t.heads, t.rows};
+  ByteView v{reinterpret_cast<uintptr_t>(base), p->head_dim * size, {0, 0, 0}, {1, 1, 1}};
+  for (int a = 0; a < 3; ++a) {
+    if (ext[a] == 1) continue;
+    v.step[a] = stride[a] * size;
+    v.ext[a] = ext[a];
+  }
+  return v;
+}
+
+ByteView row_view(const void *base, const basa_params *p) {
+  return {reinterpret_cast<uintptr_t>(base), int64_t(p->head_dim) * (p->dtype == BASA_BF16 ? 2 : 4), {0, 0, 0}, {1, 1, 1}};
+}
+
+// Nothing that a call writes is anything else that it reads or writes; a tensor may be
+// rewritten in place, element by element. Written out over the views that there are, most of
+// which are apart as a whole: a call of one token is bound by its checks.
+bool rope_disjoint(int n, const basa_rope_tensor *t, bool bwd, const basa_params *p) {
+  struct Used {
+    ByteView v;
+    uintptr_t end;
+    int tensor;
+    bool written;
+    const int64_t *stride;
+  } u[5 * BASA_ROPE_MAX_TENSORS];
+  int m = 0;
+  const auto use = [&](const ByteView &v, int i, bool written, const int64_t *stride) {
+    u[m++] = {v, v.end(), i, written, stride};
+  };
+  for (int i = 0; i < n; ++i) {
+    const basa_rope_tensor &r = t[i];
+    if (bwd && r.dweight) use(row_view(r.dweight, p), i, true, nullptr);
+    if (rope_empty(r, p)) continue;
+    use(rope_view(r.y, r.y_stride, r, p), i, true, r.y_stride);
+    if (!bwd || r.weight) use(rope_view(r.x, r.x_stride, r, p), i, false, r.x_stride);
+    if (bwd) use(rope_view(r.dy, r.dy_stride, r, p), i, false, r.dy_stride);
+    if (r.weight) use(row_view(r.weight, p), i, false, nullptr);
+  }
+  for (int a = 0; a < m; ++a)
+    for (int b = 0; b < a; ++b) {
+      if (u[a].v.base >= u[b].end || u[b].v.base >= u[a].end || !(u[a].written || u[b].written)) continue;
+      const bool in_place = u[a].tensor == u[b].tensor && u[a].v.base == u[b].v.base && u[a].stride && u[b].stride &&
+                            same_strides(u[a].stride, u[b].stride);
+      if (!in_place && views_meet(u[a].v, u[b].v)) return false;
+    }
+  return true;
+}
+
 basa_status check_rope(int n, const basa_rope_tensor *t, const float *table, float eps, bool bwd,
                        const basa_rope_params *rp, const basa_params *p) {
   basa_status st = check_common(p);
@@ -148,24 +201,14 @@ basa_status check_rope(int n, const basa_rope_tensor *t, const float *table, flo
     if (int64_t(p->B) * u.heads >= (int64_t(1) << 31)) return BASA_ERR_UNSUPPORTED;
     if (u.weight && (!aligned16(u.weight) || !(eps > 0.f) || !std::isfinite(eps))) return BASA_ERR_INVALID_ARG;
     if (bwd && u.dweight && (!u.weight || !aligned16(u.dweight))) return BASA_ERR_INVALID_ARG;
-    for (int j = 0; j < i; ++j)
-      if (bwd && u.dweight && u.dweight == t[j].dweight) return BASA_ERR_INVALID_ARG;
     if (rope_empty(u, p)) continue;
     const bool reads_x = !bwd || u.weight;
     if (!u.y || !aligned16(u.y) || !rope_strides_ok(u.y_stride, u, p, true)) return BASA_ERR_INVALID_ARG;
     if (reads_x && (!u.x || !aligned16(u.x) || !rope_strides_ok(u.x_stride, u, p, false))) return BASA_ERR_INVALID_ARG;
     if (bwd && (!u.dy || !aligned16(u.dy) || !rope_strides_ok(u.dy_stride, u, p, false))) return BASA_ERR_INVALID_ARG;
     if (u.rotate && turns && (!table || !aligned16(table))) return BASA_ERR_INVALID_ARG;
-    // in place is element by element; a tensor never writes what another one reads or writes
-    if (reads_x && u.x == u.y && !same_strides(u.x_stride, u.y_stride)) return BASA_ERR_INVALID_ARG;
-    if (bwd && u.dy == u.y && !same_strides(u.dy_stride, u.y_stride)) return BASA_ERR_INVALID_ARG;
-    for (int j = 0; j < n; ++j) {
-      if (j == i || rope_empty(t[j], p)) continue;
-      if (t[j].y == u.y || ((!bwd || t[j].weight) && t[j].x == u.y) || (bwd && t[j].dy == u.y))
-        return BASA_ERR_INVALID_ARG;
-    }
   }
-  return BASA_OK;
+  return rope_disjoint(n, t, bwd, p) ? BASA_OK : BASA_ERR_INVALID_ARG;
 }
 
 }  // namespace
