@@ -1255,12 +1255,22 @@ basa_status launch_attn_bwd_bf16(const void *q, const void *k, const void *v, co
 }
 
 namespace {
-// Differential form: whether a long key tile's chunks are summed by its last CTA. That takes
-// it 1 to 2 us a chunk, which hides behind the dq pass's waves and costs where those are few:
-// a training step of 6 chunks and 2 waves took 211 us so and 218 us with kernels of their own,
-// one of 5 chunks and 1 wave 98 us so and 89 us with kernels of their own.
-bool last_cta_sums(const BwdLayout &L, long long dq_ctas) {
-  return L.n_long > 0 && L.n_chunks <= 2 + 2 * ((dq_ctas + kLongSms - 1) / kLongSms);
+// Differential form: whether a long key tile's chunks are summed by its last CTA. The sums
+// then take that CTA about a key step's time a chunk and more for its start, behind which the
+// dq pass's steps run and those of the window pass before its epilogue; where they are too few
+// a reduction of its own, by the whole GPU, is sooner done. Steps behind the sums, chunks, and
+// the backward's time with a reduction and with the last CTA, us (windows of 16 x 16 but for
+// the 6 x 18 x 26 grid's, each in units of v, grid, routes):
+//   12, 2:  68 / 70   (12, 32 x 32, 0)      8, 6:  70 / 82   (2, 48 x 64, 0)
+//   16, 2: 128 / 121  (24, 32 x 32, 0)     12, 6:  86 / 92   (6, 48 x 64, 0)
+//   46, 2: 267 / 254  (12, 64 x 64, 0)     20, 6: 122 / 109  (3, 6 x 18 x 26, 2)
+//   14, 3:  98 / 87   (4, 32 x 48, 1)      28, 6: 138 / 141  (6, 6 x 18 x 26, 2)
+//   25, 4: 169 / 156  (6, 64 x 64, 0)      18, 8:  94 / 96   (3, 64 x 64, 0)
+//   19, 15: 154 / 174 (3, 96 x 96, 0)      34, 8: 241 / 236  (6, 96 x 96, 0)
+bool last_cta_sums(const BwdLayout &L, const BwdParams &P, long long dq_ctas) {
+  const int seen = 1 + P.routed_k;  // windows of a key list
+  const long long dq = (dq_ctas + kLongSms - 1) / kLongSms * (P.max_tiles * seen + L.n_long);
+  return L.n_long > 0 && dq + 2 * P.max_tiles * seen >= 11 + L.n_chunks;
 }
 
 // Workspace: the layout of two maps, g (with a norm), the partial sums of dlambda and
@@ -1304,7 +1314,7 @@ basa_status launch_diff_attn_bwd_bf16(const void *q, const void *k, const void *
   st = bwd_params(P, L, q, k, v, kp, vp, route_idx, dp.weight ? ws + D.g : dout, dq, dk, dv, ws, p, 2);
   if (st != BASA_OK) return st;
   const long long bh = P.bh_count, window_blocks = bh * P.g.nWin * P.max_tiles;
-  const bool any_long = L.n_long > 0, last_sums = last_cta_sums(L, 2 * window_blocks);
+  const bool any_long = L.n_long > 0, last_sums = last_cta_sums(L, P, 2 * window_blocks);
   P.lambda = static_cast<const __nv_bfloat16 *>(dp.lambda);
   P.heads = p.heads;
   P.dk = static_cast<__nv_bfloat16 *>(dk);
