@@ -424,7 +424,9 @@ basa_status basa_rope_bwd(int n, const basa_rope_tensor *t, const float *table, 
 /* ------------------------------------------------------------------------------
  * Differential attention over the key lists of basa_window_attn_fwd.
  *
- * Head h has two softmax maps, 2h and 2h + 1, that share its values (and its routes):
+ * Head h has two softmax maps, 2h and 2h + 1, that share its values (and its routes). The
+ * values have the maps' width, head_dim, and the norm spans head_dim (a head whose values are
+ * twice as wide as its maps is not of this form: its norm would span both halves):
  *   O1 = softmax(q[2h] K[2h]^T / sqrt(d)) V[h],   O2 = softmax(q[2h+1] K[2h+1]^T / sqrt(d)) V[h]
  *   a = O1 - lambda[h] O2
  *   out = gain * weight * a * rsqrt(mean(a^2) + eps)      (mean over head_dim)

@@ -38,19 +38,18 @@
 // maps' dV meet without a buffer or an atomic. (Both maps at once, sharing dout V^T, would
 // take six 128-column accumulators and TMEM holds four.) The passes overlap at their ends by
 // programmatic dependent launch: the long pass runs first, on fewer CTAs than there are SMs
-// as often as not, and the dq pass, which needs nothing of it, fills the rest. With few chunks
-// the last CTA of a long key tile to finish sums them itself (in their order), so the window
-// pass starts as the dq pass drains and waits for both before its epilogue; lambda's and the
-// weight's sums run under its end. With many chunks one CTA would sum them for longer than
-// the dq pass hides, and the reduction is a launch of its own, under which the window pass
-// starts.
+// as often as not, and the dq pass, which needs nothing of it, fills the rest. The chunks of a
+// long key tile are summed (in their order) by the last CTA of it to finish, so that the window
+// pass starts as the dq pass drains and waits for both before its epilogue, with lambda's and
+// the weight's sums under its end; or, where too little runs beside that CTA to hide it, by a
+// reduction of its own, under which the window pass starts (last_cta_sums).
 //
-// Roundings, as in the other form: P and dS to bfloat16 for the products that sum them (2^-9
+// Roundings, as in the other form: P and dS to bfloat16 for the products that sum them (2^-8
 // of each element at most), so dq, dk and dv are off 0.003 of their size where their own
-// rounding is 0.0017. Measured, forward and backward: 12 heads, 64 x 64, 16 x 16 windows, 832
+// rounding is 0.0017. Measured, forward and backward, a replayed graph: 12 heads, 64 x 64, 16 x 16 windows, 832
 // keys 336 us (18 products of 2 d FLOP a query and key where 12 would do, as the scores and
 // dout V^T are taken again in the dK/dV passes, the latter per map); 2 x 3 heads,
-// 6 x 18 x 26, 234-token windows, 2 routed 200 us. What bounds them: in the dq and long passes
+// 6 x 18 x 26, 234-token windows, 2 routed 203 us. What bounds them: in the dq and long passes
 // the chain score, P, dS of each tile (tensor cores active 30% of the time), in the window pass
 // a CTA's start and end around its few query tiles (15%).
 //

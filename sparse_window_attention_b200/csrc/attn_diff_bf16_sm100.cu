@@ -19,13 +19,14 @@
 // a key step (14 steps at 32 x 32 windows, 7 at 16 x 16).
 //
 // What bounds it: the softmax's chain (scores read, maximum, exponentials, P stored), about
-// 3.5k cycles a key step where the four products take 2.1k. Measured at 12 heads (24 maps):
-// a 128 x 128 grid, 32 x 32 windows, 1280 + 512 keys 355 us, 0.62 of the tensor cores' measured
-// rate; 64 x 64, 16 x 16 windows, 832 keys 65 us (0.39: 384 items are three rounds of 148 for
-// the work of 2.6); 21 x 30 x 52, 6 heads, 234-token windows, 4 routed 369 us (0.44: 117-row
-// tiles).
+// 3.5k cycles a key step where the four products take 2.1k. Measured at 12 heads (24 maps),
+// a graph of ten calls replayed (calls one by one from Python in brackets): a 128 x 128 grid,
+// 32 x 32 windows, 1280 + 512 keys 357 us, 0.62 of the tensor cores' measured rate (385, 0.58,
+// as a long run meets the power cap); 64 x 64, 16 x 16 windows, 832 keys 66 us (68), 0.39, as 384
+// items are three rounds of 148 for the work of 2.6; 21 x 30 x 52, 6 heads, 234-token windows, 4
+// routed 369 us (373), 0.44: 117-row tiles.
 //
-// Roundings: P to bfloat16 for the products with V, at most 2^-9 of each, while the sums it is
+// Roundings: P to bfloat16 for the products with V, at most 2^-8 of each, while the sums it is
 // divided by take it in float32: outputs are off 0.002 of their size, of which their own
 // rounding is 0.0017.
 //

@@ -162,6 +162,10 @@ basa_status launch_attn_text_f32(const void *q_text, const void *k, const void *
 // the softmax derivative: with P = softmax(S), S = q K^T / sqrt(d) and the saved
 // log-sum-exp L (p = exp(s - L)), D_i = dO_i . O_i:
 //   dS = P (dO V^T - D),  dq = dS K / sqrt(d),  dK += dS^T q / sqrt(d),  dV += P^T dO.
+// Differential form: D comes from the backward's start, odd maps count -lambda, and each map
+// goes by itself. Bound by its shuffles and shared-memory and global atomics, a sum a key and
+// channel for each warp: 390 us at 2 differential heads of 64, 16 windows of 64 tokens, 128 keys
+// (0.3 GFLOP), 2.47 ms at 4 of 128, 4 windows of 256 tokens, 397 keys (3.3 GFLOP).
 // Routing is a selection and gets no gradient; pooled keys collect their gradient
 // in dkp, dvp, which a second kernel spreads over the tokens of each patch.
 namespace {

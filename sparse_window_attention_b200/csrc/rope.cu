@@ -442,8 +442,11 @@ void run_rope(const RopeArgs &a, bool bwd, bool halves, unsigned blocks, cudaStr
 }
 
 // Blocks of a tensor list: rows in blocks of 256 threads, and the (batch, head) units
-// in as many groups as it takes to give the GPU about kTargetBlocks blocks (8 resident
-// blocks on each of 148 SMs). Depends on the shapes only, so the order of the weight
+// in as many groups as it takes to give the GPU about kTargetBlocks blocks: 8 for each of
+// 148 SMs, where 3 (backward: 2) run at a time, so that the last ones leave an SM idle for a
+// small part of the whole, and a block still walks enough units for its cos and sin. Twice as
+// many took 107 us at 24 heads of 16384 + 512 rows and 34 at 4096 + 512, four times as many
+// 104 and 37; this many 107 and 32. Depends on the shapes only, so the order of the weight
 // gradients' sums does too. Returns the block count (< 0: too many).
 constexpr long long kTargetBlocks = 8 * 148;
 bool has_rows(const basa_rope_tensor &t, const basa_params &p) { return p.B > 0 && t.heads > 0 && t.rows > 0; }

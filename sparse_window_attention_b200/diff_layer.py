@@ -19,8 +19,9 @@ class BasaDiffLayer:
     q [batch, 2 heads, N, head_dim]; k [batch, 2 heads, N + n_text, head_dim];
     v [batch, heads, N + n_text, head_dim]; ``lam`` [heads] the second maps' weights;
     ``weight`` [head_dim] (None: no norm) of the RMS norm of each head's rows, times
-    ``gain``. All tensors are contiguous. Pooled keys and values and routed windows are taken from ``kp``, ``vp``,
-    ``route_idx`` where given and computed otherwise (``pool_kv``, ``route``).
+    ``gain``. Values and maps have the same width, ``head_dim``, which the norm spans. All
+    tensors are contiguous. Pooled keys and values and routed windows are taken from ``kp``,
+    ``vp``, ``route_idx`` where given and computed otherwise (``pool_kv``, ``route``).
     """
 
     def __init__(self, batch, heads, head_dim, grid, window, pool=(0, 0, 0), n_text=0, routed_k=0, dtype="bf16",
