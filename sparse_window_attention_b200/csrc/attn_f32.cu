@@ -164,8 +164,8 @@ basa_status launch_attn_text_f32(const void *q_text, const void *k, const void *
 //   dS = P (dO V^T - D),  dq = dS K / sqrt(d),  dK += dS^T q / sqrt(d),  dV += P^T dO.
 // Differential form: D comes from the backward's start, odd maps count -lambda, and each map
 // goes by itself. Bound by its shuffles and shared-memory and global atomics, a sum a key and
-// channel for each warp: 390 us at 2 differential heads of 64, 16 windows of 64 tokens, 128 keys
-// (0.3 GFLOP), 2.47 ms at 4 of 128, 4 windows of 256 tokens, 397 keys (3.3 GFLOP).
+// channel for each warp: 387 us at 2 differential heads of 64, 16 windows of 64 tokens, 128 keys
+// (0.3 GFLOP), 2.46 ms at 4 of 128, 4 windows of 256 tokens, 397 keys (3.3 GFLOP).
 // Routing is a selection and gets no gradient; pooled keys collect their gradient
 // in dkp, dvp, which a second kernel spreads over the tokens of each patch.
 namespace {
@@ -206,7 +206,7 @@ __device__ __forceinline__ long long key_dest(const F32Args &a, long long bh, co
   return bh * rows + a.g.N + j;
 }
 
-template <int D>
+template <int D, bool DIFF>
 __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
   const F32Args &a = b.f;
   constexpr int C = D / kBwdTPQ, QPB = kBwdThreads / kBwdTPQ;
@@ -215,10 +215,10 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
   __shared__ int wins[1 + kMaxRouted];
   const int chunk = blockIdx.x % a.q_chunks;
   const int w = (blockIdx.x / a.q_chunks) % a.g.nWin;
-  const long long bh = blockIdx.x / (a.q_chunks * a.g.nWin);
+  const long long bh = blockIdx.x / (a.q_chunks * a.g.nWin), bh_v = DIFF ? bh >> 1 : bh;  // maps; units of v
   if (threadIdx.x == 0) wins[0] = w;
   if (threadIdx.x > 0 && threadIdx.x <= a.routed_k)
-    wins[threadIdx.x] = checked_route(a, a.route[((bh >> a.v_shift) * a.g.nWin + w) * a.routed_k + threadIdx.x - 1], w);
+    wins[threadIdx.x] = checked_route(a, a.route[(bh_v * a.g.nWin + w) * a.routed_k + threadIdx.x - 1], w);
   __syncthreads();
   const int part = threadIdx.x % kBwdTPQ;  // columns part, part + TPQ, ...
   const int lq = chunk * QPB + threadIdx.x / kBwdTPQ;
@@ -230,9 +230,9 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
     const int lt = lq / (a.g.wh * a.g.ww), ly = (lq / a.g.ww) % a.g.wh, lx = lq % a.g.ww;
     qtok = ((long long)((ot + lt) % a.g.T) * a.g.H + (oy + ly) % a.g.H) * a.g.W + (ox + lx) % a.g.W;
   }
-  const long long qrow = bh * a.g.N + qtok, grow = (bh >> a.v_shift) * a.g.N + qtok;
+  const long long qrow = bh * a.g.N + qtok, grow = bh_v * a.g.N + qtok;
   // what this map's dq, dK and dV are multiplied by
-  const float factor = b.lambda && (bh & 1) ? -b.lambda[(bh >> 1) % (a.heads >> 1)] : 1.f;
+  const float factor = DIFF && (bh & 1) ? -b.lambda[bh_v % (a.heads >> 1)] : 1.f;
   float q[C], dout[C], dq[C];
   float Dpart = 0.f;
 #pragma unroll
@@ -240,13 +240,13 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
     const int col = i * kBwdTPQ + part;
     q[i] = active ? a.q[qrow * D + col] : 0.f;
     dout[i] = active ? b.dout[grow * D + col] : 0.f;
-    if (!b.drow) Dpart = fmaf(dout[i], active ? b.out[qrow * D + col] : 0.f, Dpart);
+    if (!DIFF) Dpart = fmaf(dout[i], active ? b.out[qrow * D + col] : 0.f, Dpart);
     dq[i] = 0.f;
   }
   // the TPQ threads of a query are adjacent lanes
   float Drow = Dpart + __shfl_xor_sync(0xffffffffu, Dpart, 1);
   Drow += __shfl_xor_sync(0xffffffffu, Drow, 2);
-  if (b.drow) Drow = active ? b.drow[qrow] : 0.f;
+  if (DIFF) Drow = active ? b.drow[qrow] : 0.f;
   const float L = active ? b.lse[qrow] : 0.f;
   const int nk = a.n_vis_keys + a.n_pool_keys + a.n_text_keys;
   for (int k0 = 0; k0 < nk; k0 += kBwdKeyTile) {
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
       float4 kv4 = make_float4(0.f, 0.f, 0.f, 0.f), vv4 = kv4;
       if (k0 + r < nk) {
         kv4 = reinterpret_cast<const float4 *>(key_row(a, a.k, a.kp, bh, wins, k0 + r))[c4];
-        vv4 = reinterpret_cast<const float4 *>(key_row(a, a.v, a.vp, bh >> a.v_shift, wins, k0 + r))[c4];
+        vv4 = reinterpret_cast<const float4 *>(key_row(a, a.v, a.vp, bh_v, wins, k0 + r))[c4];
       }
       reinterpret_cast<float4 *>(&ks[r][0])[c4] = kv4;
       reinterpret_cast<float4 *>(&vs[r][0])[c4] = vv4;
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
       const float ds = p * (dpp - Drow);
       // the 8 queries of a warp add to the same key row: sum them with shuffles
       // (lanes l, l ^ 4, l ^ 8, l ^ 16 share a column) and let 4 lanes add to shared memory
-      const float dsq = active ? ds * a.scale * factor : 0.f, pa = active ? p * factor : 0.f;
+      const float dsq = active ? ds * (DIFF ? a.scale * factor : a.scale) : 0.f, pa = active ? (DIFF ? p * factor : p) : 0.f;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const int col = i * kBwdTPQ + part;
@@ -304,22 +304,26 @@ __global__ void __launch_bounds__(kBwdThreads) attn_bwd_f32_kernel(BwdArgs b) {
       if (k0 + r >= nk) continue;
       bool pooled;
       const long long dst = key_dest(a, bh, wins, k0 + r, &pooled);
-      const long long dst_v = a.v_shift ? key_dest(a, bh >> a.v_shift, wins, k0 + r, &pooled) : dst;
+      const long long dst_v = DIFF ? key_dest(a, bh_v, wins, k0 + r, &pooled) : dst;
       atomicAdd((pooled ? b.dkp : b.dk) + dst * D + col, dks[r][col]);
       atomicAdd((pooled ? b.dvp : b.dv) + dst_v * D + col, dvs[r][col]);
     }
   }
   if (active) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) b.dq[qrow * D + i * kBwdTPQ + part] = dq[i] * (a.scale * factor);
+    for (int i = 0; i < C; ++i) b.dq[qrow * D + i * kBwdTPQ + part] = dq[i] * (DIFF ? a.scale * factor : a.scale);
   }
 }
 
-// dx (dk or dv) of every visual token += dxp of its pool patch / |patch|.
-__global__ void __launch_bounds__(256) pool_bwd_kernel(const float *dxp, float *dx, Geo g, int pt, int ph, int pw,
-                                                       int n_pool, int n_text, int d, long long total, float inv) {
+// dk and dv (blockIdx.y) of every visual token += dkp, dvp of its pool patch / |patch|.
+__global__ void __launch_bounds__(256) pool_bwd_kernel(const float *dkp, const float *dvp, float *dk, float *dv, Geo g,
+                                                       int pt, int ph, int pw, int n_pool, int n_text, int d,
+                                                       long long total_k, long long total_v, float inv) {
+  const bool is_v = blockIdx.y == 1;
+  const float *dxp = is_v ? dvp : dkp;
+  float *dx = is_v ? dv : dk;
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;  // (bh, token, float4 column)
-  if (i >= total) return;
+  if (i >= (is_v ? total_v : total_k)) return;
   const int d4 = d / 4;
   const int c4 = int(i % d4);
   const long long tok = (i / d4) % g.N, bh = i / (d4 * (long long)g.N);
@@ -336,11 +340,11 @@ __global__ void __launch_bounds__(256) pool_bwd_kernel(const float *dxp, float *
 
 namespace {
 
-// The backward over `maps` = p.heads x B units whose values are shared in groups of
-// 2^v_shift; `pooled` holds the pooled keys' gradients, then the pooled values'.
+// The backward over p.heads x B maps, in the differential form with values for each two of
+// them; `pooled` holds the pooled keys' gradients, then the pooled values'.
 basa_status run_attn_bwd_f32(BwdArgs b, const void *q, const void *k, const void *v, const void *kp, const void *vp,
                              const int32_t *route_idx, void *dq, void *dk, void *dv, float *pooled,
-                             const basa_params &p, int v_shift, cudaStream_t s) {
+                             const basa_params &p, bool diff, cudaStream_t s) {
   F32Args &a = b.f;
   a.q = static_cast<const float *>(q);
   a.k = static_cast<const float *>(k);
@@ -359,13 +363,12 @@ basa_status run_attn_bwd_f32(BwdArgs b, const void *q, const void *k, const void
   a.n_vis_keys = a.win_tok * (1 + a.routed_k);
   a.n_pool_keys = a.n_pool;
   a.n_text_keys = p.n_text;
-  a.v_shift = v_shift;
   a.q_chunks = (a.win_tok + kBwdThreads / kBwdTPQ - 1) / (kBwdThreads / kBwdTPQ);
   a.scale = 1.0f / sqrtf(float(p.head_dim));
   b.dq = static_cast<float *>(dq);
   b.dk = static_cast<float *>(dk);
   b.dv = static_cast<float *>(dv);
-  const size_t bh = size_t(p.B) * p.heads, bh_v = bh >> v_shift;
+  const size_t bh = size_t(p.B) * p.heads, bh_v = diff ? bh / 2 : bh;
   b.dkp = pooled;
   b.dvp = b.dkp + bh * a.n_pool * p.head_dim;
   const size_t unit_bytes = (size_t(a.g.N) + p.n_text) * p.head_dim * sizeof(float);
@@ -377,14 +380,15 @@ basa_status run_attn_bwd_f32(BwdArgs b, const void *q, const void *k, const void
     return BASA_ERR_CUDA;
   const long long blocks = (long long)bh * a.g.nWin * a.q_chunks;
   if (blocks >= (1ll << 31)) return BASA_ERR_UNSUPPORTED;
-  if (p.head_dim == 64) attn_bwd_f32_kernel<64><<<unsigned(blocks), kBwdThreads, 0, s>>>(b);
-  else attn_bwd_f32_kernel<128><<<unsigned(blocks), kBwdThreads, 0, s>>>(b);
+  const auto kernel = !diff ? attn_bwd_f32_kernel<128, false> : p.head_dim == 64 ? attn_bwd_f32_kernel<64, true> : attn_bwd_f32_kernel<128, true>;
+  kernel<<<unsigned(blocks), kBwdThreads, 0, s>>>(b);
   if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
-  for (int i = 0; a.n_pool > 0 && i < 2; ++i) {
-    const long long total = (long long)(i ? bh_v : bh) * a.g.N * (p.head_dim / 4);
-    pool_bwd_kernel<<<unsigned((total + 255) / 256), 256, 0, s>>>(i ? b.dvp : b.dkp, i ? b.dv : b.dk, a.g, p.pt, p.ph,
-                                                                 p.pw, a.n_pool, p.n_text, p.head_dim, total,
-                                                                 1.0f / float(p.pt * p.ph * p.pw));
+  if (a.n_pool > 0) {
+    const long long unit = (long long)a.g.N * (p.head_dim / 4), total = (long long)bh * unit;
+    pool_bwd_kernel<<<dim3(unsigned((total + 255) / 256), 2), 256, 0, s>>>(b.dkp, b.dvp, b.dk, b.dv, a.g, p.pt, p.ph, p.pw,
+                                                                          a.n_pool, p.n_text, p.head_dim, total,
+                                                                          (long long)bh_v * unit,
+                                                                          1.0f / float(p.pt * p.ph * p.pw));
     if (cudaGetLastError() != cudaSuccess) return BASA_ERR_CUDA;
   }
   return BASA_OK;
@@ -406,7 +410,7 @@ basa_status launch_attn_bwd_f32(const void *q, const void *k, const void *v, con
   b.out = static_cast<const float *>(out);
   b.lse = lse;
   b.dout = static_cast<const float *>(dout);
-  return run_attn_bwd_f32(b, q, k, v, kp, vp, route_idx, dq, dk, dv, static_cast<float *>(workspace), p, 0, s);
+  return run_attn_bwd_f32(b, q, k, v, kp, vp, route_idx, dq, dk, dv, static_cast<float *>(workspace), p, false, s);
 }
 
 // ----------------------------------------------------------------- differential form
@@ -444,7 +448,7 @@ basa_status launch_diff_attn_bwd_f32(const void *q, const void *k, const void *v
   b.lambda = static_cast<const float *>(dp.lambda);
   basa_params pm = p;
   pm.heads = 2 * p.heads;
-  return run_attn_bwd_f32(b, q, k, v, kp, vp, route_idx, dq, dk, dv, pooled, pm, 1, s);
+  return run_attn_bwd_f32(b, q, k, v, kp, vp, route_idx, dq, dk, dv, pooled, pm, true, s);
 }
 
 }  // namespace basa

@@ -15,7 +15,6 @@ struct F32Args {
   Geo g;
   int heads, d, n_text, n_pool, routed_k, win_tok, q_chunks;
   int n_vis_keys, n_pool_keys, n_text_keys;  // keys taken from each group (0 = group not selected)
-  int v_shift;  // v, vp and the routes belong to unit bh >> v_shift (maps that share their values)
   int dense;  // text-query rows: queries are q_text rows, keys are all N + n_text rows of k, v
   float scale;
 };
