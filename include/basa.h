@@ -35,7 +35,9 @@
  * ---------------------------------------
  * Pointers. Every tensor pointer is a DEVICE pointer owned by the caller; the
  *   library never allocates, frees, copies to the host or synchronises. Tensor
- *   pointers must be 16-byte aligned (route_idx / route_score: 4-byte).
+ *   pointers must be 16-byte aligned (route_idx / route_score: 4-byte). What a call
+ *   writes must not overlap anything else that it reads or writes, unless its entry
+ *   point says so.
  * Layouts (row-major, innermost last; N = T*H*W visual tokens in raster order
  *   t, y, x; Np = (T/pt)*(H/ph)*(W/pw) pooled tokens in raster order of the
  *   pooled grid; nWin = (T/wt)*(H/wh)*(W/ww)):

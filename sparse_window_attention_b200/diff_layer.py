@@ -136,6 +136,10 @@ class BasaDiffLayer:
         self._check_inputs(q, k, v, lam, weight, kp, vp, route_idx)
         if out is not None:
             self._check("out", out, self.batch, self.heads, self.N, self.head_dim)
+            at, end = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+            for t in (q, k, v, lam, weight, kp, vp, route_idx):  # contiguous, as checked
+                if t is not None and t.data_ptr() < end and at < t.data_ptr() + t.numel() * t.element_size():
+                    raise ValueError("out: overlaps an input, which other rows still read")
         with streams.on(self.device, stream):
             kp, vp, route_idx = self._keys(q, k, v, shift, kp, vp, route_idx)
             if out is None:
